@@ -6,40 +6,22 @@
 #include <hip/hip_runtime_api.h>
 
 #include <algorithm>
-#include <cstdarg>
 #include <cstdint>
-#include <cstdio>
 #include <vector>
 
 #include "../../include/nvfp4.h"
+#include "abi_common.h"
 #include "launchers.h"
 
 namespace {
 
-thread_local char g_last_error[512] = "";
-
-int fail(int status, const char* fmt, ...) {
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(g_last_error, sizeof g_last_error, fmt, ap);
-  va_end(ap);
-  return status;
-}
-
-int ok() {
-  g_last_error[0] = '\0';
-  return NVFP4_OK;
-}
-
-int hip_status(hipError_t e, const char* what) {
-  if (e == hipSuccess) return ok();
-  return fail(NVFP4_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-
-constexpr int64_t kMaxDim = int64_t(1) << 30;
+using nvfp4::aligned16;
+using nvfp4::aligned4;
+using nvfp4::fail;
+using nvfp4::g_last_error;
+using nvfp4::hip_status;
+using nvfp4::kMaxDim;
+using nvfp4::ok;
 
 int check_shape(int64_t n, int64_t k) {
   if (n < 0 || k < 0) return fail(NVFP4_ERR_SHAPE, "negative size (n=%lld, k=%lld)", (long long)n, (long long)k);
@@ -62,19 +44,6 @@ int check_product(int64_t n, int64_t k) {
                 (long long)k, (long long)nvfp4::kMaxProductK);
   return NVFP4_OK;
 }
-
-#define NVFP4_TRY(expr)              \
-  do {                               \
-    int s_ = (expr);                 \
-    if (s_ != NVFP4_OK) return s_;   \
-  } while (0)
-
-#define NVFP4_GUARD_BEGIN try {
-#define NVFP4_GUARD_END                                                    \
-  }                                                                        \
-  catch (...) {                                                            \
-    return fail(NVFP4_ERR_ARG, "internal error: unexpected C++ exception"); \
-  }
 
 }  // namespace
 
