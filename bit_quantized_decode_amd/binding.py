@@ -1,4 +1,5 @@
-"""Python binding of libnvfp4.so: the functions of include/nvfp4.h, same names.
+"""Python binding of libnvfp4.so: the functions of include/nvfp4.h and
+include/nvfp4_attn.h, same names.
 
 Argument marshalling only: torch tensors supply device memory and the current
 stream; every step of the computation runs in the library's HIP kernels.  If
@@ -31,6 +32,21 @@ EXPORTED = (
     "nvfp4_quantize", "nvfp4_expert_cache_reset", "nvfp4_moe_streamed", "nvfp4_mx_packed_bytes", "nvfp4_mx_pack",
     "nvfp4_mx_unpack", "nvfp4_w4a4_workspace_bytes", "nvfp4_w4a4_gemm", "nvfp4_w4a4_batched_workspace_bytes",
     "nvfp4_w4a4_batched", "nvfp4_gemv_batched_noalloc",
+)
+
+# include/nvfp4_attn.h
+NVFP4_ROPE_HALF = 0
+NVFP4_ROPE_INTERLEAVED = 1
+NVFP4_ROPE_NONE = 0
+NVFP4_ROPE_LINEAR = 1
+NVFP4_ROPE_YARN = 2
+NVFP4_KV_BF16 = 0
+NVFP4_KV_E4M3 = 1
+NVFP4_KV_NVFP4 = 2
+
+EXPORTED_ATTN = (
+    "nvfp4_rope_freqs", "nvfp4_rope", "nvfp4_kv_cache_bytes", "nvfp4_kv_append", "nvfp4_kv_read",
+    "nvfp4_attn_decode_workspace_bytes", "nvfp4_attn_decode",
 )
 
 
@@ -81,6 +97,58 @@ class ExpertCache(ctypes.Structure):
     ]
 
 
+class RopeConfig(ctypes.Structure):
+    """Mirror of struct nvfp4_rope_config."""
+    _fields_ = [
+        ("rot_dim", ctypes.c_int64), ("base", ctypes.c_double), ("scaling", ctypes.c_int), ("factor", ctypes.c_double),
+        ("original_max", ctypes.c_double), ("beta_fast", ctypes.c_double), ("beta_slow", ctypes.c_double),
+    ]
+
+
+class RopeArgs(ctypes.Structure):
+    """Mirror of struct nvfp4_rope_args."""
+    _fields_ = [
+        ("tokens", ctypes.c_int64), ("heads", ctypes.c_int64), ("head_dim", ctypes.c_int64), ("rot_dim", ctypes.c_int64),
+        ("layout", ctypes.c_int), ("inverse", ctypes.c_int), ("magnitude", ctypes.c_float),
+        ("positions", ctypes.c_void_p), ("freqs", ctypes.c_void_p),
+        ("x", ctypes.c_void_p), ("x_dtype", ctypes.c_int), ("ldx", ctypes.c_int64),
+        ("y", ctypes.c_void_p), ("y_dtype", ctypes.c_int), ("ldy", ctypes.c_int64),
+    ]
+
+
+class KvCacheDesc(ctypes.Structure):
+    """Mirror of struct nvfp4_kv_cache."""
+    _fields_ = [
+        ("pool", ctypes.c_void_p), ("pages", ctypes.c_int64), ("page_size", ctypes.c_int64),
+        ("kv_heads", ctypes.c_int64), ("head_dim", ctypes.c_int64), ("format", ctypes.c_int),
+        ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float),
+    ]
+
+
+class KvAppendArgs(ctypes.Structure):
+    """Mirror of struct nvfp4_kv_append_args."""
+    _fields_ = [
+        ("cache", ctypes.POINTER(KvCacheDesc)), ("tokens", ctypes.c_int64), ("slots", ctypes.c_void_p),
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("dtype", ctypes.c_int),
+        ("ldk", ctypes.c_int64), ("ldv", ctypes.c_int64),
+        ("freqs", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("rot_dim", ctypes.c_int64),
+        ("layout", ctypes.c_int), ("magnitude", ctypes.c_float),
+        ("q_heads", ctypes.c_int64), ("q", ctypes.c_void_p), ("ldq", ctypes.c_int64),
+        ("q_out", ctypes.c_void_p), ("ldqo", ctypes.c_int64),
+    ]
+
+
+class AttnArgs(ctypes.Structure):
+    """Mirror of struct nvfp4_attn_args."""
+    _fields_ = [
+        ("cache", ctypes.POINTER(KvCacheDesc)), ("batch", ctypes.c_int64), ("q_heads", ctypes.c_int64),
+        ("q", ctypes.c_void_p), ("ldq", ctypes.c_int64), ("page_table", ctypes.c_void_p),
+        ("table_width", ctypes.c_int64), ("seq_lens", ctypes.c_void_p), ("scale", ctypes.c_float),
+        ("window", ctypes.c_int64), ("out", ctypes.c_void_p), ("ldo", ctypes.c_int64), ("lse", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
 _lib = None
 
 
@@ -122,6 +190,13 @@ def lib():
         "nvfp4_w4a4_gemm": (I, [P, i64, i64, ctypes.c_float, P, i64, i64, P, i64, I, P, sz, P]),
         "nvfp4_w4a4_batched_workspace_bytes": (I, [ctypes.POINTER(Problem), I, i64, ctypes.POINTER(sz)]),
         "nvfp4_w4a4_batched": (I, [ctypes.POINTER(Problem), I, i64, I, P, sz, P]),
+        "nvfp4_rope_freqs": (I, [ctypes.POINTER(RopeConfig), P, ctypes.POINTER(ctypes.c_float)]),
+        "nvfp4_rope": (I, [ctypes.POINTER(RopeArgs), P]),
+        "nvfp4_kv_cache_bytes": (I, [ctypes.POINTER(KvCacheDesc), ctypes.POINTER(sz)]),
+        "nvfp4_kv_append": (I, [ctypes.POINTER(KvAppendArgs), P]),
+        "nvfp4_kv_read": (I, [ctypes.POINTER(KvCacheDesc), P, i64, P, i64, P, i64, I, P]),
+        "nvfp4_attn_decode_workspace_bytes": (I, [ctypes.POINTER(AttnArgs), ctypes.POINTER(sz)]),
+        "nvfp4_attn_decode": (I, [ctypes.POINTER(AttnArgs), P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -566,3 +641,274 @@ def moe_grouped_prepared(*args, **kw):
         return keep
 
     return call, o
+
+
+# ---- the attention side (include/nvfp4_attn.h) ---------------------------------
+#
+# Every call here runs on the device of its tensors, whichever is current, on
+# `stream` or that device's current stream.  Each *_prepared() checks and
+# marshals its arguments once and returns a zero-argument callable that makes
+# the library call and returns the outputs, the same buffers each time.
+
+def _device_of(**tensors):
+    """The one GPU that all given tensors are on."""
+    dev = None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be on the GPU, not on {t.device}")
+        if dev is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, other arguments on {dev}")
+        dev = t.device
+    return dev
+
+
+def _rows(t, name, dtypes, heads=None, head_dim=None, tokens=None):
+    """The leading dimension of t [tokens][heads][head_dim] after checking its shape and strides."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens][heads][head_dim], not {tuple(t.shape)}")
+    for want, got, what in ((tokens, t.shape[0], "tokens"), (heads, t.shape[1], "heads"), (head_dim, t.shape[2], "head_dim")):
+        if want is not None and want != got:
+            raise ValueError(f"{name} has {got} {what}, expected {want}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be one of {dtypes}, not {t.dtype}")
+    if t.numel() and ((t.shape[2] > 1 and t.stride(2) != 1) or (t.shape[1] > 1 and t.stride(1) != t.shape[2])):
+        raise ValueError(f"{name}: the heads of a row must be contiguous (strides {t.stride()})")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def _vector(t, name, dtype, shape):
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {tuple(shape)}, not {tuple(t.shape)} with strides {t.stride()}")
+    return t.data_ptr()
+
+
+def _dtype_code(t):
+    return NVFP4_BF16 if t.dtype == torch.bfloat16 else NVFP4_F32
+
+
+_ACTIVATIONS = (torch.float32, torch.bfloat16)
+
+
+def _new(make, device, stream):
+    """make() with device current, and stream too if one is given: memory made there may be reused on that stream only."""
+    with torch.cuda.device(device):
+        if stream is None:
+            return make()
+        with torch.cuda.stream(stream):
+            return make()
+
+
+def _caller(fn, args, device, stream, outputs, keep):
+    """The callable of a prepared call: fn(*args, stream) on the tensors' device."""
+    index = device.index
+
+    def call():
+        if torch.cuda.current_device() == index:
+            check(fn(*args, _stream(stream)))
+        else:
+            with torch.cuda.device(index):
+                check(fn(*args, _stream(stream)))
+        return outputs
+
+    call.keep = keep   # the tensors and structures must outlive the callable
+    return call
+
+
+class RopeTable:
+    """A device table of rotary frequencies (nvfp4_rope_freqs), with the layout and magnitude that go with it."""
+
+    def __init__(self, freqs, rot_dim, layout, magnitude):
+        self.freqs, self.rot_dim, self.layout, self.magnitude = freqs, rot_dim, layout, magnitude
+
+
+def rope_freqs(rot_dim, base=10000.0, scaling=None):
+    """(freqs, magnitude): the host table as int64 bit patterns [rot_dim / 2].  scaling: None,
+    ("linear", factor) or ("yarn", factor, original_max[, beta_fast, beta_slow])."""
+    c = RopeConfig(rot_dim=rot_dim, base=base, scaling=NVFP4_ROPE_NONE, factor=1.0, beta_fast=32.0, beta_slow=1.0)
+    if scaling is not None:
+        kind, *rest = scaling
+        fields = {"linear": ("factor",), "yarn": ("factor", "original_max", "beta_fast", "beta_slow")}.get(kind)
+        if fields is None or not rest or len(rest) > len(fields) or (kind == "yarn" and len(rest) not in (2, 4)):
+            raise ValueError(f"unknown rotary scaling {scaling!r}")
+        c.scaling = NVFP4_ROPE_LINEAR if kind == "linear" else NVFP4_ROPE_YARN
+        for field, value in zip(fields, rest):
+            setattr(c, field, value)
+    freqs = torch.zeros(max(rot_dim, 0) // 2, dtype=torch.int64)
+    magnitude = ctypes.c_float()
+    check(lib().nvfp4_rope_freqs(ctypes.byref(c), _ptr(freqs), ctypes.byref(magnitude)))
+    return freqs, magnitude.value
+
+
+def rope_table(rot_dim, base=10000.0, layout="half", scaling=None, device="cuda"):
+    """A RopeTable on `device`; layout: "half" or "interleaved", the rest as in rope_freqs."""
+    code = {"half": NVFP4_ROPE_HALF, "interleaved": NVFP4_ROPE_INTERLEAVED}.get(layout)
+    if code is None:
+        raise ValueError(f"unknown rotary layout {layout!r}")
+    freqs, magnitude = rope_freqs(rot_dim, base, scaling)
+    return RopeTable(freqs.to(device), rot_dim, code, magnitude)
+
+
+def rope_prepared(x, positions, table, out=None, dtype=None, inverse=False, stream=None):
+    """rope() with its arguments marshalled once: returns a zero-argument callable that returns `out`."""
+    ldx = _rows(x, "x", _ACTIVATIONS)
+    tokens, heads, head_dim = x.shape
+    dev = _device_of(x=x, positions=positions, freqs=table.freqs, out=out)
+    if out is None:
+        out = _new(lambda: torch.empty((tokens, heads, head_dim), dtype=dtype or x.dtype, device=dev), dev, stream)
+    ldy = _rows(out, "out", _ACTIVATIONS, heads, head_dim, tokens)
+    a = RopeArgs(tokens=tokens, heads=heads, head_dim=head_dim, rot_dim=table.rot_dim, layout=table.layout,
+                 inverse=int(inverse), magnitude=table.magnitude,
+                 positions=_vector(positions, "positions", torch.int32, (tokens,)), freqs=table.freqs.data_ptr(),
+                 x=x.data_ptr(), x_dtype=_dtype_code(x), ldx=ldx, y=out.data_ptr(), y_dtype=_dtype_code(out), ldy=ldy)
+    return _caller(lib().nvfp4_rope, (ctypes.byref(a),), dev, stream, out, (a, x, positions, table, out))
+
+
+def rope(x, positions, table, out=None, dtype=None, inverse=False, stream=None):
+    """Rotary positions: x [tokens][heads][head_dim] (fp32 or bf16; the rows may be strided), positions int32
+    [tokens].  Returns out (x itself turns in place; by default a new tensor of `dtype` or x's).
+    inverse=True turns back: the gradient of rope() is rope(inverse=True) of the output's gradient."""
+    return rope_prepared(x, positions, table, out, dtype, inverse, stream)()
+
+
+class KvCache:
+    """A paged key-value cache (struct nvfp4_kv_cache) with its pool.  fmt: NVFP4_KV_BF16, NVFP4_KV_E4M3 or
+    NVFP4_KV_NVFP4 (whose tensor scales are k_scale and v_scale).  A token's slot is page * page_size + offset."""
+
+    def __init__(self, pages, page_size, kv_heads, head_dim, fmt, k_scale=1.0, v_scale=1.0, device="cuda", pool=None):
+        self.desc = KvCacheDesc(pool=None, pages=pages, page_size=page_size, kv_heads=kv_heads, head_dim=head_dim,
+                                format=fmt, k_scale=k_scale, v_scale=v_scale)
+        need = ctypes.c_size_t()
+        check(lib().nvfp4_kv_cache_bytes(ctypes.byref(self.desc), ctypes.byref(need)))
+        if pool is None:
+            pool = torch.empty(need.value, dtype=torch.uint8, device=device)
+        if pool.dtype != torch.uint8 or not pool.is_contiguous() or pool.numel() < need.value:
+            raise ValueError(f"pool must be contiguous uint8 of at least {need.value} bytes")
+        self.pool = pool
+        self.desc.pool = pool.data_ptr()
+        self.pages, self.page_size, self.kv_heads, self.head_dim, self.fmt = pages, page_size, kv_heads, head_dim, fmt
+
+
+def kv_append_prepared(cache, k, v, slots, positions=None, table=None, q=None, q_out=None, stream=None):
+    """kv_append() with its arguments marshalled once: returns a zero-argument callable that returns q_out."""
+    tokens = k.shape[0]
+    ldk = _rows(k, "k", _ACTIVATIONS, cache.kv_heads, cache.head_dim)
+    ldv = _rows(v, "v", (k.dtype,), cache.kv_heads, cache.head_dim, tokens)
+    dev = _device_of(pool=cache.pool, k=k, v=v, slots=slots, positions=positions if table is not None else None,
+                     freqs=None if table is None else table.freqs, q=q, q_out=q_out)
+    a = KvAppendArgs(cache=ctypes.pointer(cache.desc), tokens=tokens, slots=_vector(slots, "slots", torch.int64, (tokens,)),
+                     k=k.data_ptr(), v=v.data_ptr(), dtype=_dtype_code(k), ldk=ldk, ldv=ldv)
+    if table is not None:
+        if positions is None:
+            raise ValueError("a rotary table needs positions")
+        # A table that turns nothing (rot_dim 0) has no memory of its own: any aligned address stands for it.
+        a.freqs = table.freqs.data_ptr() or cache.pool.data_ptr()
+        a.positions = _vector(positions, "positions", torch.int32, (tokens,))
+        a.rot_dim, a.layout, a.magnitude = table.rot_dim, table.layout, table.magnitude
+    if q is not None:
+        a.ldq = _rows(q, "q", (k.dtype,), None, cache.head_dim, tokens)
+        if q_out is None:
+            q_out = _new(lambda: torch.empty(q.shape, dtype=torch.bfloat16, device=dev), dev, stream)
+        a.ldqo = _rows(q_out, "q_out", (torch.bfloat16,), q.shape[1], cache.head_dim, tokens)
+        a.q_heads, a.q, a.q_out = q.shape[1], q.data_ptr(), q_out.data_ptr()
+    return _caller(lib().nvfp4_kv_append, (ctypes.byref(a),), dev, stream, q_out,
+                   (a, cache, k, v, slots, positions, table, q, q_out))
+
+
+def kv_append(cache, k, v, slots, positions=None, table=None, q=None, q_out=None, stream=None):
+    """Write k, v [tokens][kv_heads][head_dim] (fp32 or bf16) into the cache at slots (int64; outside the pool:
+    skipped).  With table (and positions, int32) k is turned first, and q [tokens][q_heads][head_dim] into q_out
+    (bf16), which is returned."""
+    return kv_append_prepared(cache, k, v, slots, positions, table, q, q_out, stream)()
+
+
+def kv_read_prepared(cache, slots, k_out=None, v_out=None, dtype=torch.bfloat16, stream=None):
+    """kv_read() with its arguments marshalled once: returns a zero-argument callable that returns (k_out, v_out)."""
+    tokens = slots.shape[0]
+    dev = _device_of(pool=cache.pool, slots=slots, k_out=k_out, v_out=v_out)
+    shape = (tokens, cache.kv_heads, cache.head_dim)
+    if k_out is None and v_out is None:
+        k_out, v_out = (_new(lambda: torch.empty(shape, dtype=dtype, device=dev), dev, stream) for _ in range(2))
+    ld, codes = [0, 0], set()
+    for i, t in enumerate((k_out, v_out)):
+        if t is not None:
+            ld[i] = _rows(t, ("k_out", "v_out")[i], _ACTIVATIONS, cache.kv_heads, cache.head_dim, tokens)
+            codes.add(_dtype_code(t))
+    if len(codes) != 1:
+        raise TypeError("k_out and v_out must have the same dtype")
+    args = (ctypes.byref(cache.desc), _vector(slots, "slots", torch.int64, (tokens,)), tokens, _ptr(k_out), ld[0],
+            _ptr(v_out), ld[1], codes.pop())
+    return _caller(lib().nvfp4_kv_read, args, dev, stream, (k_out, v_out), (cache, slots, k_out, v_out))
+
+
+def kv_read(cache, slots, k_out=None, v_out=None, dtype=torch.bfloat16, stream=None):
+    """The values the cache holds at slots (int64): (k, v), each [tokens][kv_heads][head_dim].  Given one of
+    k_out and v_out, only that one is read.  Rows of slots outside the pool are left as they were."""
+    return kv_read_prepared(cache, slots, k_out, v_out, dtype, stream)()
+
+
+def _attn_workspace(nbytes, device, stream):
+    """The workspace of attention calls without one of their own.  Calls on one stream run one after the other and
+    share; calls on others have another.  Under capture the graph gets one of its own, zeroed by a
+    node of the graph: replays may overlap with anything."""
+    def make():
+        return torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
+
+    with torch.cuda.device(device):
+        if torch.cuda.is_current_stream_capturing():
+            return _new(make, device, stream)
+        s = torch.cuda.current_stream() if stream is None else stream
+        key = (str(device), "attn", s.cuda_stream)
+        ws = _workspaces.get(key)
+        if ws is None or ws.numel() < nbytes:
+            ws = _workspaces[key] = _new(make, device, stream)
+        return ws
+
+
+def _attn(q, cache, page_table, seq_lens, scale, window, out, lse, ws, stream, prepared):
+    ldq = _rows(q, "q", (torch.bfloat16,), None, cache.head_dim)
+    batch, q_heads, head_dim = q.shape
+    dev = _device_of(pool=cache.pool, q=q, page_table=page_table, seq_lens=seq_lens, out=out, ws=ws,
+                     lse=lse if isinstance(lse, torch.Tensor) else None)
+    if page_table.dim() != 2:
+        raise ValueError(f"page_table must be [batch][pages], not {tuple(page_table.shape)}")
+    if out is None:
+        out = _new(lambda: torch.empty((batch, q_heads, head_dim), dtype=torch.bfloat16, device=dev), dev, stream)
+    if lse is True:
+        lse = _new(lambda: torch.empty((batch, q_heads), dtype=torch.float32, device=dev), dev, stream)
+    a = AttnArgs(cache=ctypes.pointer(cache.desc), batch=batch, q_heads=q_heads, q=q.data_ptr(), ldq=ldq,
+                 page_table=_vector(page_table, "page_table", torch.int32, (batch, page_table.shape[1])),
+                 table_width=page_table.shape[1], seq_lens=_vector(seq_lens, "seq_lens", torch.int32, (batch,)),
+                 scale=head_dim ** -0.5 if scale is None else scale, window=window, out=out.data_ptr(),
+                 ldo=_rows(out, "out", (torch.bfloat16,), q_heads, head_dim, batch))
+    if isinstance(lse, torch.Tensor):
+        a.lse = _vector(lse, "lse", torch.float32, (batch, q_heads))
+    need = ctypes.c_size_t()
+    check(lib().nvfp4_attn_decode_workspace_bytes(ctypes.byref(a), ctypes.byref(need)))
+    if ws is None and need.value:
+        if prepared:
+            ws = _new(lambda: torch.zeros(need.value, dtype=torch.uint8, device=dev), dev, stream)
+        else:
+            ws = _attn_workspace(need.value, dev, stream)
+    if ws is not None:
+        a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
+    outputs = (out, lse) if isinstance(lse, torch.Tensor) else out
+    return _caller(lib().nvfp4_attn_decode, (ctypes.byref(a),), dev, stream, outputs,
+                   (a, cache, q, page_table, seq_lens, out, lse, ws))
+
+
+def attn_decode_prepared(q, cache, page_table, seq_lens, scale=None, window=0, out=None, lse=None, ws=None, stream=None):
+    """attn_decode() with its arguments marshalled once and a workspace of its own: returns a zero-argument callable
+    that returns what attn_decode() does."""
+    return _attn(q, cache, page_table, seq_lens, scale, window, out, lse, ws, stream, True)
+
+
+def attn_decode(q, cache, page_table, seq_lens, scale=None, window=0, out=None, lse=None, ws=None, stream=None):
+    """Attention of one new token per sequence over the cache: q bf16 [batch][q_heads][head_dim], page_table int32
+    [batch][pages], seq_lens int32 [batch] (with the new token), scale 1 / sqrt(head_dim) by default.  Returns out
+    (bf16 like q), or (out, lse) if lse is True or a float32 [batch][q_heads] tensor.  ws: a workspace, zeroed
+    before its first use, that no other running call has."""
+    return _attn(q, cache, page_table, seq_lens, scale, window, out, lse, ws, stream, False)()

@@ -1,0 +1,602 @@
+// Attention of one new token per sequence over the paged cache (nvfp4_attn_decode).
+//
+//   s_j = scale q.k_j,   o = sum_j exp(s_j - m) v_j / sum_j exp(s_j - m)
+//
+// in one pass over the cache with a running reference r in place of the maximum
+// (softmax does not depend on it): p_j = 2^(s_j log2 e - r), l = sum p_j.
+//
+// Tiles.  The query heads of one kv head (up to 16, more in further row tiles) are
+// the columns of 16x16x32 matrix instructions.  A wavefront takes 32 tokens at a
+// time: scores S = K Q^T come out with lane 16 h + q holding tokens 4h + i of
+// query q, which is exactly the k split of the second product O^T = V^T P^T, so
+// probabilities go from one to the other inside their lane.  Because a lane belongs to
+// one query, the reference and the sum are lane values; the reference only
+// moves when a score passes it by 2^kSlack, and only then do lanes talk.
+//
+// Operands.  bf16 and E4M3 caches multiply as bf16 (every E4M3 value times its
+// power of two is a bf16 number), NVFP4 as f16 (E2M1 times E4M3 is an f16
+// number); the queries, bf16, are shifted into f16's range by a power of two
+// per row.  Probabilities enter as the sum of two 16-bit numbers, so they
+// carry 16 bits (bf16) or 22 (f16); everything else is fp32.
+//
+// Work split.  One granule is 128 tokens of one (sequence, kv head, row tile): 32 a
+// wavefront.  The granules of all sequences form one line, cut evenly over the
+// workgroups whatever the lengths are; a unit (sequence, head, row tile) cut
+// between workgroups leaves partial sums, and the last to arrive joins them in
+// workgroup order.
+#include "attn_launchers.h"
+#include "device_common.h"
+
+namespace nvfp4 {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWaves = 4;
+constexpr int kTile = 32;                  // tokens of a wavefront's step
+constexpr int kGranule = kTile * kWaves;
+constexpr int kRows = 16;                  // query heads of a row tile
+constexpr int kMaxWorkgroups = 2048;       // counters in the workspace
+static_assert(kMaxWorkgroups * 4 <= (int)kAttnCounterBytes, "one counter a workgroup");
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kNegInf = -__builtin_inff();
+
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+struct AttnParams {
+  KvCache cache;
+  const uint16_t* q;
+  const int32_t* table;
+  const int32_t* lens;
+  uint16_t* out;
+  float* lse;
+  unsigned* counters;
+  float* part;         // partial sums, see part_of()
+  int64_t ldq, ldo, table_width;
+  int32_t batch, q_heads, group, row_tiles, window, part_rows;
+  float scale;
+};
+
+// The tokens that a row attends to.
+struct Span {
+  int begin, end;      // [begin, end)
+  int base;            // begin rounded down to a group
+  int granules;        // at least one, so that an empty row is written too
+};
+__device__ __forceinline__ Span span_of(const AttnParams& a, int len) {
+  Span s;
+  const int64_t most = a.table_width * a.cache.page_size;
+  s.end = len < 0 ? 0 : (int64_t)len > most ? (int)most : len;
+  s.begin = a.window > 0 && s.end > a.window ? s.end - a.window : 0;
+  s.base = s.begin & ~(kKvGroup - 1);
+  const int n = (s.end - s.base + kGranule - 1) / kGranule;
+  s.granules = n > 1 ? n : 1;
+  return s;
+}
+
+// The partial sums that workgroup w leaves of a unit that starts before its share
+// (side 0) or in it (side 1): rows of reference, sum and the padded head's sums.
+template <int DP>
+__device__ __forceinline__ float* part_of(const AttnParams& a, int w, int side) {
+  return a.part + ((int64_t)2 * w + side) * a.part_rows * (DP + 4);
+}
+
+template <int FMT, int DB>
+struct Tile {
+  using L = KvLayout<FMT, DB>;
+  static constexpr int kWords = L::kLaneBytes / 4;
+  static constexpr int kVScales = FMT == kKvNvfp4 && DB == 3 ? 3 : 1;
+  uint32_t k[2][kWords], v[2][kWords];
+  uint32_t ks[2], vs[2][kVScales];
+};
+
+template <int FMT, int DB>
+__device__ __forceinline__ void load_side(const uint8_t* p, int lane, uint32_t* w) {
+  using L = KvLayout<FMT, DB>;
+#pragma unroll
+  for (int i = 0; i < L::kPlanes16; ++i) {
+    const u32x4 x = load16(p + i * 1024 + lane * 16);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[4 * i + j] = x[j];
+  }
+  if constexpr (L::kPlane8) {
+    const uint2 x = *reinterpret_cast<const uint2*>(p + L::kPlanes16 * 1024 + lane * 8);
+    w[4 * L::kPlanes16] = x.x;
+    w[4 * L::kPlanes16 + 1] = x.y;
+  }
+}
+
+template <int FMT, int DB>
+__device__ __forceinline__ void load_tile(const KvCache& c, const int (&group)[2], int lane, Tile<FMT, DB>& t) {
+  using L = KvLayout<FMT, DB>;
+#pragma unroll
+  for (int a = 0; a < 2; ++a) {
+    const uint8_t* codes = c.codes + (int64_t)group[a] * L::kCodeBytes;
+    load_side<FMT, DB>(codes, lane, t.k[a]);
+    load_side<FMT, DB>(codes + L::kSideBytes, lane, t.v[a]);
+    if constexpr (FMT == kKvE4m3) {
+      const uint8_t* s = c.scales + (int64_t)group[a] * L::kScaleBytes;
+      t.ks[a] = s[lane & 15];
+      t.vs[a][0] = *reinterpret_cast<const uint32_t*>(s + 16 + 4 * (lane >> 4));
+    } else if constexpr (FMT == kKvNvfp4) {
+      const uint8_t* s = c.scales + (int64_t)group[a] * L::kScaleBytes;
+      if constexpr (L::kKScaleLane == 1) t.ks[a] = s[lane];
+      else if constexpr (L::kKScaleLane == 2) t.ks[a] = *reinterpret_cast<const uint16_t*>(s + 2 * lane);
+      else t.ks[a] = *reinterpret_cast<const uint32_t*>(s + 4 * lane);
+      const uint32_t* vs = reinterpret_cast<const uint32_t*>(s + L::kKScaleBytes) + (lane >> 4) * (4 * DB);
+#pragma unroll
+      for (int u = 0; u < Tile<FMT, DB>::kVScales; ++u) t.vs[a][u] = vs[(L::kW * (lane & 15) + 4 * u) / 16];
+    }
+  }
+}
+
+// E4M3 byte `i` of w as an f16 pair of that value.
+__device__ __forceinline__ f16x2 scale_pair(uint32_t w, int i) {
+  const f16x2 p = __builtin_bit_cast(f16x2, i >= 2 ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, true)
+                                                   : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, false));
+  return (i & 1) ? f16x2{p[1], p[1]} : f16x2{p[0], p[0]};
+}
+
+// Two E2M1 codes (byte `sel`) times a scale pair: exact in f16.
+template <int SEL>
+__device__ __forceinline__ uint32_t e2m1_scaled(uint32_t w, f16x2 s) {
+  const f16x2 p = __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, SEL)) * s;
+  return __builtin_bit_cast(uint32_t, p);
+}
+// Two E4M3 codes (half HI of w) times a power of two: exact in bf16.
+template <bool HI>
+__device__ __forceinline__ uint32_t e4m3_scaled(uint32_t w, float s) {
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, HI));
+}
+__device__ __forceinline__ float byte_exp2(uint32_t w, int i) { return __uint_as_float(((w >> (8 * i)) & 0xffu) << 23); }
+
+template <int FMT>
+__device__ __forceinline__ f32x4 mma(const uint32_t* a, const uint32_t* b, f32x4 acc) {
+  const u32x4 x{a[0], a[1], a[2], a[3]}, y{b[0], b[1], b[2], b[3]};
+  if constexpr (FMT == kKvNvfp4)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, x), __builtin_bit_cast(f16x8, y), acc, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, y), acc, 0, 0, 0);
+}
+
+// K operand of matrix step s: the lane's values 8s .. 8s + 7 as 16-bit pairs.
+template <int FMT, int DB>
+__device__ __forceinline__ void k_operand(const Tile<FMT, DB>& t, int a, int s, uint32_t (&o)[4]) {
+  if constexpr (FMT == kKvBf16) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = t.k[a][4 * s + i];
+  } else if constexpr (FMT == kKvE4m3) {
+    const float x = byte_exp2(t.ks[a], 0);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      o[2 * i] = e4m3_scaled<false>(t.k[a][2 * s + i], x);
+      o[2 * i + 1] = e4m3_scaled<true>(t.k[a][2 * s + i], x);
+    }
+  } else {
+    const f16x2 x = scale_pair(t.ks[a], s / 2);
+    o[0] = e2m1_scaled<0>(t.k[a][s], x);
+    o[1] = e2m1_scaled<1>(t.k[a][s], x);
+    o[2] = e2m1_scaled<2>(t.k[a][s], x);
+    o[3] = e2m1_scaled<3>(t.k[a][s], x);
+  }
+}
+
+// The lane's V values of token i as 16-bit pairs: o[j] holds d = W r + 2j, + 1.
+template <int FMT, int DB>
+__device__ __forceinline__ void v_token(const Tile<FMT, DB>& t, int a, int i, uint32_t (&o)[2 * DB]) {
+  constexpr int kPairs = 2 * DB;
+  if constexpr (FMT == kKvBf16) {
+#pragma unroll
+    for (int j = 0; j < kPairs; ++j) o[j] = t.v[a][kPairs * i + j];
+  } else if constexpr (FMT == kKvE4m3) {
+    const float x = byte_exp2(t.vs[a][0], i);
+#pragma unroll
+    for (int j = 0; j < kPairs; j += 2) {
+      o[j] = e4m3_scaled<false>(t.v[a][(kPairs * i + j) / 2], x);
+      o[j + 1] = e4m3_scaled<true>(t.v[a][(kPairs * i + j) / 2], x);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < kPairs; ++j) {
+      const f16x2 x = scale_pair(t.vs[a][DB == 3 ? j / 2 : 0], i);
+      const int byte = kPairs * i + j;
+      const uint32_t w = t.v[a][byte / 4];
+      switch (byte % 4) {
+        case 0: o[j] = e2m1_scaled<0>(w, x); break;
+        case 1: o[j] = e2m1_scaled<1>(w, x); break;
+        case 2: o[j] = e2m1_scaled<2>(w, x); break;
+        default: o[j] = e2m1_scaled<3>(w, x); break;
+      }
+    }
+  }
+}
+
+// Clears what masked tokens hold, so that garbage (NaN codes, infinities) times
+// a zero probability stays zero.  ok: bit 4a + i, tokens 4h + i of group a.
+template <int FMT, int DB>
+__device__ __forceinline__ void clear_masked(Tile<FMT, DB>& t, uint32_t ok) {
+  constexpr int kTokenWords = Tile<FMT, DB>::kWords / 4;
+#pragma unroll
+  for (int a = 0; a < 2; ++a)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool keep = (ok >> (4 * a + i)) & 1u;
+      if constexpr (FMT == kKvNvfp4) {  // a zero scale: every code is finite
+#pragma unroll
+        for (int u = 0; u < Tile<FMT, DB>::kVScales; ++u) t.vs[a][u] &= keep ? ~0u : ~(0xffu << (8 * i));
+      } else {
+#pragma unroll
+        for (int j = 0; j < kTokenWords; ++j) t.v[a][kTokenWords * i + j] = keep ? t.v[a][kTokenWords * i + j] : 0u;
+        if constexpr (FMT == kKvE4m3)
+          t.vs[a][0] = keep ? t.vs[a][0] : (t.vs[a][0] & ~(0xffu << (8 * i))) | (127u << (8 * i));
+      }
+    }
+}
+
+__device__ __forceinline__ float lane_xor(float v, int off) { return __shfl_xor(v, off); }
+
+// f16 probabilities are held 2^kOffset above the reference, so that small ones
+// keep bits down to 2^-24 * 2^-kOffset of the largest; with the slack they
+// stay below 2^15.  bf16 has fp32's range and needs no offset.
+template <int FMT>
+struct Softmax {
+  static constexpr float kOffset = FMT == kKvNvfp4 ? 7.0f : 0.0f;
+  static constexpr float kSlack = 8.0f;
+};
+
+template <int FMT, int DB>
+__global__ __launch_bounds__(kThreads) void attn_kernel(const AttnParams a) {
+  using L = KvLayout<FMT, DB>;
+  constexpr int kDp = 64 * DB, kE = L::kE, kW = L::kW, kSteps = kE / 8;
+  constexpr int kOStride = kDp + 4;
+  __shared__ float s_ml[kWaves][kRows][2];
+  __shared__ __attribute__((aligned(16))) float s_o[kWaves][kRows][kOStride];
+  __shared__ int64_t s_scan[kThreads];
+  __shared__ int64_t s_start[3];  // batch row, granules before it, all granules
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int qn = lane & 15, h = lane >> 4;
+  const int units_per_row = a.cache.heads * a.row_tiles;
+
+  // Where this workgroup's share of all granules starts: a scan over the rows'
+  // granule counts, each thread a run of rows.
+  const int per = (a.batch + kThreads - 1) / kThreads;
+  const int b0 = min(tid * per, a.batch), b1 = min(b0 + per, a.batch);
+  int64_t mine = 0;
+  for (int b = b0; b < b1; ++b) mine += (int64_t)span_of(a, a.lens[b]).granules * units_per_row;
+  s_scan[tid] = mine;
+  __syncthreads();
+  for (int off = 1; off < kThreads; off <<= 1) {
+    const int64_t x = tid >= off ? s_scan[tid - off] : 0;
+    __syncthreads();
+    s_scan[tid] += x;
+    __syncthreads();
+  }
+  const int64_t total = s_scan[kThreads - 1];
+  const int64_t nwg = min((int64_t)gridDim.x, total);
+  const int64_t w = blockIdx.x;
+  if (w >= nwg) return;
+  const int64_t g0 = total * w / nwg, g1 = total * (w + 1) / nwg;
+  const int64_t upto = s_scan[tid];
+  if (upto - mine <= g0 && g0 < upto) {
+    int64_t before = upto - mine;
+    int b = b0;
+    for (; b < b1; ++b) {
+      const int64_t n = (int64_t)span_of(a, a.lens[b]).granules * units_per_row;
+      if (g0 < before + n) break;
+      before += n;
+    }
+    s_start[0] = b;
+    s_start[1] = before;
+  }
+  __syncthreads();
+  int b = (int)s_start[0];
+  int64_t row_start = s_start[1];
+
+  for (int64_t g = g0; g < g1;) {
+    const Span sp = span_of(a, a.lens[b]);
+    const int64_t row_end = row_start + (int64_t)sp.granules * units_per_row;
+    if (g >= row_end) {
+      row_start = row_end;
+      ++b;
+      continue;
+    }
+    const int unit = (int)((g - row_start) / sp.granules);
+    const int64_t u0 = row_start + (int64_t)unit * sp.granules, u1 = u0 + sp.granules;
+    const int64_t stop = min(u1, g1);
+    const int head = unit / a.row_tiles, rt = unit - head * a.row_tiles;
+    const int rows = min(a.group - rt * kRows, kRows);
+    const int first = (int)(g - u0), count = (int)(stop - g);
+
+    // Queries: lane (q, h) holds values E h .. E h + E - 1 of row q.
+    uint32_t qv[kE / 2];
+    const int d_here = a.cache.head_dim - kE * h;  // values of this lane inside the head
+    const uint16_t* qp = a.q + (int64_t)b * a.ldq + (int64_t)(head * a.group + rt * kRows + qn) * a.cache.head_dim + kE * h;
+#pragma unroll
+    for (int i = 0; i < kE / 8; ++i) {
+      u32x4 x{0u, 0u, 0u, 0u};
+      if (qn < rows && 8 * i < d_here) x = load16(qp + 8 * i);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) qv[4 * i + j] = x[j];
+    }
+    float score_scale = a.scale * kLog2e * a.cache.k_scale;
+    if constexpr (FMT == kKvNvfp4) {
+      // bf16 -> f16: a power of two per row puts its largest magnitude at
+      // 2^14 .. 2^15; values down to 2^-28 of it stay exact.
+      uint32_t big = 0;
+#pragma unroll
+      for (int i = 0; i < kE / 2; ++i) big = max(big, max((qv[i] << 16) & 0x7fffffffu, qv[i] & 0x7fff0000u));
+      big = max(big, (uint32_t)__shfl_xor((int)big, 16));
+      big = max(big, (uint32_t)__shfl_xor((int)big, 32));
+      int e = (int)(big >> 23) - 127 - 14;
+      e = e < -100 ? -100 : e > 112 ? 112 : e;
+      const float down = __uint_as_float((uint32_t)(127 - e) << 23), up = __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+      for (int i = 0; i < kE / 2; ++i) {
+        const f16x2 p{(_Float16)(bf16_lo(qv[i]) * down), (_Float16)(bf16_hi(qv[i]) * down)};
+        qv[i] = __builtin_bit_cast(uint32_t, p);
+      }
+      score_scale *= up;
+    }
+
+    f32x4 o[kW];
+#pragma unroll
+    for (int i = 0; i < kW; ++i) o[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    float ref = kNegInf, shift = -1e30f, sum = 0.0f;
+
+    const int tiles = count;
+    int pages = -1;
+    for (int it = 0; it < tiles; ++it) {
+      // Lane j looks up the group of step it + j / 2, half j & 1, for 32 steps ahead.
+      if ((it & 31) == 0) {
+        const int tok = sp.base + ((first + it + (lane >> 1)) * kWaves + wave) * kTile + (lane & 1) * kKvGroup;
+        pages = -1;
+        if (it + (lane >> 1) < tiles && tok < sp.end) {
+          const int tg = tok / kKvGroup, pg = tg / a.cache.gpp;
+          const int page = a.table[(int64_t)b * a.table_width + pg];
+          if (page >= 0 && page < a.cache.pages) pages = (page * a.cache.heads + head) * a.cache.gpp + (tg - pg * a.cache.gpp);
+        }
+      }
+      const int tok0 = sp.base + ((first + it) * kWaves + wave) * kTile;
+      int group[2];
+      group[0] = __builtin_amdgcn_readlane(pages, 2 * (it & 31));
+      group[1] = __builtin_amdgcn_readlane(pages, 2 * (it & 31) + 1);
+      const bool has0 = group[0] >= 0, has1 = group[1] >= 0;
+      if (!has0 && !has1) continue;
+      const bool whole = has0 && has1 && tok0 >= sp.begin && tok0 + kTile <= sp.end;
+      if (!has0) group[0] = group[1];
+      if (!has1) group[1] = group[0];
+      Tile<FMT, DB> t;
+      load_tile<FMT, DB>(a.cache, group, lane, t);
+      uint32_t okbits = 0xffu;
+      if (!whole) {
+        okbits = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int tok = tok0 + (i / 4) * kKvGroup + 4 * h + i % 4;
+          okbits |= ((i / 4 ? has1 : has0) && tok >= sp.begin && tok < sp.end) ? 1u << i : 0u;
+        }
+        clear_masked<FMT, DB>(t, okbits);
+      }
+
+      // Scores.
+      float x[8];
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        f32x4 acc{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+          uint32_t op[4];
+          k_operand<FMT, DB>(t, half, s, op);
+          acc = mma<FMT>(op, &qv[4 * s], acc);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[4 * half + i] = acc[i];
+      }
+      if (!whole) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = (okbits >> i) & 1u ? x[i] : kNegInf;
+      }
+      float top = x[0];
+#pragma unroll
+      for (int i = 1; i < 8; ++i) top = fmaxf(top, x[i]);
+      top *= score_scale;
+      if (__any(top > ref + (Softmax<FMT>::kOffset + Softmax<FMT>::kSlack))) {
+        top = fmaxf(top, lane_xor(top, 16));
+        top = fmaxf(top, lane_xor(top, 32));
+        const float next = fmaxf(ref, top - Softmax<FMT>::kOffset);
+        const float alpha = next == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(ref - next);
+        ref = next;
+        shift = fmaxf(ref, -1e30f);
+        sum *= alpha;
+#pragma unroll
+        for (int i = 0; i < kW; ++i) o[i] *= alpha;
+      }
+      float p[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], score_scale, -shift));
+        sum += p[i];
+      }
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (FMT == kKvNvfp4) {
+          const f16x2 u{(_Float16)p[2 * i], (_Float16)p[2 * i + 1]};
+          const f16x2 r{(_Float16)(p[2 * i] - (float)u[0]), (_Float16)(p[2 * i + 1] - (float)u[1])};
+          hi[i] = __builtin_bit_cast(uint32_t, u);
+          lo[i] = __builtin_bit_cast(uint32_t, r);
+        } else {
+          hi[i] = pack_bf16x2(p[2 * i], p[2 * i + 1]);
+          lo[i] = pack_bf16x2(p[2 * i] - bf16_lo(hi[i]), p[2 * i + 1] - bf16_hi(hi[i]));
+        }
+      }
+
+      // O^T += V^T P^T: step j takes d = W r + j, its eight tokens gathered by
+      // byte permutes from the tokens' pairs.
+      uint32_t vt[8][2 * DB];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v_token<FMT, DB>(t, i / 4, i % 4, vt[i]);
+#pragma unroll
+      for (int j = 0; j < kW; ++j) {
+        uint32_t op[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          op[i] = __builtin_amdgcn_perm(vt[2 * i + 1][j / 2], vt[2 * i][j / 2], j % 2 ? 0x07060302u : 0x05040100u);
+        o[j] = mma<FMT>(op, hi, o[j]);
+        o[j] = mma<FMT>(op, lo, o[j]);
+      }
+    }
+
+    // Join the four wavefronts.  o[j][i] is d = W (4h + i) + j of query q.
+    sum += lane_xor(sum, 16);
+    sum += lane_xor(sum, 32);
+    if (h == 0) {
+      s_ml[wave][qn][0] = ref;
+      s_ml[wave][qn][1] = sum;
+    }
+    if (qn < rows) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < kW; ++j) s_o[wave][qn][kW * (4 * h + i) + j] = o[j][i];
+    }
+    __syncthreads();
+    const int wfirst = (int)(((u0 + 1) * nwg - 1) / total), wlast = (int)((u1 * nwg - 1) / total);
+    const bool cut = wfirst != wlast;
+    float* part = part_of<kDp>(a, (int)w, (int)w == wfirst ? 1 : 0);
+    for (int e = tid; e < rows * (kDp / 4); e += kThreads) {
+      const int r = e / (kDp / 4), d = 4 * (e - r * (kDp / 4));
+      float top = kNegInf;
+#pragma unroll
+      for (int i = 0; i < kWaves; ++i) top = fmaxf(top, s_ml[i][r][0]);
+      float l = 0.0f;
+      f32x4 acc{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int i = 0; i < kWaves; ++i) {
+        const float m = s_ml[i][r][0];
+        const float f = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m - top);
+        l += f * s_ml[i][r][1];
+        const f32x4 v = *reinterpret_cast<const f32x4*>(&s_o[i][r][d]);
+        acc += v * f;
+      }
+      if (cut) {
+        float* to = part + (int64_t)r * (kDp + 4);
+        if (d == 0) {
+          store_coherent(to, top);
+          store_coherent(to + 1, l);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) store_coherent(to + 4 + d + i, acc[i]);
+      } else {
+        const int qh = head * a.group + rt * kRows + r;
+        const float f = l > 0.0f || l != l ? a.cache.v_scale / l : 0.0f;
+        if (d < a.cache.head_dim) {
+          uint16_t* to = a.out + (int64_t)b * a.ldo + (int64_t)qh * a.cache.head_dim + d;
+          *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(acc[0] * f, acc[1] * f), pack_bf16x2(acc[2] * f, acc[3] * f));
+        }
+        if (d == 0 && a.lse) a.lse[(int64_t)b * a.q_heads + qh] = l > 0.0f || l != l ? (top + __builtin_amdgcn_logf(l)) * kLn2 : kNegInf;
+      }
+    }
+    if (cut && arrive_last(a.counters + wfirst, (unsigned)(wlast - wfirst + 1))) {
+      for (int e = tid; e < rows * (kDp / 4); e += kThreads) {
+        const int r = e / (kDp / 4), d = 4 * (e - r * (kDp / 4));
+        float top = kNegInf, l = 0.0f;
+        f32x4 acc{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int i = wfirst; i <= wlast; ++i) {
+          const float* from = part_of<kDp>(a, i, i == wfirst ? 1 : 0) + (int64_t)r * (kDp + 4);
+          const float m = load_coherent(from), li = load_coherent(from + 1);
+          f32x4 v;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[j] = load_coherent(from + 4 + d + j);
+          const float next = fmaxf(top, m);
+          const float fo = top == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(top - next);
+          const float fi = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m - next);
+          l = l * fo + li * fi;
+          acc = acc * fo + v * fi;
+          top = next;
+        }
+        const int qh = head * a.group + rt * kRows + r;
+        const float f = l > 0.0f || l != l ? a.cache.v_scale / l : 0.0f;
+        if (d < a.cache.head_dim) {
+          uint16_t* to = a.out + (int64_t)b * a.ldo + (int64_t)qh * a.cache.head_dim + d;
+          *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(acc[0] * f, acc[1] * f), pack_bf16x2(acc[2] * f, acc[3] * f));
+        }
+        if (d == 0 && a.lse) a.lse[(int64_t)b * a.q_heads + qh] = l > 0.0f || l != l ? (top + __builtin_amdgcn_logf(l)) * kLn2 : kNegInf;
+      }
+    }
+    __syncthreads();  // the LDS of this unit is free again
+    g = stop;
+  }
+}
+
+int row_tiles_of(const AttnLaunch& a) { return (a.q_heads / a.cache.heads + kRows - 1) / kRows; }
+
+// Workgroups of a launch: what the GPU holds at once, or one a granule if the
+// longest possible lengths have fewer.
+int workgroups_of(const AttnLaunch& a) {
+  int64_t tokens = a.table_width * a.cache.page_size;
+  if (a.window > 0 && a.window + kKvGroup < tokens) tokens = a.window + kKvGroup;
+  const int64_t granules = (tokens + kGranule - 1) / kGranule;
+  const int64_t all = a.batch * a.cache.heads * row_tiles_of(a) * (granules > 1 ? granules : 1);
+  const int64_t most = 512;
+  return (int)(all < most ? all : most);
+}
+
+int part_rows_of(const AttnLaunch& a) {
+  const int g = a.q_heads / a.cache.heads;
+  return g < kRows ? g : kRows;
+}
+
+template <int FMT, int DB>
+void attn_launch(const AttnLaunch& a, hipStream_t s) {
+  AttnParams p;
+  p.cache = a.cache;
+  p.q = a.q;
+  p.table = a.table;
+  p.lens = a.lens;
+  p.out = a.out;
+  p.lse = a.lse;
+  p.counters = static_cast<unsigned*>(a.ws);
+  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + kAttnCounterBytes);
+  p.ldq = a.ldq;
+  p.ldo = a.ldo;
+  p.table_width = a.table_width;
+  p.batch = (int32_t)a.batch;
+  p.q_heads = a.q_heads;
+  p.group = a.q_heads / a.cache.heads;
+  p.row_tiles = row_tiles_of(a);
+  p.window = a.window;
+  p.part_rows = part_rows_of(a);
+  p.scale = a.scale;
+  hipLaunchKernelGGL((attn_kernel<FMT, DB>), dim3((unsigned)workgroups_of(a)), dim3(kThreads), 0, s, p);
+}
+
+template <int FMT>
+void attn_launch_db(const AttnLaunch& a, hipStream_t s) {
+  switch ((a.cache.head_dim + 63) / 64) {
+    case 1: attn_launch<FMT, 1>(a, s); break;
+    case 2: attn_launch<FMT, 2>(a, s); break;
+    case 3: attn_launch<FMT, 3>(a, s); break;
+    default: attn_launch<FMT, 4>(a, s); break;
+  }
+}
+
+}  // namespace
+
+size_t attn_workspace_bytes(const AttnLaunch& a) {
+  const size_t dp = (size_t)((a.cache.head_dim + 63) / 64) * 64;
+  return kAttnCounterBytes + (size_t)workgroups_of(a) * 2 * part_rows_of(a) * (dp + 4) * sizeof(float);
+}
+
+hipError_t launch_attn_decode(const AttnLaunch& a, hipStream_t s) {
+  switch (a.format) {
+    case kKvBf16: attn_launch_db<kKvBf16>(a, s); break;
+    case kKvE4m3: attn_launch_db<kKvE4m3>(a, s); break;
+    default: attn_launch_db<kKvNvfp4>(a, s); break;
+  }
+  return hipGetLastError();
+}
+
+}  // namespace nvfp4

@@ -1,0 +1,325 @@
+"""GPU parity: attention of one new token per sequence over the paged cache, against the definition in 64 bits."""
+import numpy as np
+import pytest
+import torch
+
+import attn_reference as R
+from bit_quantized_decode_amd import binding as B
+from helpers import device
+
+pytestmark = pytest.mark.gpu
+
+FORMATS = [B.NVFP4_KV_BF16, B.NVFP4_KV_E4M3, B.NVFP4_KV_NVFP4]
+IDS = ["bf16", "e4m3", "nvfp4"]
+
+
+class Batch:
+    """A cache filled through kv_append, with everything outside the sequences' tokens left as NaN-like garbage."""
+
+    def __init__(self, dev, fmt, lens, hq, hk, d, page, seed=0, scales=(1.0, 1.0), spread=1.0, width=None):
+        rng = np.random.default_rng(seed)
+        self.fmt, self.lens, self.hq, self.hk, self.d, self.page, self.scales = fmt, list(lens), hq, hk, d, page, scales
+        b = len(lens)
+        self.width = max([1] + [-(-n // page) for n in lens]) if width is None else width
+        pages = b * self.width + 2
+        self.cache = B.KvCache(pages, page, hk, d, fmt, *scales, device=dev)
+        self.cache.pool.fill_(0xff)          # NaN codes, NaN scales, NaN bf16
+        order = rng.permutation(pages)
+        table = np.full((b, self.width), 2 ** 31 - 1, np.int64)
+        slots, at = [], 0
+        for i, n in enumerate(lens):
+            for p in range(-(-n // page)):
+                table[i, p] = order[at]
+                at += 1
+            j = np.arange(n)
+            slots.append(table[i, j // page] * page + j % page)
+        slots = np.concatenate(slots).astype(np.int64) if slots else np.zeros(0, np.int64)
+        n = len(slots)
+        k = torch.from_numpy((rng.standard_normal((n, hk, d)) * spread).astype(np.float32)).to(torch.bfloat16)
+        v = torch.from_numpy(rng.standard_normal((n, hk, d)).astype(np.float32)).to(torch.bfloat16)
+        if n:
+            B.kv_append(self.cache, k.to(dev), v.to(dev), torch.from_numpy(slots).to(dev))
+        self.k, self.v = R.stored(k.float().numpy(), fmt, scales[0]), R.stored(v.float().numpy(), fmt, scales[1])
+        self.q = torch.from_numpy(rng.standard_normal((b, hq, d)).astype(np.float32)).to(torch.bfloat16)
+        self.table = torch.from_numpy(table.astype(np.int32)).to(dev)
+        self.seq = torch.tensor(self.lens, dtype=torch.int32, device=dev)
+        self.dev = dev
+
+    def call(self, **kw):
+        return B.attn_decode(self.q.to(self.dev), self.cache, self.table, self.seq, lse=True, **kw)
+
+    def check(self, out, lse, scale=None, window=0, gone=(), what=""):
+        """gone: (sequence, page index) pairs that hold nothing."""
+        scale = self.d ** -0.5 if scale is None else scale
+        out, lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+        start, g, worst = 0, self.hq // self.hk, 0.0
+        for b, n in enumerate(self.lens):
+            j = np.arange(max(0, n - window) if window else 0, n)
+            j = j[[(b, p) not in gone for p in j // self.page]] if len(j) else j
+            for h in range(self.hk):
+                rows = slice(h * g, (h + 1) * g)
+                o, l, pv, size = R.attend(self.q[b, rows].double().numpy(), self.k[start + j, h], self.v[start + j, h], scale)
+                bo, bl = R.attend_bounds(size, len(j), self.d, o, pv, l)
+                empty = np.isneginf(l)
+                assert np.array_equal(np.isneginf(lse[b, rows]), empty), (what, b, h)
+                err = np.abs(out[b, rows] - o)
+                assert (err <= bo).all(), (what, "out", b, h, (err / bo).max())
+                errl = np.where(empty, 0, np.abs(np.where(empty, 0, lse[b, rows]) - np.where(empty, 0, l)))
+                assert (errl <= bl).all(), (what, "lse", b, h, (errl / bl).max())
+                worst = max(worst, (err / bo).max())
+            start += n
+        return worst
+
+
+@pytest.mark.parametrize("fmt", FORMATS, ids=IDS)
+@pytest.mark.parametrize("n", [1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 100, 127, 128, 129, 255, 257, 1000, 4097])
+def test_lengths(fmt, n):
+    dev = device()
+    x = Batch(dev, fmt, [n], 10, 2, 128, 64, seed=n)
+    x.check(*x.call())
+
+
+@pytest.mark.parametrize("fmt", FORMATS, ids=IDS)
+@pytest.mark.parametrize("d", [16, 48, 64, 80, 96, 128, 160, 192, 208, 256])
+def test_head_sizes(fmt, d):
+    dev = device()
+    x = Batch(dev, fmt, [70, 300, 5], 6, 2, d, 32, seed=d)
+    x.check(*x.call(), what=d)
+
+
+@pytest.mark.parametrize("fmt", FORMATS, ids=IDS)
+@pytest.mark.parametrize("hq,hk", [(1, 1), (7, 7), (8, 4), (5, 1), (16, 1), (17, 1), (32, 2), (40, 1), (66, 2)])
+def test_head_groups(fmt, hq, hk):
+    dev = device()
+    x = Batch(dev, fmt, [200, 0, 33], hq, hk, 64, 16, seed=hq)
+    x.check(*x.call(), what=(hq, hk))
+
+
+@pytest.mark.parametrize("fmt", FORMATS, ids=IDS)
+@pytest.mark.parametrize("page", [16, 32, 48, 80, 128, 1024])
+def test_page_sizes(fmt, page):
+    dev = device()
+    x = Batch(dev, fmt, [1, page - 1, page, page + 1, 3 * page + 7, 777], 4, 2, 64, page, seed=page)
+    x.check(*x.call(), what=page)
+
+
+@pytest.mark.parametrize("fmt", FORMATS, ids=IDS)
+@pytest.mark.parametrize("window", [1, 7, 16, 100, 128, 500, 10 ** 12])
+def test_windows(fmt, window):
+    dev = device()
+    x = Batch(dev, fmt, [1, 0, 99, 128, 513, 2000], 5, 1, 128, 48, seed=window % 97)
+    x.check(*x.call(window=window), window=window)
+
+
+@pytest.mark.parametrize("fmt", FORMATS, ids=IDS)
+def test_ragged_batches_and_empty_rows(fmt):
+    dev = device()
+    rng = np.random.default_rng(3)
+    for lens in ([0], [0, 0, 0], [0, 5, 0], list(rng.integers(0, 700, size=67)), [3] * 300, [6000, 1, 1, 1],
+                 [0] * 511 + [40]):
+        x = Batch(dev, fmt, lens, 4, 2, 64, 32, seed=len(lens))
+        x.check(*x.call(), what=len(lens))
+
+
+def test_large_batch_of_rows():
+    """More rows than threads of a workgroup share among them: 2000 short sequences."""
+    dev = device()
+    rng = np.random.default_rng(4)
+    x = Batch(dev, B.NVFP4_KV_NVFP4, list(rng.integers(0, 40, size=2000)), 2, 1, 64, 16)
+    x.check(*x.call())
+
+
+@pytest.mark.parametrize("fmt", FORMATS, ids=IDS)
+def test_long_sequence_split_over_every_workgroup(fmt):
+    dev = device()
+    x = Batch(dev, fmt, [70_001], 2, 1, 64, 256)
+    x.check(*x.call())
+
+
+@pytest.mark.parametrize("fmt", FORMATS, ids=IDS)
+def test_sharp_flat_and_growing_scores(fmt):
+    """Scores far apart, all equal, and rising along the sequence (the reference moves at every step)."""
+    dev = device()
+    x = Batch(dev, fmt, [900], 5, 1, 128, 64, seed=1, spread=20.0)
+    x.check(*x.call(), what="sharp")
+    x.check(*x.call(scale=1e-6), scale=1e-6, what="flat")
+    for sign in (1, -1):
+        y = Batch(dev, fmt, [900], 5, 1, 128, 64, seed=2)
+        ramp = torch.arange(1, 901, dtype=torch.float32)[:, None, None] * 0.05 * sign
+        k = (ramp.expand(900, 1, 128) * 0.5).to(torch.bfloat16)
+        v = torch.randn(900, 1, 128, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16)
+        slots = (y.table[0].long()[torch.arange(900, device=dev) // 64] * 64 + torch.arange(900, device=dev) % 64)
+        B.kv_append(y.cache, k.to(dev), v.to(dev), slots)
+        y.k, y.v = R.stored(k.float().numpy(), fmt), R.stored(v.float().numpy(), fmt)
+        y.q = torch.ones(1, 5, 128, dtype=torch.bfloat16)
+        y.check(*y.call(), what=sign)
+
+
+def test_small_terms_add_up():
+    """One token at the maximum and 60,000 that each weigh 2^-20 of it: no term may be lost to a 16-bit range."""
+    dev = device()
+    n = 60_000
+    for fmt in FORMATS:
+        x = Batch(dev, fmt, [n], 1, 1, 64, 256)
+        k = torch.zeros(n, 1, 64)
+        k[n // 3, 0, 0] = 6.0
+        v = torch.ones(n, 1, 64)
+        v[n // 3] = -1.0
+        slots = (x.table[0].long()[torch.arange(n, device=dev) // 256] * 256 + torch.arange(n, device=dev) % 256)
+        B.kv_append(x.cache, k.to(dev), v.to(dev), slots)
+        x.k, x.v = R.stored(k.numpy(), fmt), R.stored(v.numpy(), fmt)
+        x.q = torch.zeros(1, 1, 64, dtype=torch.bfloat16)
+        x.q[0, 0, 0] = 1.0
+        scale = 20 * np.log(2) / 6
+        x.check(*x.call(scale=scale), scale=scale, what=fmt)
+
+
+def test_tensor_scales_and_query_range():
+    dev = device()
+    x = Batch(dev, B.NVFP4_KV_NVFP4, [333, 20], 6, 2, 128, 64, scales=(0.25, 3.0))
+    x.check(*x.call())
+    x = Batch(dev, B.NVFP4_KV_NVFP4, [333, 20], 6, 2, 128, 64, scales=(2.0 ** -40, 2.0 ** 30))
+    for size in (2.0 ** -60, 2.0 ** 40):
+        y = Batch(dev, B.NVFP4_KV_NVFP4, [333, 20], 6, 2, 128, 64, scales=(1.0, 1.0))
+        y.q = (y.q.float() * size).to(torch.bfloat16)
+        scale = 1 / (size * 11)
+        y.check(*y.call(scale=scale), scale=scale, what=size)
+
+
+@pytest.mark.parametrize("fmt", FORMATS, ids=IDS)
+def test_evicted_pages(fmt):
+    """Page ids outside the pool hold nothing; a row whose pages are all gone is empty."""
+    dev = device()
+    x = Batch(dev, fmt, [300, 300, 90], 4, 2, 64, 48, seed=9)
+    gone = [(0, 0), (0, 3), (1, 6), (2, 0), (2, 1)]
+    for b, p in gone:
+        x.table[b, p] = [-1, 10 ** 9, x.cache.pages, -2 ** 31, -7][(b + p) % 5]
+    x.check(*x.call(), gone=set(gone))
+
+
+@pytest.mark.parametrize("fmt", FORMATS, ids=IDS)
+def test_lengths_out_of_range(fmt):
+    """Negative lengths count as 0, lengths past the table as the table's."""
+    dev = device()
+    x = Batch(dev, fmt, [96, 96, 0], 4, 2, 64, 48, seed=2)
+    x.seq = torch.tensor([10 ** 9, 96, -5], dtype=torch.int32, device=dev)
+    x.check(*x.call())
+
+
+@pytest.mark.parametrize("fmt", FORMATS, ids=IDS)
+def test_nan_in_a_row_stays_in_its_head(fmt):
+    dev = device()
+    x = Batch(dev, fmt, [200, 50], 4, 2, 64, 32, seed=1)
+    bad = torch.ones(1, 2, 64, device=dev)
+    bad[0, 1, 5] = float("nan")
+    slot = (x.table[0, 1].long() * 32 + 3).view(1)
+    for side in (0, 1):
+        y = Batch(dev, fmt, [200, 50], 4, 2, 64, 32, seed=1)
+        ok = torch.ones(1, 2, 64, device=dev)
+        B.kv_append(y.cache, *((bad, ok) if side == 0 else (ok, bad)), slot)
+        out, lse = y.call()
+        assert not out[0, :2].isnan().any() and not out[1].isnan().any() and not lse[1].isnan().any()
+        assert out[0, 2:].isnan().any(-1).all()
+        assert lse[0, 2:].isnan().all() == (side == 0)
+
+
+def test_strided_rows_and_untouched_neighbours():
+    dev = device()
+    x = Batch(dev, B.NVFP4_KV_E4M3, [100, 64, 7], 4, 2, 80, 32, seed=2)
+    wide_q = torch.full((3, 4 * 80 + 64), float("nan"), dtype=torch.bfloat16, device=dev)
+    q = wide_q[:, :320].unflatten(1, (4, 80))
+    q.copy_(x.q)
+    wide_o = torch.full((4, 4 * 80 + 40), 9.0, dtype=torch.bfloat16, device=dev)
+    out = wide_o[:3, :320].unflatten(1, (4, 80))
+    lse = torch.empty(3, 4, device=dev)
+    B.attn_decode(q, x.cache, x.table, x.seq, out=out, lse=lse)
+    x.check(out, lse)
+    assert (wide_o[:, 320:] == 9.0).all() and (wide_o[3] == 9.0).all()
+
+
+def test_repeats_are_bit_identical_and_leave_counters_zero():
+    dev = device()
+    x = Batch(dev, B.NVFP4_KV_NVFP4, [5000, 30, 1200], 10, 2, 128, 64, seed=2)
+    ws = torch.zeros(64 << 20, dtype=torch.uint8, device=dev)
+    first = x.call(ws=ws)
+    for _ in range(5):
+        again = x.call(ws=ws)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+    y = Batch(dev, B.NVFP4_KV_BF16, [3000] * 3, 4, 1, 256, 64, seed=2)     # another shape through the same workspace
+    y.check(*y.call(ws=ws))
+    assert not ws[:8192].any()
+    assert torch.equal(first[0], x.call(ws=ws)[0])
+
+
+def test_capture_and_replay():
+    """A captured call replayed among eager calls on the same stream, over changing lengths and queries."""
+    dev = device()
+    x = Batch(dev, B.NVFP4_KV_NVFP4, [2000, 700, 1], 10, 2, 128, 64, seed=2)
+    q, seq = x.q.to(dev), x.seq.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graphs = []
+    with torch.cuda.stream(side):
+        B.attn_decode(q, x.cache, x.table, seq, lse=True)
+        for _ in range(2):
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=side):
+                out = B.attn_decode(q, x.cache, x.table, seq, lse=True)
+            graphs.append((g, out))
+    torch.cuda.synchronize()
+    for step, lens in enumerate(([2000, 700, 1], [1, 0, 1], [1999, 333, 0], [2000, 700, 1])):
+        seq.copy_(torch.tensor(lens, dtype=torch.int32))
+        x.seq.copy_(seq)
+        q.mul_(-1 if step % 2 else 1)
+        want = B.attn_decode(q, x.cache, x.table, seq, lse=True)
+        for g, out in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        eager = B.attn_decode(q, x.cache, x.table, seq, lse=True)
+        torch.cuda.synchronize()
+        for g, out in graphs:
+            assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1]), step
+        assert torch.equal(eager[0], want[0])
+
+
+def test_streams_overlap():
+    """Calls on several streams, each with its own default workspace; and a call told its stream."""
+    dev = device()
+    xs = [Batch(dev, f, [3000, 100], 10, 2, 128, 64, seed=s) for s, f in enumerate(FORMATS)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    got = []
+    for _ in range(10):
+        got = []
+        for x, s in zip(xs, streams):
+            q = x.q.to(dev)
+            s.wait_stream(torch.cuda.current_stream())
+            got.append(B.attn_decode(q, x.cache, x.table, x.seq, lse=True, stream=s))
+            q.record_stream(s)
+    torch.cuda.synchronize()
+    for x, o in zip(xs, got):
+        x.check(*o)
+
+
+def test_prepared_call():
+    dev = device()
+    x = Batch(dev, B.NVFP4_KV_E4M3, [500, 64], 8, 2, 64, 32)
+    call = B.attn_decode_prepared(x.q.to(dev), x.cache, x.table, x.seq, lse=True)
+    a = [t.clone() for t in call()]
+    b = call()
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    x.check(*b)
+
+
+def test_shared_pages_as_several_new_tokens():
+    """Three new tokens of one sequence as rows with the same table and lengths n, n + 1, n + 2."""
+    dev = device()
+    x = Batch(dev, B.NVFP4_KV_NVFP4, [402], 5, 1, 128, 64, seed=4)
+    q = torch.randn(3, 5, 128, device=dev).to(torch.bfloat16)
+    lens = torch.tensor([400, 401, 402], dtype=torch.int32, device=dev)
+    out, lse = B.attn_decode(q, x.cache, x.table.expand(3, -1).contiguous(), lens, lse=True)
+    for i in range(3):
+        y = Batch.__new__(Batch)
+        y.__dict__.update(x.__dict__)
+        y.lens, y.q = [400 + i], q[i:i + 1].cpu()
+        y.check(out[i:i + 1], lse[i:i + 1])
