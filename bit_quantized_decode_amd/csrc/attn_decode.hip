@@ -54,7 +54,7 @@ struct AttnParams {
   unsigned* counters;
   float* part;         // partial sums, see part_of()
   int64_t ldq, ldo, table_width;
-  int32_t batch, q_heads, group, row_tiles, window, part_rows;
+  int32_t batch, q_heads, group, row_tiles, window, part_rows, part_bytes;
   float scale;
 };
 
@@ -77,9 +77,21 @@ __device__ __forceinline__ Span span_of(const AttnParams& a, int len) {
 
 // The partial sums that workgroup w leaves of a unit that starts before its share
 // (side 0) or in it (side 1): rows of reference, sum and the padded head's sums.
+// They are written through to memory and read from it (sc1), whichever XCDs the
+// workgroups run on; offsets are bytes, below 2^31 for every workspace.
 template <int DP>
-__device__ __forceinline__ float* part_of(const AttnParams& a, int w, int side) {
-  return a.part + ((int64_t)2 * w + side) * a.part_rows * (DP + 4);
+__device__ __forceinline__ int part_offset(const AttnParams& a, int w, int side, int row) {
+  return ((2 * w + side) * a.part_rows + row) * (DP + 4) * 4;
+}
+constexpr int kThroughMemory = 16;  // cache policy sc1
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t part_buffer(const AttnParams& a) {
+  return __builtin_amdgcn_make_buffer_rsrc(a.part, 0, a.part_bytes, 0x00020000);
+}
+__device__ __forceinline__ f32x4 load_part(__amdgpu_buffer_rsrc_t r, int offset) {
+  return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, offset, 0, kThroughMemory));
+}
+__device__ __forceinline__ void store_part(__amdgpu_buffer_rsrc_t r, int offset, f32x4 v) {
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), r, offset, 0, kThroughMemory);
 }
 
 template <int FMT, int DB>
@@ -245,6 +257,99 @@ struct Softmax {
   static constexpr float kSlack = 8.0f;
 };
 
+// Four outputs of row `qh` of sequence b from their sums, and (d == 0) its lse.
+__device__ __forceinline__ void write_out(const AttnParams& a, int b, int qh, int d, float ref, float l, f32x4 acc) {
+  const bool some = l > 0.0f || l != l;  // NaN stays NaN
+  const float f = some ? a.cache.v_scale / l : 0.0f;
+  if (d < a.cache.head_dim) {
+    uint16_t* to = a.out + (int64_t)b * a.ldo + (int64_t)qh * a.cache.head_dim + d;
+    *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(acc[0] * f, acc[1] * f), pack_bf16x2(acc[2] * f, acc[3] * f));
+  }
+  if (d == 0 && a.lse) a.lse[(int64_t)b * a.q_heads + qh] = some ? (ref + __builtin_amdgcn_logf(l)) * kLn2 : kNegInf;
+}
+
+// Joins the partial sums that workgroups wfirst .. wlast left of a unit.  The
+// parts are cut into runs over the threads that its values leave over; each
+// thread adds its run in workgroup order, eight parts a round trip, under
+// weights formed from the references and sums that were read first; the runs are
+// then added in order through LDS.  `lds` is the kernel's staging space.
+template <int DP>
+__device__ __forceinline__ void join_parts(const AttnParams& a, int wfirst, int wlast, int rows, int b, int q0, float* lds) {
+  constexpr int kChunk = 64;                       // parts whose references and sums LDS holds at once
+  constexpr int kBatch = 8;                        // parts a round trip
+  constexpr int kQuads = DP / 4;
+  float (*ml)[kRows][2] = reinterpret_cast<float (*)[kRows][2]>(lds);   // [kChunk][kRows][2]
+  const int parts = wlast - wfirst + 1, items = rows * kQuads;
+  const int runs = items >= kThreads ? 1 : kThreads / items;
+  const __amdgpu_buffer_rsrc_t buf = part_buffer(a);
+  const auto row_of = [&](int part, int r) { return part_offset<DP>(a, wfirst + part, part == 0 ? 1 : 0, r); };
+  for (int e0 = 0; e0 < items; e0 += kThreads) {   // more than one round: runs == 1
+    const int e = e0 + (int)threadIdx.x, run = e / items, item = runs > 1 ? e - run * items : e;
+    const bool live = runs > 1 ? run < runs : e < items;
+    const int r = live ? item / kQuads : 0, d = live ? 4 * (item - r * kQuads) : 0;
+    float top = kNegInf, l = 0.0f;
+    f32x4 acc{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int c0 = 0; c0 < parts; c0 += kChunk) {
+      const int n = min(kChunk, parts - c0);
+      __syncthreads();
+      for (int i = threadIdx.x; i < n * rows; i += kThreads) {
+        const int part = i / rows, rr = i - part * rows;
+        const f32x4 v = load_part(buf, row_of(c0 + part, rr));
+        ml[part][rr][0] = v[0];
+        ml[part][rr][1] = v[1];
+      }
+      __syncthreads();
+      if (!live) continue;
+      const int mine = runs > 1 ? run : 0;
+      const int p0 = n * mine / runs, p1 = n * (mine + 1) / runs;
+      if (p0 >= p1) continue;
+      float next = top;
+      for (int i = p0; i < p1; ++i) next = fmaxf(next, ml[i][r][0]);
+      const float fo = top == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(top - next);
+      l *= fo;
+      acc *= fo;
+      top = next;
+      for (int i = p0; i < p1; i += kBatch) {
+        f32x4 v[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) v[j] = load_part(buf, row_of(c0 + min(i + j, p1 - 1), r) + (4 + d) * 4);
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          if (i + j >= p1) break;
+          const float m = ml[i + j][r][0];
+          const float f = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m - top);
+          l += f * ml[i + j][r][1];
+          acc += v[j] * f;
+        }
+      }
+    }
+    if (runs > 1) {
+      float* mine = lds + (run * items + item) * 6;
+      __syncthreads();
+      if (live) {
+        mine[0] = top;
+        mine[1] = l;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mine[2 + j] = acc[j];
+      }
+      __syncthreads();
+      if (live && run == 0) {
+        for (int i = 1; i < runs; ++i) {
+          const float* other = lds + (i * items + item) * 6;
+          const float m = other[0], next = fmaxf(top, m);
+          const float fo = top == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(top - next);
+          const float fi = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m - next);
+          l = l * fo + other[1] * fi;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[j] = acc[j] * fo + other[2 + j] * fi;
+          top = next;
+        }
+      }
+    }
+    if (live && (runs == 1 || run == 0)) write_out(a, b, q0 + r, d, top, l, acc);
+  }
+}
+
 template <int FMT, int DB>
 __global__ __launch_bounds__(kThreads) void attn_kernel(const AttnParams a) {
   using L = KvLayout<FMT, DB>;
@@ -252,7 +357,7 @@ __global__ __launch_bounds__(kThreads) void attn_kernel(const AttnParams a) {
   constexpr int kOStride = kDp + 4;
   __shared__ float s_ml[kWaves][kRows][2];
   __shared__ __attribute__((aligned(16))) float s_o[kWaves][kRows][kOStride];
-  __shared__ int64_t s_scan[kThreads];
+  __shared__ int64_t s_scan[kWaves];
   __shared__ int64_t s_start[3];  // batch row, granules before it, all granules
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -265,20 +370,24 @@ __global__ __launch_bounds__(kThreads) void attn_kernel(const AttnParams a) {
   const int b0 = min(tid * per, a.batch), b1 = min(b0 + per, a.batch);
   int64_t mine = 0;
   for (int b = b0; b < b1; ++b) mine += (int64_t)span_of(a, a.lens[b]).granules * units_per_row;
-  s_scan[tid] = mine;
-  __syncthreads();
-  for (int off = 1; off < kThreads; off <<= 1) {
-    const int64_t x = tid >= off ? s_scan[tid - off] : 0;
-    __syncthreads();
-    s_scan[tid] += x;
-    __syncthreads();
+  int64_t upto = mine;   // inclusive: lanes of the wavefront, then the wavefronts before
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int64_t x = __shfl_up(upto, off);
+    upto += lane >= off ? x : 0;
   }
-  const int64_t total = s_scan[kThreads - 1];
+  if (lane == 63) s_scan[wave] = upto;
+  __syncthreads();
+  int64_t total = 0;
+#pragma unroll
+  for (int i = 0; i < kWaves; ++i) {
+    upto += i < wave ? s_scan[i] : 0;
+    total += s_scan[i];
+  }
   const int64_t nwg = min((int64_t)gridDim.x, total);
   const int64_t w = blockIdx.x;
   if (w >= nwg) return;
   const int64_t g0 = total * w / nwg, g1 = total * (w + 1) / nwg;
-  const int64_t upto = s_scan[tid];
   if (upto - mine <= g0 && g0 < upto) {
     int64_t before = upto - mine;
     int b = b0;
@@ -465,7 +574,7 @@ __global__ __launch_bounds__(kThreads) void attn_kernel(const AttnParams a) {
     __syncthreads();
     const int wfirst = (int)(((u0 + 1) * nwg - 1) / total), wlast = (int)((u1 * nwg - 1) / total);
     const bool cut = wfirst != wlast;
-    float* part = part_of<kDp>(a, (int)w, (int)w == wfirst ? 1 : 0);
+    const __amdgpu_buffer_rsrc_t buf = part_buffer(a);
     for (int e = tid; e < rows * (kDp / 4); e += kThreads) {
       const int r = e / (kDp / 4), d = 4 * (e - r * (kDp / 4));
       float top = kNegInf;
@@ -482,50 +591,15 @@ __global__ __launch_bounds__(kThreads) void attn_kernel(const AttnParams a) {
         acc += v * f;
       }
       if (cut) {
-        float* to = part + (int64_t)r * (kDp + 4);
-        if (d == 0) {
-          store_coherent(to, top);
-          store_coherent(to + 1, l);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) store_coherent(to + 4 + d + i, acc[i]);
+        const int to = part_offset<kDp>(a, (int)w, (int)w == wfirst ? 1 : 0, r);
+        if (d == 0) store_part(buf, to, f32x4{top, l, 0.0f, 0.0f});
+        store_part(buf, to + (4 + d) * 4, acc);
       } else {
-        const int qh = head * a.group + rt * kRows + r;
-        const float f = l > 0.0f || l != l ? a.cache.v_scale / l : 0.0f;
-        if (d < a.cache.head_dim) {
-          uint16_t* to = a.out + (int64_t)b * a.ldo + (int64_t)qh * a.cache.head_dim + d;
-          *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(acc[0] * f, acc[1] * f), pack_bf16x2(acc[2] * f, acc[3] * f));
-        }
-        if (d == 0 && a.lse) a.lse[(int64_t)b * a.q_heads + qh] = l > 0.0f || l != l ? (top + __builtin_amdgcn_logf(l)) * kLn2 : kNegInf;
+        write_out(a, b, head * a.group + rt * kRows + r, d, top, l, acc);
       }
     }
-    if (cut && arrive_last(a.counters + wfirst, (unsigned)(wlast - wfirst + 1))) {
-      for (int e = tid; e < rows * (kDp / 4); e += kThreads) {
-        const int r = e / (kDp / 4), d = 4 * (e - r * (kDp / 4));
-        float top = kNegInf, l = 0.0f;
-        f32x4 acc{0.0f, 0.0f, 0.0f, 0.0f};
-        for (int i = wfirst; i <= wlast; ++i) {
-          const float* from = part_of<kDp>(a, i, i == wfirst ? 1 : 0) + (int64_t)r * (kDp + 4);
-          const float m = load_coherent(from), li = load_coherent(from + 1);
-          f32x4 v;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) v[j] = load_coherent(from + 4 + d + j);
-          const float next = fmaxf(top, m);
-          const float fo = top == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(top - next);
-          const float fi = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m - next);
-          l = l * fo + li * fi;
-          acc = acc * fo + v * fi;
-          top = next;
-        }
-        const int qh = head * a.group + rt * kRows + r;
-        const float f = l > 0.0f || l != l ? a.cache.v_scale / l : 0.0f;
-        if (d < a.cache.head_dim) {
-          uint16_t* to = a.out + (int64_t)b * a.ldo + (int64_t)qh * a.cache.head_dim + d;
-          *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(acc[0] * f, acc[1] * f), pack_bf16x2(acc[2] * f, acc[3] * f));
-        }
-        if (d == 0 && a.lse) a.lse[(int64_t)b * a.q_heads + qh] = l > 0.0f || l != l ? (top + __builtin_amdgcn_logf(l)) * kLn2 : kNegInf;
-      }
-    }
+    if (cut && arrive_last(a.counters + wfirst, (unsigned)(wlast - wfirst + 1)))
+      join_parts<kDp>(a, wfirst, wlast, rows, b, head * a.group + rt * kRows, &s_o[0][0][0]);
     __syncthreads();  // the LDS of this unit is free again
     g = stop;
   }
@@ -549,6 +623,11 @@ int part_rows_of(const AttnLaunch& a) {
   return g < kRows ? g : kRows;
 }
 
+size_t part_bytes_of(const AttnLaunch& a) {
+  const size_t dp = (size_t)((a.cache.head_dim + 63) / 64) * 64;
+  return (size_t)workgroups_of(a) * 2 * part_rows_of(a) * (dp + 4) * sizeof(float);
+}
+
 template <int FMT, int DB>
 void attn_launch(const AttnLaunch& a, hipStream_t s) {
   AttnParams p;
@@ -569,6 +648,7 @@ void attn_launch(const AttnLaunch& a, hipStream_t s) {
   p.row_tiles = row_tiles_of(a);
   p.window = a.window;
   p.part_rows = part_rows_of(a);
+  p.part_bytes = (int32_t)part_bytes_of(a);
   p.scale = a.scale;
   hipLaunchKernelGGL((attn_kernel<FMT, DB>), dim3((unsigned)workgroups_of(a)), dim3(kThreads), 0, s, p);
 }
@@ -585,10 +665,7 @@ void attn_launch_db(const AttnLaunch& a, hipStream_t s) {
 
 }  // namespace
 
-size_t attn_workspace_bytes(const AttnLaunch& a) {
-  const size_t dp = (size_t)((a.cache.head_dim + 63) / 64) * 64;
-  return kAttnCounterBytes + (size_t)workgroups_of(a) * 2 * part_rows_of(a) * (dp + 4) * sizeof(float);
-}
+size_t attn_workspace_bytes(const AttnLaunch& a) { return kAttnCounterBytes + part_bytes_of(a); }
 
 hipError_t launch_attn_decode(const AttnLaunch& a, hipStream_t s) {
   switch (a.format) {
