@@ -104,29 +104,6 @@ nvfp4::KvCache cache_of(const nvfp4_kv_cache* c) {
   return r;
 }
 
-int check_attn(const nvfp4_attn_args* a, bool need_buffers) {
-  if (!a) return fail(NVFP4_ERR_NULL, "args is NULL");
-  NVFP4_TRY(check_cache(a->cache, need_buffers && a->batch > 0));
-  if (a->batch < 0 || a->batch > 65536) return fail(NVFP4_ERR_SHAPE, "batch=%lld must be in [0, 65536]", (long long)a->batch);
-  if (a->q_heads < 1 || a->q_heads > kMaxHeads || a->q_heads % a->cache->kv_heads != 0)
-    return fail(NVFP4_ERR_SHAPE, "q_heads=%lld must be a multiple of kv_heads=%lld, at most %lld", (long long)a->q_heads,
-                (long long)a->cache->kv_heads, (long long)kMaxHeads);
-  if (a->table_width < 0 || a->table_width > nvfp4::kMaxDim / a->cache->page_size)
-    return fail(NVFP4_ERR_SHAPE, "table_width=%lld must be >= 0, and table_width * page_size at most 2^30",
-                (long long)a->table_width);
-  if (a->window < 0) return fail(NVFP4_ERR_ARG, "window=%lld is negative", (long long)a->window);
-  if (!need_buffers || a->batch == 0) return NVFP4_OK;
-  if (!(a->scale > 0.0f) || !std::isfinite(a->scale)) return fail(NVFP4_ERR_ARG, "scale must be positive and finite");
-  NVFP4_TRY(check_ld(a->ldq, a->q_heads * a->cache->head_dim, "ldq"));
-  NVFP4_TRY(check_ld(a->ldo, a->q_heads * a->cache->head_dim, "ldo"));
-  if (!a->q || !a->out || !a->seq_lens || (a->table_width > 0 && !a->page_table))
-    return fail(NVFP4_ERR_NULL, "q, page_table, seq_lens and out must be non-NULL");
-  if (!aligned16(a->q) || !aligned16(a->out)) return fail(NVFP4_ERR_ALIGN, "q and out must be 16-byte aligned");
-  if (!aligned4(a->page_table) || !aligned4(a->seq_lens) || !aligned4(a->lse))
-    return fail(NVFP4_ERR_ALIGN, "page_table, seq_lens and lse must be 4-byte aligned");
-  return NVFP4_OK;
-}
-
 nvfp4::AttnLaunch attn_of(const nvfp4_attn_args* a) {
   nvfp4::AttnLaunch l;
   l.cache = cache_of(a->cache);
@@ -145,6 +122,31 @@ nvfp4::AttnLaunch attn_of(const nvfp4_attn_args* a) {
   l.lse = a->lse;
   l.ws = a->workspace;
   return l;
+}
+
+int check_attn(const nvfp4_attn_args* a, bool need_buffers) {
+  if (!a) return fail(NVFP4_ERR_NULL, "args is NULL");
+  NVFP4_TRY(check_cache(a->cache, need_buffers && a->batch > 0));
+  if (a->batch < 0 || a->batch > 65536) return fail(NVFP4_ERR_SHAPE, "batch=%lld must be in [0, 65536]", (long long)a->batch);
+  if (a->q_heads < 1 || a->q_heads > kMaxHeads || a->q_heads % a->cache->kv_heads != 0)
+    return fail(NVFP4_ERR_SHAPE, "q_heads=%lld must be a multiple of kv_heads=%lld, at most %lld", (long long)a->q_heads,
+                (long long)a->cache->kv_heads, (long long)kMaxHeads);
+  if (a->table_width < 0 || a->table_width > nvfp4::kMaxDim / a->cache->page_size)
+    return fail(NVFP4_ERR_SHAPE, "table_width=%lld must be >= 0, and table_width * page_size at most 2^30",
+                (long long)a->table_width);
+  if (a->window < 0) return fail(NVFP4_ERR_ARG, "window=%lld is negative", (long long)a->window);
+  if (!nvfp4::attn_fits(attn_of(a)))
+    return fail(NVFP4_ERR_SHAPE, "batch x query rows x table too large: the call would have 2^31 tiles of 32 tokens or more");
+  if (!need_buffers || a->batch == 0) return NVFP4_OK;
+  if (!(a->scale > 0.0f) || !std::isfinite(a->scale)) return fail(NVFP4_ERR_ARG, "scale must be positive and finite");
+  NVFP4_TRY(check_ld(a->ldq, a->q_heads * a->cache->head_dim, "ldq"));
+  NVFP4_TRY(check_ld(a->ldo, a->q_heads * a->cache->head_dim, "ldo"));
+  if (!a->q || !a->out || !a->seq_lens || (a->table_width > 0 && !a->page_table))
+    return fail(NVFP4_ERR_NULL, "q, page_table, seq_lens and out must be non-NULL");
+  if (!aligned16(a->q) || !aligned16(a->out)) return fail(NVFP4_ERR_ALIGN, "q and out must be 16-byte aligned");
+  if (!aligned4(a->page_table) || !aligned4(a->seq_lens) || !aligned4(a->lse))
+    return fail(NVFP4_ERR_ALIGN, "page_table, seq_lens and lse must be 4-byte aligned");
+  return NVFP4_OK;
 }
 
 }  // namespace

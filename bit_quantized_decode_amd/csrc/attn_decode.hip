@@ -19,24 +19,27 @@
 // per row.  Probabilities enter as the sum of two 16-bit numbers, so they
 // carry 16 bits (bf16) or 22 (f16); everything else is fp32.
 //
-// Work split.  One granule is 128 tokens of one (sequence, kv head, row tile): 32 a
-// wavefront.  The granules of all sequences form one line, cut evenly over the
-// workgroups whatever the lengths are; a unit (sequence, head, row tile) cut
-// between workgroups leaves partial sums, and the last to arrive joins them in
-// workgroup order.
+// Work split.  The 32-token tiles of all units (sequence, kv head, row tile) form
+// one line, each unit led by kLead blank places for what starting it costs.
+// The line is cut evenly over the workgroups (one a CU) and each share over the
+// wavefronts, whatever the lengths are.  A wavefront walks its run of the line
+// by itself: it writes the units that lie inside its run, leaves the end of a
+// unit begun by an earlier wavefront in LDS, and keeps the beginning of one that
+// goes on in registers.  Once all are through, each beginning is joined with
+// what follows it in LDS.  What goes on in another workgroup becomes a partial
+// sum in memory, and the last workgroup of a unit to arrive joins those, in order.
 #include "attn_launchers.h"
 #include "device_common.h"
 
 namespace nvfp4 {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWaves = 4;
 constexpr int kTile = 32;                  // tokens of a wavefront's step
-constexpr int kGranule = kTile * kWaves;
 constexpr int kRows = 16;                  // query heads of a row tile
-constexpr int kMaxWorkgroups = 2048;       // counters in the workspace
-static_assert(kMaxWorkgroups * 4 <= (int)kAttnCounterBytes, "one counter a workgroup");
+constexpr int kCus = 256;
+constexpr int kLead = 2;                   // places before a unit's tiles
+constexpr int kShare = 6;                  // places of a workgroup's share, at least
+static_assert(kCus * 4 <= (int)kAttnCounterBytes, "one counter a workgroup");
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNegInf = -__builtin_inff();
@@ -52,7 +55,7 @@ struct AttnParams {
   uint16_t* out;
   float* lse;
   unsigned* counters;
-  float* part;         // partial sums, see part_of()
+  float* part;         // partial sums, see part_offset()
   int64_t ldq, ldo, table_width;
   int32_t batch, q_heads, group, row_tiles, window, part_rows, part_bytes;
   float scale;
@@ -62,7 +65,7 @@ struct AttnParams {
 struct Span {
   int begin, end;      // [begin, end)
   int base;            // begin rounded down to a group
-  int granules;        // at least one, so that an empty row is written too
+  int tiles;           // at least one, so that an empty row is written too
 };
 __device__ __forceinline__ Span span_of(const AttnParams& a, int len) {
   Span s;
@@ -70,8 +73,8 @@ __device__ __forceinline__ Span span_of(const AttnParams& a, int len) {
   s.end = len < 0 ? 0 : (int64_t)len > most ? (int)most : len;
   s.begin = a.window > 0 && s.end > a.window ? s.end - a.window : 0;
   s.base = s.begin & ~(kKvGroup - 1);
-  const int n = (s.end - s.base + kGranule - 1) / kGranule;
-  s.granules = n > 1 ? n : 1;
+  const int n = (s.end - s.base + kTile - 1) / kTile;
+  s.tiles = n > 1 ? n : 1;
   return s;
 }
 
@@ -120,23 +123,31 @@ __device__ __forceinline__ void load_side(const uint8_t* p, int lane, uint32_t* 
 }
 
 template <int FMT, int DB>
-__device__ __forceinline__ void load_tile(const KvCache& c, const int (&group)[2], int lane, Tile<FMT, DB>& t) {
+__device__ __forceinline__ void load_k(const KvCache& c, const int (&group)[2], int lane, Tile<FMT, DB>& t) {
   using L = KvLayout<FMT, DB>;
 #pragma unroll
   for (int a = 0; a < 2; ++a) {
-    const uint8_t* codes = c.codes + (int64_t)group[a] * L::kCodeBytes;
-    load_side<FMT, DB>(codes, lane, t.k[a]);
-    load_side<FMT, DB>(codes + L::kSideBytes, lane, t.v[a]);
-    if constexpr (FMT == kKvE4m3) {
-      const uint8_t* s = c.scales + (int64_t)group[a] * L::kScaleBytes;
-      t.ks[a] = s[lane & 15];
-      t.vs[a][0] = *reinterpret_cast<const uint32_t*>(s + 16 + 4 * (lane >> 4));
-    } else if constexpr (FMT == kKvNvfp4) {
-      const uint8_t* s = c.scales + (int64_t)group[a] * L::kScaleBytes;
+    load_side<FMT, DB>(c.codes + (int64_t)group[a] * L::kCodeBytes, lane, t.k[a]);
+    const uint8_t* s = c.scales + (int64_t)group[a] * L::kScaleBytes;
+    if constexpr (FMT == kKvE4m3) t.ks[a] = s[lane & 15];
+    else if constexpr (FMT == kKvNvfp4) {
       if constexpr (L::kKScaleLane == 1) t.ks[a] = s[lane];
       else if constexpr (L::kKScaleLane == 2) t.ks[a] = *reinterpret_cast<const uint16_t*>(s + 2 * lane);
       else t.ks[a] = *reinterpret_cast<const uint32_t*>(s + 4 * lane);
-      const uint32_t* vs = reinterpret_cast<const uint32_t*>(s + L::kKScaleBytes) + (lane >> 4) * (4 * DB);
+    }
+  }
+}
+
+template <int FMT, int DB>
+__device__ __forceinline__ void load_v(const KvCache& c, const int (&group)[2], int lane, Tile<FMT, DB>& t) {
+  using L = KvLayout<FMT, DB>;
+#pragma unroll
+  for (int a = 0; a < 2; ++a) {
+    load_side<FMT, DB>(c.codes + (int64_t)group[a] * L::kCodeBytes + L::kSideBytes, lane, t.v[a]);
+    const uint8_t* s = c.scales + (int64_t)group[a] * L::kScaleBytes + L::kKScaleBytes;
+    if constexpr (FMT == kKvE4m3) t.vs[a][0] = *reinterpret_cast<const uint32_t*>(s + 4 * (lane >> 4));
+    else if constexpr (FMT == kKvNvfp4) {
+      const uint32_t* vs = reinterpret_cast<const uint32_t*>(s) + (lane >> 4) * (4 * DB);
 #pragma unroll
       for (int u = 0; u < Tile<FMT, DB>::kVScales; ++u) t.vs[a][u] = vs[(L::kW * (lane & 15) + 4 * u) / 16];
     }
@@ -268,60 +279,49 @@ __device__ __forceinline__ void write_out(const AttnParams& a, int b, int qh, in
   if (d == 0 && a.lse) a.lse[(int64_t)b * a.q_heads + qh] = some ? (ref + __builtin_amdgcn_logf(l)) * kLn2 : kNegInf;
 }
 
-// Joins the partial sums that workgroups wfirst .. wlast left of a unit.  The
-// parts are cut into runs over the threads that its values leave over; each
-// thread adds its run in workgroup order, eight parts a round trip, under
-// weights formed from the references and sums that were read first; the runs are
-// then added in order through LDS.  `lds` is the kernel's staging space.
-template <int DP>
+// Adds (m, l, v) to running sums under the larger reference.
+template <int N>
+__device__ __forceinline__ void add_part(float& top, float& sum, f32x4 (&acc)[N], float m, float l, const f32x4 (&v)[N]) {
+  const float next = fmaxf(top, m);
+  const float fo = top == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(top - next);
+  const float fi = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m - next);
+  sum = sum * fo + l * fi;
+#pragma unroll
+  for (int u = 0; u < N; ++u) acc[u] = acc[u] * fo + v[u] * fi;
+  top = next;
+}
+
+// Joins the partial sums that workgroups wfirst .. wlast left of a unit.  The parts
+// are cut into runs over the threads that its values leave over; each thread adds
+// its run in workgroup order, kBatch parts a round trip to memory; the runs are
+// then added in order through LDS (6 floats a thread).
+template <int DP, int kThreads>
 __device__ __forceinline__ void join_parts(const AttnParams& a, int wfirst, int wlast, int rows, int b, int q0, float* lds) {
-  constexpr int kChunk = 64;                       // parts whose references and sums LDS holds at once
-  constexpr int kBatch = 8;                        // parts a round trip
+  constexpr int kBatch = 8;
   constexpr int kQuads = DP / 4;
-  float (*ml)[kRows][2] = reinterpret_cast<float (*)[kRows][2]>(lds);   // [kChunk][kRows][2]
   const int parts = wlast - wfirst + 1, items = rows * kQuads;
-  const int runs = items >= kThreads ? 1 : kThreads / items;
+  const int runs = min(items >= kThreads ? 1 : kThreads / items, parts);
   const __amdgpu_buffer_rsrc_t buf = part_buffer(a);
-  const auto row_of = [&](int part, int r) { return part_offset<DP>(a, wfirst + part, part == 0 ? 1 : 0, r); };
   for (int e0 = 0; e0 < items; e0 += kThreads) {   // more than one round: runs == 1
     const int e = e0 + (int)threadIdx.x, run = e / items, item = runs > 1 ? e - run * items : e;
     const bool live = runs > 1 ? run < runs : e < items;
     const int r = live ? item / kQuads : 0, d = live ? 4 * (item - r * kQuads) : 0;
+    const int p0 = !live ? 0 : runs > 1 ? parts * run / runs : 0, p1 = !live ? 0 : runs > 1 ? parts * (run + 1) / runs : parts;
     float top = kNegInf, l = 0.0f;
-    f32x4 acc{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int c0 = 0; c0 < parts; c0 += kChunk) {
-      const int n = min(kChunk, parts - c0);
-      __syncthreads();
-      for (int i = threadIdx.x; i < n * rows; i += kThreads) {
-        const int part = i / rows, rr = i - part * rows;
-        const f32x4 v = load_part(buf, row_of(c0 + part, rr));
-        ml[part][rr][0] = v[0];
-        ml[part][rr][1] = v[1];
-      }
-      __syncthreads();
-      if (!live) continue;
-      const int mine = runs > 1 ? run : 0;
-      const int p0 = n * mine / runs, p1 = n * (mine + 1) / runs;
-      if (p0 >= p1) continue;
-      float next = top;
-      for (int i = p0; i < p1; ++i) next = fmaxf(next, ml[i][r][0]);
-      const float fo = top == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(top - next);
-      l *= fo;
-      acc *= fo;
-      top = next;
-      for (int i = p0; i < p1; i += kBatch) {
-        f32x4 v[kBatch];
+    f32x4 acc[1] = {{0.0f, 0.0f, 0.0f, 0.0f}};
+    for (int i = p0; i < p1; i += kBatch) {
+      f32x4 ml[kBatch], v[kBatch][1];
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) v[j] = load_part(buf, row_of(c0 + min(i + j, p1 - 1), r) + (4 + d) * 4);
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-          if (i + j >= p1) break;
-          const float m = ml[i + j][r][0];
-          const float f = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m - top);
-          l += f * ml[i + j][r][1];
-          acc += v[j] * f;
+      for (int j = 0; j < kBatch; ++j) {
+        if (i + j < p1) {
+          const int from = part_offset<DP>(a, wfirst + i + j, i + j == 0 ? 1 : 0, r);
+          ml[j] = load_part(buf, from);
+          v[j][0] = load_part(buf, from + (4 + d) * 4);
         }
       }
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+        if (i + j < p1) add_part<1>(top, l, acc, ml[j][0], ml[j][1], v[j]);
     }
     if (runs > 1) {
       float* mine = lds + (run * items + item) * 6;
@@ -330,98 +330,155 @@ __device__ __forceinline__ void join_parts(const AttnParams& a, int wfirst, int 
         mine[0] = top;
         mine[1] = l;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) mine[2 + j] = acc[j];
+        for (int j = 0; j < 4; ++j) mine[2 + j] = acc[0][j];
       }
       __syncthreads();
       if (live && run == 0) {
         for (int i = 1; i < runs; ++i) {
           const float* other = lds + (i * items + item) * 6;
-          const float m = other[0], next = fmaxf(top, m);
-          const float fo = top == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(top - next);
-          const float fi = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m - next);
-          l = l * fo + other[1] * fi;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[j] = acc[j] * fo + other[2 + j] * fi;
-          top = next;
+          const f32x4 v[1] = {{other[2], other[3], other[4], other[5]}};
+          add_part<1>(top, l, acc, other[0], other[1], v);
         }
       }
     }
-    if (live && (runs == 1 || run == 0)) write_out(a, b, q0 + r, d, top, l, acc);
+    if (live && (runs == 1 || run == 0)) write_out(a, b, q0 + r, d, top, l, acc[0]);
   }
 }
 
+// Wavefronts a SIMD that the registers leave room for; a workgroup fills a CU.
+constexpr int waves_per_simd(int fmt, int db) {
+  return fmt == kKvBf16 ? (db == 1 ? 4 : db == 4 ? 1 : 2) : db == 1 ? 4 : db == 2 ? 3 : 2;
+}
+
+// The line cut into n runs of nearly equal length, the first `more` one longer.
+struct Cut {
+  int n, each, more;
+};
+__device__ __forceinline__ Cut cut_of(int length, int n) {
+  const int each = (int)((unsigned)length / (unsigned)n);
+  return Cut{n, each, length - each * n};
+}
+__device__ __forceinline__ int run_start(const Cut& c, int i) { return c.each * i + min(i, c.more); }
+__device__ __forceinline__ int run_of(const Cut& c, int place) {
+  const int longer = c.more * (c.each + 1);
+  return place < longer ? (int)((unsigned)place / (unsigned)(c.each + 1))
+                        : c.more + (int)((unsigned)(place - longer) / (unsigned)max(c.each, 1));
+}
+
+// A unit, as much of it as joins need: places [u0, u1) of its tiles, and where its
+// rows go.
+struct Unit {
+  int u0, u1;
+  int b, q0, rows;
+};
+
+// Inclusive sum over the lanes below: within each row of sixteen by shifts, then
+// the rows' last lanes carried into the rows after them.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int add_lanes(int v) {
+  return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xf, true);
+}
+__device__ __forceinline__ int lane_scan(int v) {
+  v = add_lanes<0x111, 0xf>(v);  // row_shr:1, 2, 4, 8
+  v = add_lanes<0x112, 0xf>(v);
+  v = add_lanes<0x114, 0xf>(v);
+  v = add_lanes<0x118, 0xf>(v);
+  v = add_lanes<0x142, 0xa>(v);  // row_bcast:15 into rows 1 and 3
+  return add_lanes<0x143, 0xc>(v);  // row_bcast:31 into rows 2 and 3
+}
+
+// One workgroup's LDS.
+template <int DP, int WAVES>
+struct Staging {
+  float ml[WAVES][kRows][2];                                        // reference and sum
+  float o[WAVES][kRows][DP + 4] __attribute__((aligned(16)));
+  Unit first, last;          // the units cut by the share's two ends
+  int has_first, has_last, join_first, join_last;
+};
+
 template <int FMT, int DB>
-__global__ __launch_bounds__(kThreads) void attn_kernel(const AttnParams a) {
+__global__ __launch_bounds__(256 * waves_per_simd(FMT, DB), (waves_per_simd(FMT, DB))) void attn_kernel(const AttnParams a) {
   using L = KvLayout<FMT, DB>;
-  constexpr int kDp = 64 * DB, kE = L::kE, kW = L::kW, kSteps = kE / 8;
-  constexpr int kOStride = kDp + 4;
-  __shared__ float s_ml[kWaves][kRows][2];
-  __shared__ __attribute__((aligned(16))) float s_o[kWaves][kRows][kOStride];
-  __shared__ int64_t s_scan[kWaves];
-  __shared__ int64_t s_start[3];  // batch row, granules before it, all granules
+  constexpr int kWaves = 4 * waves_per_simd(FMT, DB), kThreads = 64 * kWaves;
+  constexpr int kDp = 64 * DB, kE = L::kE, kW = L::kW, kSteps = kE / 8, kQuads = kE / 4;
+  __shared__ Staging<kDp, kWaves> lds;
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int qn = lane & 15, h = lane >> 4;
+  const int qn = lane & 15, h = lane >> 4, d0 = kE * h;
   const int units_per_row = a.cache.heads * a.row_tiles;
 
-  // Where this workgroup's share of all granules starts: a scan over the rows'
-  // granule counts, each thread a run of rows.
-  const int per = (a.batch + kThreads - 1) / kThreads;
-  const int b0 = min(tid * per, a.batch), b1 = min(b0 + per, a.batch);
-  int64_t mine = 0;
-  for (int b = b0; b < b1; ++b) mine += (int64_t)span_of(a, a.lens[b]).granules * units_per_row;
-  int64_t upto = mine;   // inclusive: lanes of the wavefront, then the wavefronts before
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const int64_t x = __shfl_up(upto, off);
-    upto += lane >= off ? x : 0;
-  }
-  if (lane == 63) s_scan[wave] = upto;
+  // The line's length, and each lane's stretch of it: `per` rows of the batch.
+  const auto row_places = [&](int row) {
+    return row < a.batch ? (span_of(a, a.lens[row]).tiles + kLead) * units_per_row : 0;
+  };
+  const int per = (a.batch + 63) / 64;
+  int mine = 0;
+#pragma unroll 4
+  for (int i = 0; i < per; ++i) mine += row_places(lane * per + i);
+  const int upto = lane_scan(mine);
+  const int total = __builtin_amdgcn_readlane(upto, 63);
+  const int w = blockIdx.x;
+  const Cut shares = cut_of(total, min((int)gridDim.x, max(total / kShare, 1)));
+  if (w >= shares.n) return;
+  if (tid == 0) lds.has_first = lds.has_last = lds.join_first = lds.join_last = 0;
   __syncthreads();
-  int64_t total = 0;
-#pragma unroll
-  for (int i = 0; i < kWaves; ++i) {
-    upto += i < wave ? s_scan[i] : 0;
-    total += s_scan[i];
-  }
-  const int64_t nwg = min((int64_t)gridDim.x, total);
-  const int64_t w = blockIdx.x;
-  if (w >= nwg) return;
-  const int64_t g0 = total * w / nwg, g1 = total * (w + 1) / nwg;
-  if (upto - mine <= g0 && g0 < upto) {
-    int64_t before = upto - mine;
-    int b = b0;
-    for (; b < b1; ++b) {
-      const int64_t n = (int64_t)span_of(a, a.lens[b]).granules * units_per_row;
-      if (g0 < before + n) break;
-      before += n;
+  const int s0 = run_start(shares, w), s1 = run_start(shares, w + 1);  // the workgroup's share
+  const Cut runs = cut_of(s1 - s0, kWaves);
+  const auto run_at = [&](int i) { return s0 + run_start(runs, i); };
+  const int g0 = run_at(wave), g1 = run_at(wave + 1);
+  // The batch row where this wavefront's run starts, and where that row starts:
+  // the lane whose rows hold place g0, then the row among them.
+  int b = 0, row_start = 0;
+  if (g0 < g1) {
+    const int in = __builtin_ctzll(__ballot(upto > g0));
+    b = in * per;
+    row_start = __builtin_amdgcn_readlane(upto - mine, in);
+    for (int i = 0; per > 1; i += 64) {
+      const int places = i + lane < per ? row_places(b + lane) : 0;
+      const int sum = lane_scan(places);
+      const uint64_t past = __ballot(row_start + sum > g0);
+      if (past) {
+        const int at = __builtin_ctzll(past);
+        b += at;
+        row_start += __builtin_amdgcn_readlane(sum - places, at);
+        break;
+      }
+      b += 64;
+      row_start += __builtin_amdgcn_readlane(sum, 63);
     }
-    s_start[0] = b;
-    s_start[1] = before;
   }
-  __syncthreads();
-  int b = (int)s_start[0];
-  int64_t row_start = s_start[1];
 
-  for (int64_t g = g0; g < g1;) {
+  // What is left in registers at the end: the beginning of a unit that goes on.
+  f32x4 o[kW];
+  float ref = kNegInf, sum = 0.0f;
+  Unit tail{0, 0, 0, 0, 0};
+  // o[j][i] is d = W (4h + i) + j of query q: the lane's quad u is d0 + 4u.
+  const auto quad = [&](int u) {
+    const int i = 4 * u / kW, j = 4 * u % kW;
+    return f32x4{o[j][i], o[j + 1][i], o[j + 2][i], o[j + 3][i]};
+  };
+
+  for (int g = g0; g < g1;) {
     const Span sp = span_of(a, a.lens[b]);
-    const int64_t row_end = row_start + (int64_t)sp.granules * units_per_row;
+    const int places = sp.tiles + kLead, row_end = row_start + places * units_per_row;
     if (g >= row_end) {
       row_start = row_end;
       ++b;
       continue;
     }
-    const int unit = (int)((g - row_start) / sp.granules);
-    const int64_t u0 = row_start + (int64_t)unit * sp.granules, u1 = u0 + sp.granules;
-    const int64_t stop = min(u1, g1);
+    const int unit = (int)((unsigned)(g - row_start) / (unsigned)places);
+    const int u0 = row_start + unit * places + kLead, u1 = u0 + sp.tiles;
+    g = max(g, u0);
+    const int stop = min(u1, g1);
+    if (g >= stop) break;                       // the run ends before the unit's first tile
     const int head = unit / a.row_tiles, rt = unit - head * a.row_tiles;
-    const int rows = min(a.group - rt * kRows, kRows);
-    const int first = (int)(g - u0), count = (int)(stop - g);
+    const int rows = min(a.group - rt * kRows, kRows), q0 = head * a.group + rt * kRows;
+    const int first = g - u0, count = stop - g;
 
     // Queries: lane (q, h) holds values E h .. E h + E - 1 of row q.
     uint32_t qv[kE / 2];
     const int d_here = a.cache.head_dim - kE * h;  // values of this lane inside the head
-    const uint16_t* qp = a.q + (int64_t)b * a.ldq + (int64_t)(head * a.group + rt * kRows + qn) * a.cache.head_dim + kE * h;
+    const uint16_t* qp = a.q + (int64_t)b * a.ldq + (int64_t)(q0 + qn) * a.cache.head_dim + kE * h;
 #pragma unroll
     for (int i = 0; i < kE / 8; ++i) {
       u32x4 x{0u, 0u, 0u, 0u};
@@ -429,6 +486,42 @@ __global__ __launch_bounds__(kThreads) void attn_kernel(const AttnParams a) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) qv[4 * i + j] = x[j];
     }
+    // Page lookups: lane j holds the group of step it + j / 2, half j & 1, for 32
+    // steps from the last multiple of 32; -1: none there.
+    int looked_up = -1;
+    const auto look_up = [&](int it, int (&group)[2]) {
+      if ((it & 31) == 0) {
+        const int tok = sp.base + (first + it + (lane >> 1)) * kTile + (lane & 1) * kKvGroup;
+        looked_up = -1;
+        if (it + (lane >> 1) < count && tok < sp.end) {
+          const int tg = tok / kKvGroup, pg = tg / a.cache.gpp;
+          const int page = a.table[(int64_t)b * a.table_width + pg];
+          if (page >= 0 && page < a.cache.pages)
+            looked_up = (page * a.cache.heads + head) * a.cache.gpp + (tg - pg * a.cache.gpp);
+        }
+      }
+      group[0] = __builtin_amdgcn_readlane(looked_up, 2 * (it & 31));
+      group[1] = __builtin_amdgcn_readlane(looked_up, 2 * (it & 31) + 1);
+    };
+    // What to load for a step: a half that is not there reads the pool's first
+    // group, which every wavefront finds in the cache, and is masked.
+    const auto to_load = [](const int (&group)[2], int (&from)[2]) {
+      from[0] = max(group[0], 0);
+      from[1] = max(group[1], 0);
+    };
+
+    // K of the next step is loaded once this step's scores are formed, V of the
+    // next once this step's V is in its operands: one tile of registers, and
+    // loads in flight all the time.  The last step loads its own tile again.
+    Tile<FMT, DB> t;
+    int group[2], from[2];
+    look_up(0, group);
+    to_load(group, from);
+    // (In the loop's own order, so that its waits count the same loads on entry.)
+    load_k<FMT, DB>(a.cache, from, lane, t);
+    __builtin_amdgcn_sched_barrier(0);
+    load_v<FMT, DB>(a.cache, from, lane, t);
+    __builtin_amdgcn_sched_barrier(0);
     float score_scale = a.scale * kLog2e * a.cache.k_scale;
     if constexpr (FMT == kKvNvfp4) {
       // bf16 -> f16: a power of two per row puts its largest magnitude at
@@ -449,35 +542,18 @@ __global__ __launch_bounds__(kThreads) void attn_kernel(const AttnParams a) {
       score_scale *= up;
     }
 
-    f32x4 o[kW];
 #pragma unroll
     for (int i = 0; i < kW; ++i) o[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    float ref = kNegInf, shift = -1e30f, sum = 0.0f;
+    ref = kNegInf;
+    sum = 0.0f;
+    float shift = -1e30f;
 
-    const int tiles = count;
-    int pages = -1;
-    for (int it = 0; it < tiles; ++it) {
-      // Lane j looks up the group of step it + j / 2, half j & 1, for 32 steps ahead.
-      if ((it & 31) == 0) {
-        const int tok = sp.base + ((first + it + (lane >> 1)) * kWaves + wave) * kTile + (lane & 1) * kKvGroup;
-        pages = -1;
-        if (it + (lane >> 1) < tiles && tok < sp.end) {
-          const int tg = tok / kKvGroup, pg = tg / a.cache.gpp;
-          const int page = a.table[(int64_t)b * a.table_width + pg];
-          if (page >= 0 && page < a.cache.pages) pages = (page * a.cache.heads + head) * a.cache.gpp + (tg - pg * a.cache.gpp);
-        }
-      }
-      const int tok0 = sp.base + ((first + it) * kWaves + wave) * kTile;
-      int group[2];
-      group[0] = __builtin_amdgcn_readlane(pages, 2 * (it & 31));
-      group[1] = __builtin_amdgcn_readlane(pages, 2 * (it & 31) + 1);
+    for (int it = 0; it < count; ++it) {
+      const int tok0 = sp.base + (first + it) * kTile;
       const bool has0 = group[0] >= 0, has1 = group[1] >= 0;
-      if (!has0 && !has1) continue;
       const bool whole = has0 && has1 && tok0 >= sp.begin && tok0 + kTile <= sp.end;
-      if (!has0) group[0] = group[1];
-      if (!has1) group[1] = group[0];
-      Tile<FMT, DB> t;
-      load_tile<FMT, DB>(a.cache, group, lane, t);
+      if (it + 1 < count) look_up(it + 1, group);
+      to_load(group, from);
       uint32_t okbits = 0xffu;
       if (!whole) {
         okbits = 0;
@@ -486,7 +562,6 @@ __global__ __launch_bounds__(kThreads) void attn_kernel(const AttnParams a) {
           const int tok = tok0 + (i / 4) * kKvGroup + 4 * h + i % 4;
           okbits |= ((i / 4 ? has1 : has0) && tok >= sp.begin && tok < sp.end) ? 1u << i : 0u;
         }
-        clear_masked<FMT, DB>(t, okbits);
       }
 
       // Scores.
@@ -503,6 +578,7 @@ __global__ __launch_bounds__(kThreads) void attn_kernel(const AttnParams a) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[4 * half + i] = acc[i];
       }
+      load_k<FMT, DB>(a.cache, from, lane, t);
       if (!whole) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = (okbits >> i) & 1u ? x[i] : kNegInf;
@@ -544,78 +620,147 @@ __global__ __launch_bounds__(kThreads) void attn_kernel(const AttnParams a) {
 
       // O^T += V^T P^T: step j takes d = W r + j, its eight tokens gathered by
       // byte permutes from the tokens' pairs.
+      if (!whole) clear_masked<FMT, DB>(t, okbits);
       uint32_t vt[8][2 * DB];
 #pragma unroll
       for (int i = 0; i < 8; ++i) v_token<FMT, DB>(t, i / 4, i % 4, vt[i]);
+      uint32_t op[kW][4];
 #pragma unroll
-      for (int j = 0; j < kW; ++j) {
-        uint32_t op[4];
+      for (int j = 0; j < kW; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          op[i] = __builtin_amdgcn_perm(vt[2 * i + 1][j / 2], vt[2 * i][j / 2], j % 2 ? 0x07060302u : 0x05040100u);
-        o[j] = mma<FMT>(op, hi, o[j]);
-        o[j] = mma<FMT>(op, lo, o[j]);
+          op[j][i] = __builtin_amdgcn_perm(vt[2 * i + 1][j / 2], vt[2 * i][j / 2], j % 2 ? 0x07060302u : 0x05040100u);
+      load_v<FMT, DB>(a.cache, from, lane, t);
+#pragma unroll
+      for (int j = 0; j < kW; ++j) {
+        o[j] = mma<FMT>(op[j], hi, o[j]);
+        o[j] = mma<FMT>(op[j], lo, o[j]);
       }
     }
 
-    // Join the four wavefronts.  o[j][i] is d = W (4h + i) + j of query q.
     sum += lane_xor(sum, 16);
     sum += lane_xor(sum, 32);
-    if (h == 0) {
-      s_ml[wave][qn][0] = ref;
-      s_ml[wave][qn][1] = sum;
-    }
-    if (qn < rows) {
+    if (u0 < g0) {
+      // The end, or a stretch, of a unit that an earlier wavefront began.
+      if (qn < rows) {
+        if (h == 0) {
+          lds.ml[wave][qn][0] = ref;
+          lds.ml[wave][qn][1] = sum;
+        }
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < kW; ++j) s_o[wave][qn][kW * (4 * h + i) + j] = o[j][i];
-    }
-    __syncthreads();
-    const int wfirst = (int)(((u0 + 1) * nwg - 1) / total), wlast = (int)((u1 * nwg - 1) / total);
-    const bool cut = wfirst != wlast;
-    const __amdgpu_buffer_rsrc_t buf = part_buffer(a);
-    for (int e = tid; e < rows * (kDp / 4); e += kThreads) {
-      const int r = e / (kDp / 4), d = 4 * (e - r * (kDp / 4));
-      float top = kNegInf;
-#pragma unroll
-      for (int i = 0; i < kWaves; ++i) top = fmaxf(top, s_ml[i][r][0]);
-      float l = 0.0f;
-      f32x4 acc{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int i = 0; i < kWaves; ++i) {
-        const float m = s_ml[i][r][0];
-        const float f = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m - top);
-        l += f * s_ml[i][r][1];
-        const f32x4 v = *reinterpret_cast<const f32x4*>(&s_o[i][r][d]);
-        acc += v * f;
+        for (int u = 0; u < kQuads; ++u) *reinterpret_cast<f32x4*>(&lds.o[wave][qn][d0 + 4 * u]) = quad(u);
       }
-      if (cut) {
-        const int to = part_offset<kDp>(a, (int)w, (int)w == wfirst ? 1 : 0, r);
-        if (d == 0) store_part(buf, to, f32x4{top, l, 0.0f, 0.0f});
-        store_part(buf, to + (4 + d) * 4, acc);
-      } else {
-        write_out(a, b, head * a.group + rt * kRows + r, d, top, l, acc);
+      if (u0 < s0 && lane == 0 && g == s0) {
+        lds.first = Unit{u0, u1, b, q0, rows};
+        lds.has_first = 1;
       }
+    } else if (u1 > g1) {
+      tail = Unit{u0, u1, b, q0, rows};
+    } else if (qn < rows) {
+#pragma unroll
+      for (int u = 0; u < kQuads; ++u) write_out(a, b, q0 + qn, d0 + 4 * u, ref, sum, quad(u));
     }
-    if (cut && arrive_last(a.counters + wfirst, (unsigned)(wlast - wfirst + 1)))
-      join_parts<kDp>(a, wfirst, wlast, rows, b, head * a.group + rt * kRows, &s_o[0][0][0]);
-    __syncthreads();  // the LDS of this unit is free again
     g = stop;
   }
+  __syncthreads();
+
+  // Adds what wavefronts from .. left in LDS of a unit that ends at place u1 (runs
+  // without a place are the share's last).
+  const auto add_from = [&](int from, int u1, f32x4 (&acc)[kQuads], float& top, float& l) {
+    const int end = u1 >= s1 ? (runs.each > 0 ? kWaves : runs.more) : run_of(runs, u1 - 1 - s0) + 1;
+    float next = top;
+    for (int i = from; i < end; ++i) next = fmaxf(next, lds.ml[i][qn][0]);
+    const float fo = top == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(top - next);
+    l *= fo;
+#pragma unroll
+    for (int u = 0; u < kQuads; ++u) acc[u] *= fo;
+#pragma unroll 2
+    for (int i = from; i < end; ++i) {
+      const float m = lds.ml[i][qn][0];
+      const float f = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m - next);
+      l += lds.ml[i][qn][1] * f;
+#pragma unroll
+      for (int u = 0; u < kQuads; ++u) acc[u] += *reinterpret_cast<const f32x4*>(&lds.o[i][qn][d0 + 4 * u]) * f;
+    }
+    top = next;
+  };
+  const __amdgpu_buffer_rsrc_t buf = part_buffer(a);
+  const auto store_sums = [&](int side, int rows, const f32x4 (&acc)[kQuads], float top, float l) {
+    if (qn >= rows) return;
+    const int to = part_offset<kDp>(a, w, side, qn);
+    if (h == 0) store_part(buf, to, f32x4{top, l, 0.0f, 0.0f});
+#pragma unroll
+    for (int u = 0; u < kQuads; ++u) store_part(buf, to + (4 + d0 + 4 * u) * 4, acc[u]);
+  };
+  f32x4 acc[kQuads];
+  if (tail.rows > 0) {
+#pragma unroll
+    for (int u = 0; u < kQuads; ++u) acc[u] = quad(u);
+    add_from(wave + 1, tail.u1, acc, ref, sum);
+    if (tail.u1 <= s1) {
+      if (qn < tail.rows) {
+#pragma unroll
+        for (int u = 0; u < kQuads; ++u) write_out(a, tail.b, tail.q0 + qn, d0 + 4 * u, ref, sum, acc[u]);
+      }
+    } else {
+      store_sums(1, tail.rows, acc, ref, sum);
+      if (lane == 0) {
+        lds.last = tail;
+        lds.has_last = 1;
+      }
+    }
+  }
+  if (wave == kWaves - 1 && lds.has_first) {  // (no wavefront after it: its own tail needed no joining)
+#pragma unroll
+    for (int u = 0; u < kQuads; ++u) acc[u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    float top = kNegInf, l = 0.0f;
+    add_from(0, lds.first.u1, acc, top, l);
+    store_sums(0, lds.first.rows, acc, top, l);
+  }
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);  // keep the stores of partial sums above the wait
+  __builtin_amdgcn_s_waitcnt(0);            // they have completed
+  __syncthreads();
+  if (!lds.has_first && !lds.has_last) return;
+  const int first0 = lds.has_first ? run_of(shares, lds.first.u0) : 0, first1 = lds.has_first ? run_of(shares, lds.first.u1 - 1) : 0;
+  const int last1 = lds.has_last ? run_of(shares, lds.last.u1 - 1) : 0;
+  if (tid == 0) {
+    // A unit's counter is that of the workgroup where it begins; the last to
+    // arrive finds all others counted and leaves it at zero.
+    unsigned p = 0, q = 0;
+    if (lds.has_first) p = __hip_atomic_fetch_add(a.counters + first0, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (lds.has_last) q = __hip_atomic_fetch_add(a.counters + w, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (lds.has_first && p == (unsigned)(first1 - first0)) {
+      __hip_atomic_store(a.counters + first0, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      lds.join_first = 1;
+    }
+    if (lds.has_last && q == (unsigned)(last1 - w)) {
+      __hip_atomic_store(a.counters + w, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      lds.join_last = 1;
+    }
+  }
+  __syncthreads();
+  const Unit uf = lds.first, ul = lds.last;
+  if (lds.join_first) join_parts<kDp, kThreads>(a, first0, first1, uf.rows, uf.b, uf.q0, &lds.o[0][0][0]);
+  if (lds.join_last) join_parts<kDp, kThreads>(a, w, last1, ul.rows, ul.b, ul.q0, &lds.o[0][0][0]);
 }
 
 int row_tiles_of(const AttnLaunch& a) { return (a.q_heads / a.cache.heads + kRows - 1) / kRows; }
 
-// Workgroups of a launch: what the GPU holds at once, or one a granule if the
-// longest possible lengths have fewer.
-int workgroups_of(const AttnLaunch& a) {
+int waves_of(const AttnLaunch& a) { return 4 * waves_per_simd(a.format, (a.cache.head_dim + 63) / 64); }
+
+// The places of the line, at the longest possible lengths.
+int64_t places_of(const AttnLaunch& a) {
   int64_t tokens = a.table_width * a.cache.page_size;
   if (a.window > 0 && a.window + kKvGroup < tokens) tokens = a.window + kKvGroup;
-  const int64_t granules = (tokens + kGranule - 1) / kGranule;
-  const int64_t all = a.batch * a.cache.heads * row_tiles_of(a) * (granules > 1 ? granules : 1);
-  const int64_t most = 512;
-  return (int)(all < most ? all : most);
+  const int64_t tiles = tokens > kTile ? (tokens + kTile - 1) / kTile : 1;
+  return a.batch * a.cache.heads * row_tiles_of(a) * (tiles + kLead);
+}
+
+// Workgroups of a launch: one a CU, or fewer if the longest possible lengths have
+// no work for them.
+int workgroups_of(const AttnLaunch& a) {
+  const int64_t all = places_of(a) / kShare;
+  return (int)(all < 1 ? 1 : all < kCus ? all : kCus);
 }
 
 int part_rows_of(const AttnLaunch& a) {
@@ -650,7 +795,7 @@ void attn_launch(const AttnLaunch& a, hipStream_t s) {
   p.part_rows = part_rows_of(a);
   p.part_bytes = (int32_t)part_bytes_of(a);
   p.scale = a.scale;
-  hipLaunchKernelGGL((attn_kernel<FMT, DB>), dim3((unsigned)workgroups_of(a)), dim3(kThreads), 0, s, p);
+  hipLaunchKernelGGL((attn_kernel<FMT, DB>), dim3((unsigned)workgroups_of(a)), dim3(64 * waves_of(a)), 0, s, p);
 }
 
 template <int FMT>
@@ -664,6 +809,8 @@ void attn_launch_db(const AttnLaunch& a, hipStream_t s) {
 }
 
 }  // namespace
+
+bool attn_fits(const AttnLaunch& a) { return places_of(a) < (int64_t(1) << 31); }
 
 size_t attn_workspace_bytes(const AttnLaunch& a) { return kAttnCounterBytes + part_bytes_of(a); }
 

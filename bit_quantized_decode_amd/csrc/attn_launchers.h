@@ -76,7 +76,9 @@ struct AttnLaunch {
   float* lse;              // nullptr: none
   void* ws;
 };
-constexpr size_t kAttnCounterBytes = 8192;  // one counter a workgroup
+constexpr size_t kAttnCounterBytes = 1024;  // one counter a workgroup
+// Whether the call's tiles can be numbered in 31 bits (at the longest lengths its table allows).
+bool attn_fits(const AttnLaunch& a);
 size_t attn_workspace_bytes(const AttnLaunch& a);
 hipError_t launch_attn_decode(const AttnLaunch& a, hipStream_t s);
 

@@ -192,7 +192,7 @@ int nvfp4_kv_read(const nvfp4_kv_cache* cache /* host */, const int64_t* slots, 
  * use; every call leaves them zero.  Calls that share one must not overlap.
  * batch == 0 is a no-op.
  */
-#define NVFP4_ATTN_COUNTER_BYTES 8192
+#define NVFP4_ATTN_COUNTER_BYTES 1024
 
 typedef struct nvfp4_attn_args {
   const nvfp4_kv_cache* cache;  /* host */

@@ -218,7 +218,7 @@ def attn(d, **over):
     (dict(out=None), B.NVFP4_ERR_NULL), (dict(seq_lens=None), B.NVFP4_ERR_NULL), (dict(page_table=None), B.NVFP4_ERR_NULL),
     (dict(q=A + 8), B.NVFP4_ERR_ALIGN), (dict(out=ODD), B.NVFP4_ERR_ALIGN), (dict(page_table=ODD), B.NVFP4_ERR_ALIGN),
     (dict(seq_lens=ODD), B.NVFP4_ERR_ALIGN), (dict(lse=ODD), B.NVFP4_ERR_ALIGN), (dict(workspace=None), B.NVFP4_ERR_WORKSPACE),
-    (dict(workspace_bytes=4096), B.NVFP4_ERR_WORKSPACE), (dict(workspace=A + 8), B.NVFP4_ERR_ALIGN),
+    (dict(workspace_bytes=1024), B.NVFP4_ERR_WORKSPACE), (dict(workspace=A + 8), B.NVFP4_ERR_ALIGN),
     (dict(batch=0, q=None, out=None, workspace=None), B.NVFP4_OK)])
 def test_attention_refusals(L, over, status):
     d = desc()
@@ -234,7 +234,7 @@ def test_attention_workspace(L):
     blank = dict(q=None, out=None, page_table=None, seq_lens=None, workspace=None, scale=0.0, ldq=0, ldo=0)
     assert L.nvfp4_attn_decode_workspace_bytes(ctypes.byref(attn(d, **blank)), ctypes.byref(n)) == 0
     need = n.value
-    assert need > 8192
+    assert need > 1024
     a = attn(d, workspace_bytes=need - 1)
     assert L.nvfp4_attn_decode(ctypes.byref(a), None) == B.NVFP4_ERR_WORKSPACE
     assert str(need).encode() in L.nvfp4_last_error()
