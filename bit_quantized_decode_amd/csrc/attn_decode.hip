@@ -16,8 +16,9 @@
 // Operands.  bf16 and E4M3 caches multiply as bf16 (every E4M3 value times its
 // power of two is a bf16 number), NVFP4 as f16 (E2M1 times E4M3 is an f16
 // number); the queries, bf16, are shifted into f16's range by a power of two
-// per row.  Probabilities enter as the sum of two 16-bit numbers, so they
-// carry 16 bits (bf16) or 22 (f16); everything else is fp32.
+// per row.  Probabilities enter as one f16 number (half a step: 2^-12, an eighth
+// of the output's own rounding) or as the sum of two bf16 numbers (2^-17; one
+// alone would add as much as the output's rounding); everything else is fp32.
 //
 // Work split.  The 32-token tiles of all units (sequence, kv head, row tile) form
 // one line, each unit led by kLead blank places for what starting it costs.
@@ -37,7 +38,7 @@ namespace {
 constexpr int kTile = 32;                  // tokens of a wavefront's step
 constexpr int kRows = 16;                  // query heads of a row tile
 constexpr int kCus = 256;
-constexpr int kLead = 2;                   // places before a unit's tiles
+constexpr int kLead = 3;                   // places before a unit's tiles
 constexpr int kShare = 6;                  // places of a workgroup's share, at least
 static_assert(kCus * 4 <= (int)kAttnCounterBytes, "one counter a workgroup");
 constexpr float kLog2e = 1.4426950408889634f;
@@ -111,7 +112,7 @@ __device__ __forceinline__ void load_side(const uint8_t* p, int lane, uint32_t* 
   using L = KvLayout<FMT, DB>;
 #pragma unroll
   for (int i = 0; i < L::kPlanes16; ++i) {
-    const u32x4 x = load16(p + i * 1024 + lane * 16);
+    const u32x4 x = load16_stream(p + i * 1024 + lane * 16);
 #pragma unroll
     for (int j = 0; j < 4; ++j) w[4 * i + j] = x[j];
   }
@@ -608,10 +609,7 @@ __global__ __launch_bounds__(256 * waves_per_simd(FMT, DB), (waves_per_simd(FMT,
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if constexpr (FMT == kKvNvfp4) {
-          const f16x2 u{(_Float16)p[2 * i], (_Float16)p[2 * i + 1]};
-          const f16x2 r{(_Float16)(p[2 * i] - (float)u[0]), (_Float16)(p[2 * i + 1] - (float)u[1])};
-          hi[i] = __builtin_bit_cast(uint32_t, u);
-          lo[i] = __builtin_bit_cast(uint32_t, r);
+          hi[i] = __builtin_bit_cast(uint32_t, f16x2{(_Float16)p[2 * i], (_Float16)p[2 * i + 1]});
         } else {
           hi[i] = pack_bf16x2(p[2 * i], p[2 * i + 1]);
           lo[i] = pack_bf16x2(p[2 * i] - bf16_lo(hi[i]), p[2 * i + 1] - bf16_hi(hi[i]));
@@ -634,7 +632,7 @@ __global__ __launch_bounds__(256 * waves_per_simd(FMT, DB), (waves_per_simd(FMT,
 #pragma unroll
       for (int j = 0; j < kW; ++j) {
         o[j] = mma<FMT>(op[j], hi, o[j]);
-        o[j] = mma<FMT>(op[j], lo, o[j]);
+        if constexpr (FMT != kKvNvfp4) o[j] = mma<FMT>(op[j], lo, o[j]);
       }
     }
 

@@ -91,12 +91,12 @@ def attend(q, k, v, scale):
     return p @ v / total, (m + np.log(total))[:, 0], p @ np.abs(v) / total, size
 
 
-def attend_bounds(size, n, d, o, pv, lse):
+def attend_bounds(size, n, d, o, pv, lse, fmt):
     """How far a bf16 output and an fp32 lse may be off.
 
     Scores: d exact products summed in fp32, then a product and a sum: (d + 4) half steps of sum |q k|.  A term
-    exp(s - m) is off by that, by four half steps of the exponential, and by 2^-17 from its two 16-bit parts; sums over n
-    tokens by n half steps.  A quotient of two such sums is off by twice as much of sum p |v|; then one rounding to bf16."""
+    exp(s - m) is off by that, by four half steps of the exponential, and by its rounding for the matrix cores (two bf16
+    parts, 2^-17; for format 2 one f16 number, 2^-12); sums over n tokens by n half steps.  A quotient of two such sums is off by twice as much of sum p |v|; then one rounding to bf16."""
     ds = (d + 4) * U24 * size
-    term = ds + 4 * U24 + 2.0 ** -17 + (n + 8) * U24
+    term = ds + 4 * U24 + (2.0 ** -12 if fmt == 2 else 2.0 ** -17) + (n + 8) * U24
     return 2.0 ** -8 * np.abs(o) + 2 * term[:, None] * pv + 1e-30, ds + (n + 8) * U24 + 4 * U24 * (1 + np.abs(np.where(np.isfinite(lse), lse, 0)))

@@ -59,7 +59,7 @@ class Batch:
             for h in range(self.hk):
                 rows = slice(h * g, (h + 1) * g)
                 o, l, pv, size = R.attend(self.q[b, rows].double().numpy(), self.k[start + j, h], self.v[start + j, h], scale)
-                bo, bl = R.attend_bounds(size, len(j), self.d, o, pv, l)
+                bo, bl = R.attend_bounds(size, len(j), self.d, o, pv, l, self.fmt)
                 empty = np.isneginf(l)
                 assert np.array_equal(np.isneginf(lse[b, rows]), empty), (what, b, h)
                 err = np.abs(out[b, rows] - o)

@@ -96,7 +96,7 @@ def test_decode_steps(fmt, users, graph):
             for h in range(hk):
                 rows = slice(h * hq // hk, (h + 1) * hq // hk)
                 o, lse, pv, sz = R.attend(q64[u, rows], ck[:, h], cv[:, h], d ** -0.5)
-                bound, _ = R.attend_bounds(sz, n, d, o, pv, lse)
+                bound, _ = R.attend_bounds(sz, n, d, o, pv, lse, fmt)
                 assert (np.abs(res["o"][u, rows].double().cpu().numpy() - o) <= bound).all(), (i, u, h)
         o_bits = res["o"].reshape(users, o_k).cpu().view(torch.int16).numpy().view(np.uint16)
         y_ref, s = oracle.gemm(wo[0], wo[1], st, o_bits)
