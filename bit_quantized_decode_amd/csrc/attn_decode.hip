@@ -22,8 +22,9 @@
 //
 // Work split.  The 32-token tiles of all units (sequence, kv head, row tile) form
 // one line, each unit led by kLead blank places for what starting it costs.
-// The line is cut evenly over the workgroups (one a CU) and each share over the
-// wavefronts, whatever the lengths are.  A wavefront walks its run of the line
+// The line is cut evenly over the workgroups (one a CU), cuts inside a short unit
+// moved to its nearer end, and each share over the wavefronts, whatever the
+// lengths are.  A wavefront walks its run of the line
 // by itself: it writes the units that lie inside its run, leaves the end of a
 // unit begun by an earlier wavefront in LDS, and keeps the beginning of one that
 // goes on in registers.  Once all are through, each beginning is joined with
@@ -39,7 +40,7 @@ constexpr int kTile = 32;                  // tokens of a wavefront's step
 constexpr int kRows = 16;                  // query heads of a row tile
 constexpr int kCus = 256;
 constexpr int kLead = 3;                   // places before a unit's tiles
-constexpr int kShare = 6;                  // places of a workgroup's share, at least
+constexpr int kShare = 6;                  // places of a workgroup's share, at least, if units are cut
 static_assert(kCus * 4 <= (int)kAttnCounterBytes, "one counter a workgroup");
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -409,45 +410,69 @@ __global__ __launch_bounds__(256 * waves_per_simd(FMT, DB), (waves_per_simd(FMT,
   const int units_per_row = a.cache.heads * a.row_tiles;
 
   // The line's length, and each lane's stretch of it: `per` rows of the batch.
-  const auto row_places = [&](int row) {
-    return row < a.batch ? (span_of(a, a.lens[row]).tiles + kLead) * units_per_row : 0;
+  const auto len_of = [&](int row) { return row < a.batch ? a.lens[row] : 0; };
+  const auto places_in = [&](int row, int len) {
+    return row < a.batch ? (span_of(a, len).tiles + kLead) * units_per_row : 0;
   };
   const int per = (a.batch + 63) / 64;
-  int mine = 0;
+  // A window of 64 rows from row `win` on, which starts at place `win_start`: the
+  // lanes' lengths, places and inclusive sums of places.
+  int win = 0, win_start = 0, win_len = 0, win_mine = 0, win_upto = 0;
+  const auto move_window = [&](int row, int start) {
+    win = row;
+    win_start = start;
+    win_len = len_of(row + lane);
+    win_mine = places_in(row + lane, win_len);
+    win_upto = lane_scan(win_mine);
+  };
+  int mine, upto;                           // of each lane's `per` rows
+  if (per == 1) {
+    move_window(0, 0);
+    mine = win_mine;
+    upto = win_upto;
+  } else {
+    mine = 0;
 #pragma unroll 4
-  for (int i = 0; i < per; ++i) mine += row_places(lane * per + i);
-  const int upto = lane_scan(mine);
+    for (int i = 0; i < per; ++i) mine += places_in(lane * per + i, len_of(lane * per + i));
+    upto = lane_scan(mine);
+  }
   const int total = __builtin_amdgcn_readlane(upto, 63);
   const int w = blockIdx.x;
-  const Cut shares = cut_of(total, min((int)gridDim.x, max(total / kShare, 1)));
+  const Cut shares = cut_of(total, min((int)gridDim.x, max(total / kShare, a.batch * units_per_row)));
   if (w >= shares.n) return;
-  if (tid == 0) lds.has_first = lds.has_last = lds.join_first = lds.join_last = 0;
-  __syncthreads();
-  const int s0 = run_start(shares, w), s1 = run_start(shares, w + 1);  // the workgroup's share
+  // The row that holds a place, where it starts and how long its units are; the
+  // window moves there if it is elsewhere.
+  struct Row {
+    int b, start, unit;
+  };
+  const auto row_at = [&](int place) {
+    if (place < win_start || place >= win_start + __builtin_amdgcn_readlane(win_upto, 63)) {
+      const int in = __builtin_ctzll(__ballot(upto > place));
+      move_window(in * per, __builtin_amdgcn_readlane(upto - mine, in));
+      while (place >= win_start + __builtin_amdgcn_readlane(win_upto, 63))  // (ends in the lane's own rows)
+        move_window(win + 64, win_start + __builtin_amdgcn_readlane(win_upto, 63));
+    }
+    const int at = __builtin_ctzll(__ballot(win_start + win_upto > place));
+    return Row{win + at, win_start + __builtin_amdgcn_readlane(win_upto - win_mine, at),
+               __builtin_amdgcn_readlane(win_mine, at) / units_per_row};
+  };
+  // An end of a share: moved to a unit's end if the unit is short.
+  const auto share_end = [&](int i) {
+    const int place = run_start(shares, i);
+    if (i == 0 || i == shares.n) return place;
+    const Row r = row_at(place);
+    const int into = (place - r.start) % r.unit;
+    return r.unit > kLead + 2 * kWaves ? place : 2 * into < r.unit ? place - into : place - into + r.unit;
+  };
+  const int s0 = share_end(w), s1 = share_end(w + 1);  // the workgroup's share
+  if (s0 >= s1) return;
   const Cut runs = cut_of(s1 - s0, kWaves);
   const auto run_at = [&](int i) { return s0 + run_start(runs, i); };
   const int g0 = run_at(wave), g1 = run_at(wave + 1);
-  // The batch row where this wavefront's run starts, and where that row starts:
-  // the lane whose rows hold place g0, then the row among them.
-  int b = 0, row_start = 0;
-  if (g0 < g1) {
-    const int in = __builtin_ctzll(__ballot(upto > g0));
-    b = in * per;
-    row_start = __builtin_amdgcn_readlane(upto - mine, in);
-    for (int i = 0; per > 1; i += 64) {
-      const int places = i + lane < per ? row_places(b + lane) : 0;
-      const int sum = lane_scan(places);
-      const uint64_t past = __ballot(row_start + sum > g0);
-      if (past) {
-        const int at = __builtin_ctzll(past);
-        b += at;
-        row_start += __builtin_amdgcn_readlane(sum - places, at);
-        break;
-      }
-      b += 64;
-      row_start += __builtin_amdgcn_readlane(sum, 63);
-    }
-  }
+  const Row r0 = row_at(min(g0, total - 1));
+  int b = r0.b, row_start = r0.start;
+  // (Set again, if at all, by this wavefront or after the next barrier.)
+  if (tid == 0) lds.has_first = lds.has_last = lds.join_first = lds.join_last = 0;
 
   // What is left in registers at the end: the beginning of a unit that goes on.
   f32x4 o[kW];
@@ -460,7 +485,8 @@ __global__ __launch_bounds__(256 * waves_per_simd(FMT, DB), (waves_per_simd(FMT,
   };
 
   for (int g = g0; g < g1;) {
-    const Span sp = span_of(a, a.lens[b]);
+    if (b - win >= 64) move_window(b, row_start);
+    const Span sp = span_of(a, __builtin_amdgcn_readlane(win_len, b - win));
     const int places = sp.tiles + kLead, row_end = row_start + places * units_per_row;
     if (g >= row_end) {
       row_start = row_end;
@@ -757,8 +783,9 @@ int64_t places_of(const AttnLaunch& a) {
 // Workgroups of a launch: one a CU, or fewer if the longest possible lengths have
 // no work for them.
 int workgroups_of(const AttnLaunch& a) {
-  const int64_t all = places_of(a) / kShare;
-  return (int)(all < 1 ? 1 : all < kCus ? all : kCus);
+  const int64_t shares = places_of(a) / kShare, units = a.batch * a.cache.heads * row_tiles_of(a);
+  const int64_t all = shares > units ? shares : units;
+  return (int)(all < kCus ? all : kCus);
 }
 
 int part_rows_of(const AttnLaunch& a) {
