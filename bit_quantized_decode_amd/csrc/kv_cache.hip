@@ -2,10 +2,18 @@
 // keys (and queries) turned on the way (nvfp4_kv_append), and reading them back
 // (nvfp4_kv_read).
 //
-// One lane takes one block of sixteen values of one token and head; the blocks of
-// a row sit in neighbouring lanes, so that a row is read in one piece and the
-// E4M3 format's row maximum is a few lane exchanges.  A wavefront takes the same
-// head of consecutive tokens: its writes then fill the layout's 16-token pieces.
+// One lane takes one block of sixteen values of one token, in each head of its
+// share; the blocks of a row sit in neighbouring lanes, so that a row is read in
+// one piece and the E4M3 format's row maximum is a few lane exchanges.  A
+// wavefront takes the same head of consecutive tokens: its writes then fill the
+// layout's 16-token pieces.  Sines and cosines are formed once per lane, for all
+// its heads.
+//
+// Bound by the bytes.  8192 tokens of 8 heads of 128, bf16 in: written as bf16 in
+// 15.9 us (67 MB read and written, 4.2 TB/s; 18.0 with ordinary stores, while E4M3
+// takes 10.8 with ordinary and 11.0 with non-temporal ones: hence by format), E4M3
+// 10.8 (4.7 TB/s), NVFP4 11.4 (3.8 TB/s; 18.6 with a division a value and codes by
+// comparison), keys turned on the way 12.2; read back in 15.1, 10.9 and 10.7 us.
 #include "attn_launchers.h"
 #include "rope_device.h"
 
@@ -31,11 +39,6 @@ __device__ __forceinline__ Place place_of(const KvCache& c, int64_t slot, int he
   p.group = ((int64_t)page * c.heads + head) * c.gpp + (tg - page * (uint32_t)c.gpp);
   return p;
 }
-
-template <int N>
-struct Words {
-  uint32_t w[N];
-};
 
 __device__ __forceinline__ float e4m3_of(uint32_t byte) { return __builtin_amdgcn_cvt_f32_fp8((int)byte, 0); }
 __device__ __forceinline__ float exp2_of_byte(uint32_t byte) { return __uint_as_float(byte << 23); }
@@ -65,14 +68,28 @@ __device__ __forceinline__ void encode16(const float (&v)[16], uint32_t amax, fl
   } else {
     const float q = __uint_as_float(amax) / (6.0f * st);
     uint32_t sb = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(fminf(q, 448.0f), 0.0f, 0, false) & 0xffu;
-    const float d = e4m3_of(sb) * st;
+    // Quotients |v| / d rounded as a division rounds them: with the correctly
+    // rounded reciprocal r, q0 = a r is within a unit of the quotient, and one
+    // step with the exact residual a - q0 d rounds it correctly (Markstein, "Computation
+    // of elementary functions on the IBM RISC System/6000 processor", 1990).  Beyond
+    // 8 d every code is the largest; the minimum keeps the steps finite.
+    const float d = e4m3_of(sb) * st, r = 1.0f / d, most = 8.0f * d;
     uint32_t p[2] = {0u, 0u};
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float a = fabsf(v[i] / d);
-      const uint32_t m = (uint32_t)(a > 0.25f) + (uint32_t)(a >= 0.75f) + (uint32_t)(a > 1.25f) + (uint32_t)(a >= 1.75f) +
-                         (uint32_t)(a > 2.5f) + (uint32_t)(a >= 3.5f) + (uint32_t)(a > 5.0f);
-      p[i / 8] |= (m | ((__float_as_uint(v[i]) >> 31) << 3)) << (4 * (i % 8));
+    for (int i = 0; i < 8; ++i) {
+      float q2[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float a = fminf(fabsf(v[2 * i + j]), most), q0 = a * r;
+        q2[j] = __builtin_copysignf(__builtin_fmaf(__builtin_fmaf(-q0, d, a), r, q0), v[2 * i + j]);
+      }
+      // Nearest E2M1, ties to even, +-6 beyond: the conversion's own rounding.
+      switch (i % 4) {
+        case 0: p[i / 4] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(p[i / 4], q2[0], q2[1], 1.0f, 0); break;
+        case 1: p[i / 4] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(p[i / 4], q2[0], q2[1], 1.0f, 1); break;
+        case 2: p[i / 4] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(p[i / 4], q2[0], q2[1], 1.0f, 2); break;
+        default: p[i / 4] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(p[i / 4], q2[0], q2[1], 1.0f, 3); break;
+      }
     }
     const bool some = sb != 0u && finite;
     w[0] = some ? p[0] : 0u;
@@ -81,11 +98,13 @@ __device__ __forceinline__ void encode16(const float (&v)[16], uint32_t amax, fl
   }
 }
 
-template <int BYTES>
+// STREAM: a non-temporal store.
+template <int BYTES, bool STREAM>
 __device__ __forceinline__ void store_bytes(uint8_t* p, const uint32_t* w, int shift) {
   if constexpr (BYTES == 2) *reinterpret_cast<uint16_t*>(p) = (uint16_t)(w[0] >> shift);
   else if constexpr (BYTES == 4) *reinterpret_cast<uint32_t*>(p) = w[0];
   else if constexpr (BYTES == 8) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+  else if constexpr (STREAM) __builtin_nontemporal_store(u32x4{w[0], w[1], w[2], w[3]}, reinterpret_cast<u32x4*>(p));
   else *reinterpret_cast<u32x4*>(p) = u32x4{w[0], w[1], w[2], w[3]};
 }
 template <int BYTES>
@@ -114,8 +133,10 @@ __device__ __forceinline__ void move_codes(uint8_t* codes, int64_t group, int t,
   constexpr int kRun = !VSIDE ? 16 : L::kW == 8 ? 8 : L::kW == 16 ? 16 : 4;
   constexpr int kRunBytes = kRun * L::kBits / 8;
   constexpr int kPiece = kRunBytes > 16 ? 16 : kRunBytes;
+  constexpr int kPerRun = kRunBytes / kPiece;
 #pragma unroll
-  for (int i = 0; i < 16 / kRun; ++i) {
+  for (int n = 0; n < 16 / kRun * kPerRun; ++n) {
+    const int i = n / kPerRun, j = n % kPerRun;
     const int d = 16 * b + kRun * i;
     int lane, byte;
     if (!VSIDE) {
@@ -127,14 +148,9 @@ __device__ __forceinline__ void move_codes(uint8_t* codes, int64_t group, int t,
       lane = 16 * (t / 4) + r;
       byte = ((t % 4) * L::kW + d - r * L::kW) * L::kBits / 8;
     }
-#pragma unroll
-    for (int j = 0; j < kRunBytes / kPiece; ++j) {
-      constexpr int kWordBits = 32;
-      const int bit = i * kRunBytes * 8 + j * kPiece * 8;
-      uint8_t* p = base + L::lane_byte(lane, byte + j * kPiece);
-      if (WRITE) store_bytes<kPiece>(p, &w[bit / kWordBits], bit % kWordBits);
-      else load_bytes<kPiece>(p, &w[bit / kWordBits], bit % kWordBits);
-    }
+    uint8_t* p = base + L::lane_byte(lane, byte + j * kPiece);
+    if (WRITE) store_bytes<kPiece, FMT == kKvBf16>(p, w + n * kPiece / 4, n * kPiece % 4 * 8);
+    else load_bytes<kPiece>(p, w + n * kPiece / 4, n * kPiece % 4 * 8);
   }
 }
 
@@ -167,68 +183,71 @@ __device__ __forceinline__ void write_block(const KvCache& c, const Place& p, in
   if (FMT == kKvNvfp4 || (FMT == kKvE4m3 && b == 0)) *scale_at<FMT, DB, VSIDE>(c.scales, p.group, p.t, b) = (uint8_t)scale;
 }
 
-// blockIdx.x: a run of tokens; blockIdx.y: a K head, a V head, or a query head.
+// blockIdx.x: a run of tokens; blockIdx.y: a chunk of the K, V or query heads.
 template <int FMT, int DB, bool BF16>
-__global__ __launch_bounds__(kThreads) void append_kernel(const KvAppendLaunch a) {
+__global__ __launch_bounds__(kThreads) void append_kernel(const KvAppendLaunch a, int heads_per) {
   constexpr int kLpr = lanes_per_row(DB), kRows = kThreads / kLpr, kStride = 64 * DB + 4;
   __shared__ __attribute__((aligned(16))) float s_row[kRows * kStride];
   const int row = threadIdx.x / kLpr, b = threadIdx.x % kLpr;
   const int64_t tok = (int64_t)blockIdx.x * kRows + row;
-  const int d_blocks = a.cache.head_dim / 16;
-  const int kind = blockIdx.y < a.cache.heads ? 0 : blockIdx.y < 2 * a.cache.heads ? 1 : 2;
-  const int head = blockIdx.y - kind * a.cache.heads;
+  const int kv_chunks = (a.cache.heads + heads_per - 1) / heads_per;
+  const int kind = blockIdx.y < kv_chunks ? 0 : blockIdx.y < 2 * kv_chunks ? 1 : 2;
+  const int h0 = (blockIdx.y - kind * kv_chunks) * heads_per;
+  const int h1 = min(h0 + heads_per, kind == 2 ? a.q_heads : a.cache.heads);
   const int64_t slot = tok < a.tokens ? a.slots[tok] : -1;
-  const Place p = place_of(a.cache, slot, kind == 2 ? 0 : head);
-  const bool live = p.valid && b < d_blocks;
-  float v[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = 0.0f;
-  if (kind == 1) {
-    if (live) {
-      const int64_t at = tok * a.ldv + (int64_t)head * a.cache.head_dim + 16 * b;
-      load8<BF16>(a.v, at, v);
-      load8<BF16>(a.v, at + 8, v + 8);
-    }
-    write_block<FMT, DB, true>(a.cache, p, b, v);
-    return;
-  }
+  Place p = place_of(a.cache, slot, kind == 2 ? 0 : h0);
+  const bool live = p.valid && 16 * b < a.cache.head_dim;
   RopeUnit r{16 * b, 16 * b + 8, false};
-  if (a.rope.freqs) r = rope_unit(b, a.rope.rot, a.rope.interleaved);
-  if (live) {
-    const void* src = kind == 0 ? a.k : a.q;
-    const int64_t at = tok * (kind == 0 ? a.ldk : a.ldq) + (int64_t)head * a.cache.head_dim;
-    load8<BF16>(src, at + r.first, v);
-    load8<BF16>(src, at + r.second, v + 8);
-    if (r.turned) {
-      float c[8], s[8];
-      rope_angles(a.rope.freqs, b, a.rope.pos[tok], a.rope.magnitude, a.rope.sign, c, s);
-      rope_turn(v, a.rope.interleaved, c, s);
-    }
+  float c[8], s[8];
+  if (kind != 1 && a.rope.freqs) {
+    r = rope_unit(b, a.rope.rot, a.rope.interleaved);
+    if (live && r.turned) rope_angles(a.rope.freqs, b, a.rope.pos[tok], a.rope.magnitude, a.rope.sign, c, s);
   }
-  if (kind == 2) {
+  const void* src = kind == 0 ? a.k : kind == 1 ? a.v : a.q;
+  int64_t at = tok * (kind == 0 ? a.ldk : kind == 1 ? a.ldv : a.ldq) + (int64_t)h0 * a.cache.head_dim;
+  int64_t to = tok * a.ldqo + (int64_t)h0 * a.cache.head_dim;
+  for (int h = h0; h < h1; ++h) {
+    float v[16];
     if (live) {
-      const int64_t at = tok * a.ldqo + (int64_t)head * a.cache.head_dim;
-      store8<true>(a.q_out, at + r.first, v);
-      store8<true>(a.q_out, at + r.second, v + 8);
-    }
-    return;
-  }
-  if (a.rope.freqs && !a.rope.interleaved) {  // units are not blocks: exchange through LDS
-    float* mine = s_row + row * kStride;
-    if (b < 4 * DB) {
+      load8<BF16>(src, at + r.first, v);
+      load8<BF16>(src, at + r.second, v + 8);
+    } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        mine[r.first + i] = v[i];
-        mine[r.second + i] = v[8 + i];
+      for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+    }
+    if (r.turned) rope_turn(v, a.rope.interleaved, c, s);
+    if (kind == 2) {
+      if (live) {
+        store8<true>(a.q_out, to + r.first, v);
+        store8<true>(a.q_out, to + r.second, v + 8);
       }
-    }
-    __syncthreads();
-    if (b < 4 * DB) {
+      to += a.cache.head_dim;
+    } else {
+      if (kind == 0 && a.rope.freqs && !a.rope.interleaved) {  // units are not blocks: exchange through LDS
+        float* mine = s_row + row * kStride;
+        if (b < 4 * DB) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = mine[16 * b + i];
+          for (int i = 0; i < 8; i += 4) {
+            *reinterpret_cast<f32x4*>(mine + r.first + i) = f32x4{v[i], v[i + 1], v[i + 2], v[i + 3]};
+            *reinterpret_cast<f32x4*>(mine + r.second + i) = f32x4{v[8 + i], v[9 + i], v[10 + i], v[11 + i]};
+          }
+        }
+        __syncthreads();
+        if (b < 4 * DB) {
+#pragma unroll
+          for (int i = 0; i < 16; i += 4) {
+            const f32x4 x = *reinterpret_cast<const f32x4*>(mine + 16 * b + i);
+            v[i] = x[0], v[i + 1] = x[1], v[i + 2] = x[2], v[i + 3] = x[3];
+          }
+        }
+        __syncthreads();
+      }
+      if (kind == 0) write_block<FMT, DB, false>(a.cache, p, b, v);
+      else write_block<FMT, DB, true>(a.cache, p, b, v);
+      p.group += a.cache.gpp;
     }
+    at += a.cache.head_dim;
   }
-  write_block<FMT, DB, false>(a.cache, p, b, v);
 }
 
 // ---- reading back -----------------------------------------------------------
@@ -292,12 +311,19 @@ __global__ __launch_bounds__(kThreads) void read_kernel(const KvReadLaunch a) {
   else read_block<FMT, DB, false, BF16>(a, p, tok, head, b);
 }
 
+// Heads of a workgroup's share: one while the rows do not fill the GPU, more
+// where they do (sines and addresses are then shared), four workgroups a CU kept.
 template <int FMT, int DB>
 void append_launch(const KvAppendLaunch& a, hipStream_t s) {
   constexpr int kRows = kThreads / lanes_per_row(DB);
-  const dim3 grid((unsigned)((a.tokens + kRows - 1) / kRows), (unsigned)(2 * a.cache.heads + (a.q ? a.q_heads : 0)));
-  if (a.bf16) hipLaunchKernelGGL((append_kernel<FMT, DB, true>), grid, dim3(kThreads), 0, s, a);
-  else hipLaunchKernelGGL((append_kernel<FMT, DB, false>), grid, dim3(kThreads), 0, s, a);
+  const int64_t runs = (a.tokens + kRows - 1) / kRows;
+  const int64_t heads = 2 * a.cache.heads + (a.q ? a.q_heads : 0);
+  const int64_t per = runs * heads / 1024;
+  const int heads_per = (int)(per < 1 ? 1 : per > 8 ? 8 : per);
+  const auto chunks = [&](int n) { return (n + heads_per - 1) / heads_per; };
+  const dim3 grid((unsigned)runs, (unsigned)(2 * chunks(a.cache.heads) + (a.q ? chunks(a.q_heads) : 0)));
+  if (a.bf16) hipLaunchKernelGGL((append_kernel<FMT, DB, true>), grid, dim3(kThreads), 0, s, a, heads_per);
+  else hipLaunchKernelGGL((append_kernel<FMT, DB, false>), grid, dim3(kThreads), 0, s, a, heads_per);
 }
 
 template <int FMT, int DB>

@@ -31,23 +31,25 @@ __device__ __forceinline__ void sincos_phase(uint32_t phase, float& s, float& c)
   c = ((quarter + 1u) & 2u) ? -b : b;
 }
 
-// Sixteen consecutive values at p (16-byte aligned) in fp32, or eight.
-template <bool BF16>
+// Eight consecutive values at element `off` of p (16-byte aligned), in fp32.
+// STREAM: read once, by a non-temporal load.
+template <bool BF16, bool STREAM = false>
 __device__ __forceinline__ void load8(const void* p, int64_t off, float* v) {
   if (BF16) {
-    const u32x4 a = load16(static_cast<const uint16_t*>(p) + off);
+    const uint16_t* q = static_cast<const uint16_t*>(p) + off;
+    const u32x4 a = STREAM ? load16_stream(q) : load16(q);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       v[2 * i] = bf16_lo(a[i]);
       v[2 * i + 1] = bf16_hi(a[i]);
     }
   } else {
-    const f32x4* q = reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + off);
-    const f32x4 a = q[0], b = q[1];
+    const float* q = static_cast<const float*>(p) + off;
+    const u32x4 a = STREAM ? load16_stream(q) : load16(q), b = STREAM ? load16_stream(q + 4) : load16(q + 4);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      v[i] = a[i];
-      v[4 + i] = b[i];
+      v[i] = __uint_as_float(a[i]);
+      v[4 + i] = __uint_as_float(b[i]);
     }
   }
 }
@@ -94,7 +96,9 @@ __device__ __forceinline__ void rope_angles(const uint64_t* __restrict__ freqs, 
   }
 }
 
-// Turns v[0..8) and v[8..16) in place.
+// Turns a unit's pairs in place.  (The empty statements differ, so that the
+// compiler does not merge the two layouts into one code with v indexed at run
+// time, which puts it into scratch memory.)
 __device__ __forceinline__ void rope_turn(float (&v)[16], bool interleaved, const float (&c)[8], const float (&s)[8]) {
   if (interleaved) {
 #pragma unroll
@@ -102,6 +106,7 @@ __device__ __forceinline__ void rope_turn(float (&v)[16], bool interleaved, cons
       const float a = v[2 * i], b = v[2 * i + 1];
       v[2 * i] = a * c[i] - b * s[i];
       v[2 * i + 1] = a * s[i] + b * c[i];
+      asm volatile("; interleaved pair");
     }
   } else {
 #pragma unroll
@@ -109,6 +114,7 @@ __device__ __forceinline__ void rope_turn(float (&v)[16], bool interleaved, cons
       const float a = v[i], b = v[8 + i];
       v[i] = a * c[i] - b * s[i];
       v[8 + i] = a * s[i] + b * c[i];
+      asm volatile("; pair of halves");
     }
   }
 }
