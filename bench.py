@@ -101,7 +101,8 @@ def parse():
                    help="rows to run; optional, not default: quantize (the NVFP4 quantiser over the layer), "
                         "decode_m2 .. decode_m8 (the layer at decode widths 2..8), head_b1 (the output head, batch 1), "
                         "moe_stream (the MoE layer with experts streamed from host memory), prefill_w4a4 (the prefill "
-                        "products as W4A4 on the FP4 matrix cores)")
+                        "products as W4A4 on the FP4 matrix cores), attn_b1 / attn_b32 (cache write and attention of one "
+                        "token for 1 user over 131072 tokens / 32 users over 8192, NVFP4 cache)")
     p.add_argument("--order", default="prefill,moe,decode_b32,gemv_1k,decode_b1",
                    help="row order within a step (the batch-1 GEMV last: see the note at the plan)")
     p.add_argument("--graphs", action="store_true", help="replay per-row HIP graphs instead of direct launches")
@@ -287,6 +288,38 @@ def main():
         hbytes = I.HEAD.n * I.HEAD.k * 9 // 16 + 2 * I.HEAD.k + 4 * I.HEAD.n
         extra_rows["head_b1"] = ([B.gemv_batched_prepared([(head_packed, I.HEAD.n, I.HEAD.k, I.TENSOR_SCALE, xh, yh)],
                                                           ws=ws_split)], 1, [yh], hbytes, 2.0 * I.HEAD.n * I.HEAD.k)
+
+    # ---- optional rows: the layer's attention side (40 query and 8 key-value
+    # heads of 128, as its QKV and O products have) for one token a user over an
+    # NVFP4 cache: keys and queries turned and the cache written, then attention.
+    # Two caches in turn, so that none is still in the MALL --------------------
+    for r, users, context in (("attn_b1", 1, 131072), ("attn_b32", 32, 8192)):
+        if r not in rows:
+            continue
+        hq, hk, hd, page = 40, 8, 128, 64
+        gen = torch.Generator(device=dev)
+        gen.manual_seed(4321)
+        pages = users * context // page
+        pt = torch.randperm(pages, generator=gen, device=dev).to(torch.int32).view(users, context // page)
+        kv = torch.randn((pages * page, 2 * hk, hd), generator=gen, device=dev).to(torch.bfloat16)
+        qkv = torch.randn((users, hq + 2 * hk, hd), generator=gen, device=dev).to(torch.bfloat16)
+        pos = torch.full((users,), context - 1, dtype=torch.int32, device=dev)
+        slots = pt[:, -1].long() * page + page - 1
+        lens = torch.full((users,), context, dtype=torch.int32, device=dev)
+        turns = B.rope_table(hd, base=1e6, device=dev)
+        q_rot = torch.empty((users, hq, hd), dtype=torch.bfloat16, device=dev)
+        o = torch.empty((users, hq, hd), dtype=torch.bfloat16, device=dev)
+        calls = []
+        for _ in range(2):
+            cache = B.KvCache(pages, page, hk, hd, B.NVFP4_KV_NVFP4, device=dev)
+            B.kv_append(cache, kv[:, :hk], kv[:, hk:], torch.arange(pages * page, device=dev))
+            write = B.kv_append_prepared(cache, qkv[:, hq:hq + hk], qkv[:, hq + hk:], slots, positions=pos, table=turns,
+                                         q=qkv[:, :hq], q_out=q_rot)
+            attend = B.attn_decode_prepared(q_rot, cache, pt, lens, out=o)
+            calls.append(lambda w_=write, a_=attend: (w_(), a_()))
+        del kv
+        nbytes = 2 * users * context * hk * hd * 9 // 16 + users * (hq + 2 * hk) * hd * 2 + 3 * users * hq * hd * 2
+        extra_rows[r] = (calls, 2, [q_rot, o], nbytes, 4.0 * users * context * hq * hd)
 
     # ---- the single 1024 x 1024 GEMV (batch 1), one launch per step; 1800
     # copies of its 589,824 packed bytes (1.06 GB) so that no copy is read

@@ -323,3 +323,29 @@ def test_shared_pages_as_several_new_tokens():
         y.__dict__.update(x.__dict__)
         y.lens, y.q = [400 + i], q[i:i + 1].cpu()
         y.check(out[i:i + 1], lse[i:i + 1])
+
+
+@pytest.mark.parametrize("fmt", FORMATS, ids=IDS)
+def test_offsets_past_32_bits(fmt):
+    """Groups, slots and scales whose byte offsets in the pool pass 2^32: pages at both ends of a large pool."""
+    dev = device()
+    page, hk, d = 64, 8, 128
+    group = {0: 8192, 1: 4128, 2: 2304}[fmt]
+    pages = (5 << 30) // (group * hk * page // 16)
+    cache = B.KvCache(pages, page, hk, d, fmt, device=dev)
+    assert cache.pool.numel() > 1 << 32
+    g = torch.Generator().manual_seed(1)
+    ids = torch.tensor([[pages - 1, 0, pages // 2, pages - 2]], dtype=torch.int32)
+    n = 4 * page - 5
+    j = torch.arange(n)
+    slots = ids[0].long()[j // page] * page + j % page
+    k, v = (torch.randn(n, hk, d, generator=g).to(torch.bfloat16) for _ in range(2))
+    B.kv_append(cache, k.to(dev), v.to(dev), slots.to(dev))
+    k2, v2 = B.kv_read(cache, slots.to(dev), dtype=torch.float32)
+    ks, vs = R.stored(k.float().numpy(), fmt), R.stored(v.float().numpy(), fmt)
+    assert np.array_equal(k2.double().cpu().numpy(), ks) and np.array_equal(v2.double().cpu().numpy(), vs)
+    x = Batch.__new__(Batch)
+    x.fmt, x.lens, x.hq, x.hk, x.d, x.page, x.k, x.v = fmt, [n], 2 * hk, hk, d, page, ks, vs
+    x.q = torch.randn(1, 2 * hk, d, generator=g).to(torch.bfloat16)
+    out, lse = B.attn_decode(x.q.to(dev), cache, ids.to(dev), torch.tensor([n], dtype=torch.int32, device=dev), lse=True)
+    x.check(out, lse)
