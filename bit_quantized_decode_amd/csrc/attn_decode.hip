@@ -47,6 +47,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNegInf = -__builtin_inff();
 
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 struct AttnParams {
@@ -363,8 +364,8 @@ __device__ __forceinline__ Cut cut_of(int length, int n) {
 __device__ __forceinline__ int run_start(const Cut& c, int i) { return c.each * i + min(i, c.more); }
 __device__ __forceinline__ int run_of(const Cut& c, int place) {
   const int longer = c.more * (c.each + 1);
-  return place < longer ? (int)((unsigned)place / (unsigned)(c.each + 1))
-                        : c.more + (int)((unsigned)(place - longer) / (unsigned)max(c.each, 1));
+  const bool in = place < longer;
+  return (in ? 0 : c.more) + (int)((unsigned)(in ? place : place - longer) / (unsigned)(in ? c.each + 1 : max(c.each, 1)));
 }
 
 // A unit, as much of it as joins need: places [u0, u1) of its tiles, and where its
@@ -392,10 +393,12 @@ __device__ __forceinline__ int lane_scan(int v) {
 // One workgroup's LDS.
 template <int DP, int WAVES>
 struct Staging {
-  float ml[WAVES][kRows][2];                                        // reference and sum
-  float o[WAVES][kRows][DP + 4] __attribute__((aligned(16)));
+  // Sums that wavefronts leave (slot: the wavefront), and the beginning of the
+  // unit that goes on in another workgroup (slot WAVES).
+  float ml[WAVES + 1][kRows][2];                                    // reference and sum
+  float o[WAVES + 1][kRows][DP + 4] __attribute__((aligned(16)));
   Unit first, last;          // the units cut by the share's two ends
-  int has_first, has_last, join_first, join_last;
+  int has_first, has_last, last_from, joins[2], from[2], to[2];
 };
 
 template <int FMT, int DB>
@@ -412,17 +415,21 @@ __global__ __launch_bounds__(256 * waves_per_simd(FMT, DB), (waves_per_simd(FMT,
   // The line's length, and each lane's stretch of it: `per` rows of the batch.
   const auto len_of = [&](int row) { return row < a.batch ? a.lens[row] : 0; };
   const auto places_in = [&](int row, int len) {
-    return row < a.batch ? (span_of(a, len).tiles + kLead) * units_per_row : 0;
+    return row < a.batch ? span_of(a, len).tiles + kLead : 0;  // of a unit
   };
+  if (tid == 0) lds.has_first = lds.has_last = lds.joins[0] = lds.joins[1] = 0;
+  wait_vmcnt_lgkm0<63>();
+  barrier_only();
   const int per = (a.batch + 63) / 64;
   // A window of 64 rows from row `win` on, which starts at place `win_start`: the
-  // lanes' lengths, places and inclusive sums of places.
-  int win = 0, win_start = 0, win_len = 0, win_mine = 0, win_upto = 0;
+  // lanes' lengths, places of a unit and of the row, and inclusive sums of places.
+  int win = 0, win_start = 0, win_len = 0, win_unit = 0, win_mine = 0, win_upto = 0;
   const auto move_window = [&](int row, int start) {
     win = row;
     win_start = start;
     win_len = len_of(row + lane);
-    win_mine = places_in(row + lane, win_len);
+    win_unit = places_in(row + lane, win_len);
+    win_mine = win_unit * units_per_row;
     win_upto = lane_scan(win_mine);
   };
   int mine, upto;                           // of each lane's `per` rows
@@ -433,7 +440,7 @@ __global__ __launch_bounds__(256 * waves_per_simd(FMT, DB), (waves_per_simd(FMT,
   } else {
     mine = 0;
 #pragma unroll 4
-    for (int i = 0; i < per; ++i) mine += places_in(lane * per + i, len_of(lane * per + i));
+    for (int i = 0; i < per; ++i) mine += places_in(lane * per + i, len_of(lane * per + i)) * units_per_row;
     upto = lane_scan(mine);
   }
   const int total = __builtin_amdgcn_readlane(upto, 63);
@@ -454,25 +461,30 @@ __global__ __launch_bounds__(256 * waves_per_simd(FMT, DB), (waves_per_simd(FMT,
     }
     const int at = __builtin_ctzll(__ballot(win_start + win_upto > place));
     return Row{win + at, win_start + __builtin_amdgcn_readlane(win_upto - win_mine, at),
-               __builtin_amdgcn_readlane(win_mine, at) / units_per_row};
+               __builtin_amdgcn_readlane(win_unit, at)};
   };
-  // An end of a share: moved to a unit's end if the unit is short.
-  const auto share_end = [&](int i) {
-    const int place = run_start(shares, i);
-    if (i == 0 || i == shares.n) return place;
-    const Row r = row_at(place);
-    const int into = (place - r.start) % r.unit;
-    return r.unit > kLead + 2 * kWaves ? place : 2 * into < r.unit ? place - into : place - into + r.unit;
-  };
-  const int s0 = share_end(w), s1 = share_end(w + 1);  // the workgroup's share
-  if (s0 >= s1) return;
-  const Cut runs = cut_of(s1 - s0, kWaves);
-  const auto run_at = [&](int i) { return s0 + run_start(runs, i); };
-  const int g0 = run_at(wave), g1 = run_at(wave + 1);
-  const Row r0 = row_at(min(g0, total - 1));
+  // The workgroup's share [s0, s1), an end moved to a unit's end if that unit is
+  // short; the wavefront's run [g0, g1) of it, and the row where that starts.
+  int s0 = 0, s1 = 0, g0 = 0, g1 = 0;
+  Cut runs{kWaves, 0, 0};
+  Row r0{0, 0, 1};
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    if (k == 2) {
+      if (s0 >= s1) return;
+      runs = cut_of(s1 - s0, kWaves);
+      g0 = s0 + run_start(runs, wave);
+      g1 = s0 + run_start(runs, wave + 1);
+    }
+    const int place = k == 2 ? g0 : run_start(shares, w + k);
+    r0 = row_at(min(place, total - 1));
+    const int into = (int)((unsigned)(place - r0.start) % (unsigned)r0.unit);
+    const bool moved = k < 2 && place < total && r0.unit <= kLead + 2 * kWaves;
+    const int end = !moved ? place : 2 * into < r0.unit ? place - into : place - into + r0.unit;
+    if (k == 0) s0 = end;
+    else if (k == 1) s1 = end;
+  }
   int b = r0.b, row_start = r0.start;
-  // (Set again, if at all, by this wavefront or after the next barrier.)
-  if (tid == 0) lds.has_first = lds.has_last = lds.join_first = lds.join_last = 0;
 
   // What is left in registers at the end: the beginning of a unit that goes on.
   f32x4 o[kW];
@@ -498,20 +510,21 @@ __global__ __launch_bounds__(256 * waves_per_simd(FMT, DB), (waves_per_simd(FMT,
     g = max(g, u0);
     const int stop = min(u1, g1);
     if (g >= stop) break;                       // the run ends before the unit's first tile
-    const int head = unit / a.row_tiles, rt = unit - head * a.row_tiles;
+    const int head = a.row_tiles > 1 ? unit / a.row_tiles : unit, rt = unit - head * a.row_tiles;
     const int rows = min(a.group - rt * kRows, kRows), q0 = head * a.group + rt * kRows;
     const int first = g - u0, count = stop - g;
 
     // Queries: lane (q, h) holds values E h .. E h + E - 1 of row q.
     uint32_t qv[kE / 2];
     const int d_here = a.cache.head_dim - kE * h;  // values of this lane inside the head
-    const uint16_t* qp = a.q + (int64_t)b * a.ldq + (int64_t)(q0 + qn) * a.cache.head_dim + kE * h;
+    const bool in_head = qn < rows && d_here > 0;  // other lanes and values: zeros, from addresses inside
+    const uint16_t* qp = a.q + (int64_t)b * a.ldq + (in_head ? (q0 + qn) * a.cache.head_dim + kE * h : q0 * a.cache.head_dim);
+    const int last = in_head ? d_here - 8 : 0;
 #pragma unroll
     for (int i = 0; i < kE / 8; ++i) {
-      u32x4 x{0u, 0u, 0u, 0u};
-      if (qn < rows && 8 * i < d_here) x = load16(qp + 8 * i);
+      const u32x4 x = load16(qp + min(8 * i, last));
 #pragma unroll
-      for (int j = 0; j < 4; ++j) qv[4 * i + j] = x[j];
+      for (int j = 0; j < 4; ++j) qv[4 * i + j] = in_head && 8 * i <= last ? x[j] : 0u;
     }
     // Page lookups: lane j holds the group of step it + j / 2, half j & 1, for 32
     // steps from the last multiple of 32; -1: none there.
@@ -553,9 +566,10 @@ __global__ __launch_bounds__(256 * waves_per_simd(FMT, DB), (waves_per_simd(FMT,
     if constexpr (FMT == kKvNvfp4) {
       // bf16 -> f16: a power of two per row puts its largest magnitude at
       // 2^14 .. 2^15; values down to 2^-28 of it stay exact.
-      uint32_t big = 0;
+      u16x2 pair{0, 0};
 #pragma unroll
-      for (int i = 0; i < kE / 2; ++i) big = max(big, max((qv[i] << 16) & 0x7fffffffu, qv[i] & 0x7fff0000u));
+      for (int i = 0; i < kE / 2; ++i) pair = __builtin_elementwise_max(pair, __builtin_bit_cast(u16x2, qv[i] & 0x7fff7fffu));
+      uint32_t big = (uint32_t)(pair[0] > pair[1] ? pair[0] : pair[1]) << 16;
       big = max(big, (uint32_t)__shfl_xor((int)big, 16));
       big = max(big, (uint32_t)__shfl_xor((int)big, 32));
       int e = (int)(big >> 23) - 127 - 14;
@@ -664,19 +678,26 @@ __global__ __launch_bounds__(256 * waves_per_simd(FMT, DB), (waves_per_simd(FMT,
 
     sum += lane_xor(sum, 16);
     sum += lane_xor(sum, 32);
-    if (u0 < g0) {
-      // The end, or a stretch, of a unit that an earlier wavefront began.
+    if (u0 < g0 || u1 > s1) {
+      // The end, or a stretch, of a unit that an earlier wavefront began; or the
+      // beginning of one that goes on in another workgroup.
+      const int slot = u0 < g0 ? wave : kWaves;
       if (qn < rows) {
         if (h == 0) {
-          lds.ml[wave][qn][0] = ref;
-          lds.ml[wave][qn][1] = sum;
+          lds.ml[slot][qn][0] = ref;
+          lds.ml[slot][qn][1] = sum;
         }
 #pragma unroll
-        for (int u = 0; u < kQuads; ++u) *reinterpret_cast<f32x4*>(&lds.o[wave][qn][d0 + 4 * u]) = quad(u);
+        for (int u = 0; u < kQuads; ++u) *reinterpret_cast<f32x4*>(&lds.o[slot][qn][d0 + 4 * u]) = quad(u);
       }
-      if (u0 < s0 && lane == 0 && g == s0) {
+      if (lane == 0 && u0 < s0 && g == s0) {
         lds.first = Unit{u0, u1, b, q0, rows};
         lds.has_first = 1;
+      }
+      if (lane == 0 && u0 >= g0) {
+        lds.last = Unit{u0, u1, b, q0, rows};
+        lds.has_last = 1;
+        lds.last_from = wave + 1;
       }
     } else if (u1 > g1) {
       tail = Unit{u0, u1, b, q0, rows};
@@ -688,84 +709,90 @@ __global__ __launch_bounds__(256 * waves_per_simd(FMT, DB), (waves_per_simd(FMT,
   }
   __syncthreads();
 
-  // Adds what wavefronts from .. left in LDS of a unit that ends at place u1 (runs
-  // without a place are the share's last).
-  const auto add_from = [&](int from, int u1, f32x4 (&acc)[kQuads], float& top, float& l) {
-    const int end = u1 >= s1 ? (runs.each > 0 ? kWaves : runs.more) : run_of(runs, u1 - 1 - s0) + 1;
-    float next = top;
-    for (int i = from; i < end; ++i) next = fmaxf(next, lds.ml[i][qn][0]);
-    const float fo = top == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(top - next);
-    l *= fo;
+  // One past the last wavefront with a place before u1 (runs without a place are the
+  // share's last).
+  const auto wave_end = [&](int u1) {
+    return u1 >= s1 ? (runs.each > 0 ? kWaves : runs.more) : run_of(runs, u1 - 1 - s0) + 1;
+  };
+  if (tail.rows > 0) {
+    // A unit inside the share: its beginning, in registers, and what the
+    // wavefronts after it left.
+    f32x4 acc[kQuads];
+#pragma unroll
+    for (int u = 0; u < kQuads; ++u) acc[u] = quad(u);
+    const int from = wave + 1, end = wave_end(tail.u1);
+    float top = ref;
+    for (int i = from; i < end; ++i) top = fmaxf(top, lds.ml[i][qn][0]);
+    const float fo = ref == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(ref - top);
+    sum *= fo;
 #pragma unroll
     for (int u = 0; u < kQuads; ++u) acc[u] *= fo;
 #pragma unroll 2
     for (int i = from; i < end; ++i) {
       const float m = lds.ml[i][qn][0];
-      const float f = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m - next);
-      l += lds.ml[i][qn][1] * f;
+      const float f = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m - top);
+      sum += lds.ml[i][qn][1] * f;
 #pragma unroll
       for (int u = 0; u < kQuads; ++u) acc[u] += *reinterpret_cast<const f32x4*>(&lds.o[i][qn][d0 + 4 * u]) * f;
     }
-    top = next;
-  };
-  const __amdgpu_buffer_rsrc_t buf = part_buffer(a);
-  const auto store_sums = [&](int side, int rows, const f32x4 (&acc)[kQuads], float top, float l) {
-    if (qn >= rows) return;
-    const int to = part_offset<kDp>(a, w, side, qn);
-    if (h == 0) store_part(buf, to, f32x4{top, l, 0.0f, 0.0f});
+    if (qn < tail.rows) {
 #pragma unroll
-    for (int u = 0; u < kQuads; ++u) store_part(buf, to + (4 + d0 + 4 * u) * 4, acc[u]);
-  };
-  f32x4 acc[kQuads];
-  if (tail.rows > 0) {
-#pragma unroll
-    for (int u = 0; u < kQuads; ++u) acc[u] = quad(u);
-    add_from(wave + 1, tail.u1, acc, ref, sum);
-    if (tail.u1 <= s1) {
-      if (qn < tail.rows) {
-#pragma unroll
-        for (int u = 0; u < kQuads; ++u) write_out(a, tail.b, tail.q0 + qn, d0 + 4 * u, ref, sum, acc[u]);
-      }
-    } else {
-      store_sums(1, tail.rows, acc, ref, sum);
-      if (lane == 0) {
-        lds.last = tail;
-        lds.has_last = 1;
-      }
+      for (int u = 0; u < kQuads; ++u) write_out(a, tail.b, tail.q0 + qn, d0 + 4 * u, top, sum, acc[u]);
     }
   }
-  if (wave == kWaves - 1 && lds.has_first) {  // (no wavefront after it: its own tail needed no joining)
-#pragma unroll
-    for (int u = 0; u < kQuads; ++u) acc[u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    float top = kNegInf, l = 0.0f;
-    add_from(0, lds.first.u1, acc, top, l);
-    store_sums(0, lds.first.rows, acc, top, l);
+  const int has_first = lds.has_first, has_last = lds.has_last;
+  if (!has_first && !has_last) return;
+  // The units cut by the share's two ends, by all threads: each four values of a
+  // row, from slot kWaves (the beginning of the second) and those of the wavefronts
+  // from `from` on.
+  const __amdgpu_buffer_rsrc_t buf = part_buffer(a);
+#pragma unroll 1
+  for (int side = has_first ? 0 : 1; side <= has_last; ++side) {
+    const int from = side ? lds.last_from - 1 : 0, rows = side ? lds.last.rows : lds.first.rows;
+    const int end = wave_end(side ? lds.last.u1 : lds.first.u1);
+    for (int e = tid; e < rows * (kDp / 4); e += kThreads) {
+      const int r = e / (kDp / 4), d = 4 * (e - r * (kDp / 4));
+      const auto slot = [&](int i) { return side && i == from ? kWaves : i; };
+      float top = kNegInf, l = 0.0f;
+#pragma unroll 1
+      for (int i = from; i < end; ++i) top = fmaxf(top, lds.ml[slot(i)][r][0]);
+      f32x4 acc{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+      for (int i = from; i < end; ++i) {
+        const int k = slot(i);
+        const float m = lds.ml[k][r][0];
+        const float f = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m - top);
+        l += lds.ml[k][r][1] * f;
+        acc += *reinterpret_cast<const f32x4*>(&lds.o[k][r][d]) * f;
+      }
+      const int to = part_offset<kDp>(a, w, side, r);
+      if (d == 0) store_part(buf, to, f32x4{top, l, 0.0f, 0.0f});
+      store_part(buf, to + (4 + d) * 4, acc);
+    }
   }
   __atomic_signal_fence(__ATOMIC_SEQ_CST);  // keep the stores of partial sums above the wait
   __builtin_amdgcn_s_waitcnt(0);            // they have completed
   __syncthreads();
-  if (!lds.has_first && !lds.has_last) return;
-  const int first0 = lds.has_first ? run_of(shares, lds.first.u0) : 0, first1 = lds.has_first ? run_of(shares, lds.first.u1 - 1) : 0;
-  const int last1 = lds.has_last ? run_of(shares, lds.last.u1 - 1) : 0;
-  if (tid == 0) {
+  if (tid < 2 && (tid ? has_last : has_first)) {
     // A unit's counter is that of the workgroup where it begins; the last to
     // arrive finds all others counted and leaves it at zero.
-    unsigned p = 0, q = 0;
-    if (lds.has_first) p = __hip_atomic_fetch_add(a.counters + first0, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    if (lds.has_last) q = __hip_atomic_fetch_add(a.counters + w, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    if (lds.has_first && p == (unsigned)(first1 - first0)) {
-      __hip_atomic_store(a.counters + first0, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      lds.join_first = 1;
-    }
-    if (lds.has_last && q == (unsigned)(last1 - w)) {
-      __hip_atomic_store(a.counters + w, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      lds.join_last = 1;
+    const Unit u = tid ? lds.last : lds.first;
+    const int from = run_of(shares, u.u0), to = run_of(shares, u.u1 - 1);
+    const unsigned before = __hip_atomic_fetch_add(a.counters + from, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (before == (unsigned)(to - from)) {
+      __hip_atomic_store(a.counters + from, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      lds.joins[tid] = 1;
+      lds.from[tid] = from;
+      lds.to[tid] = to;
     }
   }
   __syncthreads();
-  const Unit uf = lds.first, ul = lds.last;
-  if (lds.join_first) join_parts<kDp, kThreads>(a, first0, first1, uf.rows, uf.b, uf.q0, &lds.o[0][0][0]);
-  if (lds.join_last) join_parts<kDp, kThreads>(a, w, last1, ul.rows, ul.b, ul.q0, &lds.o[0][0][0]);
+  const int joins[2] = {lds.joins[0], lds.joins[1]};
+#pragma unroll 1
+  for (int side = joins[0] ? 0 : 1; side <= joins[1]; ++side) {
+    const Unit u = side ? lds.last : lds.first;
+    join_parts<kDp, kThreads>(a, lds.from[side], lds.to[side], u.rows, u.b, u.q0, &lds.o[0][0][0]);
+  }
 }
 
 int row_tiles_of(const AttnLaunch& a) { return (a.q_heads / a.cache.heads + kRows - 1) / kRows; }
