@@ -123,7 +123,7 @@ typedef struct nvfp4_kv_cache {
   int64_t kv_heads;         /* 1..1024 */
   int64_t head_dim;         /* multiple of 16, 16..256 */
   int format;               /* nvfp4_kv_format */
-  float k_scale, v_scale;   /* tensor scales, > 0 and finite; 1 unless NVFP4_KV_NVFP4 */
+  float k_scale, v_scale;   /* tensor scales, 2^-64 .. 2^64; 1 unless NVFP4_KV_NVFP4 */
 } nvfp4_kv_cache;
 
 /* (host) *bytes = size of the pool (cache->pool is not looked at). */
@@ -188,6 +188,10 @@ int nvfp4_kv_read(const nvfp4_kv_cache* cache /* host */, const int64_t* slots, 
  * two bf16 numbers) or 2^-12 (NVFP4: one f16 number); their sum takes them whole.
  * o is bf16, rounded once.  The work is split evenly over the GPU along all
  * sequences' lengths, whatever their mix, and joined in a fixed order.
+ *
+ * One call takes up to 2^31 tiles of 32 tokens, counted over all sequences, kv
+ * heads and sixteens of a kv head's query heads, each at the longest length that
+ * the table (or the window) allows, plus a few for each; more is refused.
  *
  * The workspace's first NVFP4_ATTN_COUNTER_BYTES must be zero before its first
  * use; every call leaves them zero.  Calls that share one must not overlap.

@@ -73,6 +73,10 @@ int main() {
   nvfp4_attn_args t{};
   t.cache = &c; t.batch = 65536; t.q_heads = 32768; t.table_width = ((int64_t)1 << 30) / 64; t.window = INT64_MAX;
   t.scale = 1.0f; t.ldq = t.ldo = 32768 * 128;
+  expect(nvfp4_attn_decode_workspace_bytes(&t, &sz), NVFP4_ERR_SHAPE, "attention of 2^31 tiles");
+  t.batch = 1;  // 8 kv heads x 256 row tiles x 2^20 tiles
+  expect(nvfp4_attn_decode_workspace_bytes(&t, &sz), NVFP4_ERR_SHAPE, "attention of 2^31 tiles");
+  t.batch = 65536; t.q_heads = 8; t.window = 1000;  // 8 kv heads x 35 tiles a sequence
   expect(nvfp4_attn_decode_workspace_bytes(&t, &sz), NVFP4_OK, "attention workspace");
   expect(nvfp4_attn_decode(&t, nullptr), NVFP4_ERR_NULL, "attention null");
   t.q = t.out = static_cast<uint16_t*>(A);

@@ -212,7 +212,9 @@ def attn(d, **over):
 @pytest.mark.parametrize("over,status", [
     (dict(batch=-1), B.NVFP4_ERR_SHAPE), (dict(batch=65537), B.NVFP4_ERR_SHAPE), (dict(q_heads=0), B.NVFP4_ERR_SHAPE),
     (dict(q_heads=12), B.NVFP4_ERR_SHAPE), (dict(q_heads=32776), B.NVFP4_ERR_SHAPE), (dict(table_width=-1), B.NVFP4_ERR_SHAPE),
-    (dict(table_width=(1 << 24) + 1), B.NVFP4_ERR_SHAPE), (dict(window=-1), B.NVFP4_ERR_ARG), (dict(scale=0.0), B.NVFP4_ERR_ARG),
+    (dict(table_width=(1 << 24) + 1), B.NVFP4_ERR_SHAPE), (dict(batch=65536, table_width=1 << 22), B.NVFP4_ERR_SHAPE),
+    (dict(batch=65536, q_heads=32768, ldq=1 << 23, ldo=1 << 23, table_width=8), B.NVFP4_ERR_SHAPE),
+    (dict(window=-1), B.NVFP4_ERR_ARG), (dict(scale=0.0), B.NVFP4_ERR_ARG),
     (dict(scale=-1.0), B.NVFP4_ERR_ARG), (dict(scale=float("nan")), B.NVFP4_ERR_ARG), (dict(scale=float("inf")), B.NVFP4_ERR_ARG),
     (dict(ldq=5112), B.NVFP4_ERR_SHAPE), (dict(ldo=5124), B.NVFP4_ERR_SHAPE), (dict(q=None), B.NVFP4_ERR_NULL),
     (dict(out=None), B.NVFP4_ERR_NULL), (dict(seq_lens=None), B.NVFP4_ERR_NULL), (dict(page_table=None), B.NVFP4_ERR_NULL),
