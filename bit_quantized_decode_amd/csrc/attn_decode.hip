@@ -260,6 +260,13 @@ __device__ __forceinline__ void clear_masked(Tile<FMT, DB>& t, uint32_t ok) {
     }
 }
 
+// Rounded as written: a fused product and difference would take p from a score that is
+// not rounded, against a reference that is, and at scores past 2^25 give it any size.
+__device__ __forceinline__ float rounded_product(float a, float b) {
+#pragma clang fp contract(off)
+  return a * b;
+}
+
 __device__ __forceinline__ float lane_xor(float v, int off) { return __shfl_xor(v, off); }
 
 // f16 probabilities are held 2^kOffset above the reference, so that small ones
@@ -587,7 +594,7 @@ __global__ __launch_bounds__(256 * waves_per_simd(FMT, DB), (waves_per_simd(FMT,
     for (int i = 0; i < kW; ++i) o[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     ref = kNegInf;
     sum = 0.0f;
-    float shift = -1e30f;
+    float shift = 0.0f;
 
     for (int it = 0; it < count; ++it) {
       const int tok0 = sp.base + (first + it) * kTile;
@@ -617,7 +624,7 @@ __global__ __launch_bounds__(256 * waves_per_simd(FMT, DB), (waves_per_simd(FMT,
           acc = mma<FMT>(op, &qv[4 * s], acc);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[4 * half + i] = acc[i];
+        for (int i = 0; i < 4; ++i) x[4 * half + i] = rounded_product(acc[i], score_scale);
       }
       load_k<FMT, DB>(a.cache, from, lane, t);
       if (!whole) {
@@ -627,14 +634,15 @@ __global__ __launch_bounds__(256 * waves_per_simd(FMT, DB), (waves_per_simd(FMT,
       float top = x[0];
 #pragma unroll
       for (int i = 1; i < 8; ++i) top = fmaxf(top, x[i]);
-      top *= score_scale;
-      if (__any(top > ref + (Softmax<FMT>::kOffset + Softmax<FMT>::kSlack))) {
+      // (Differences of scores are exact where a bound on them matters; sums with the
+      // reference would be rounded to the scores' own steps.)
+      if (__any(top - ref > Softmax<FMT>::kOffset + Softmax<FMT>::kSlack)) {
         top = fmaxf(top, lane_xor(top, 16));
         top = fmaxf(top, lane_xor(top, 32));
         const float next = fmaxf(ref, top - Softmax<FMT>::kOffset);
         const float alpha = next == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(ref - next);
         ref = next;
-        shift = fmaxf(ref, -1e30f);
+        shift = ref == kNegInf ? 0.0f : ref;
         sum *= alpha;
 #pragma unroll
         for (int i = 0; i < kW; ++i) o[i] *= alpha;
@@ -642,7 +650,7 @@ __global__ __launch_bounds__(256 * waves_per_simd(FMT, DB), (waves_per_simd(FMT,
       float p[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], score_scale, -shift));
+        p[i] = __builtin_amdgcn_exp2f(x[i] - shift);
         sum += p[i];
       }
       uint32_t hi[4], lo[4];

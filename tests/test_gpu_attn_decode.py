@@ -155,6 +155,43 @@ def test_sharp_flat_and_growing_scores(fmt):
         y.check(*y.call(), what=sign)
 
 
+@pytest.mark.parametrize("fmt", FORMATS, ids=IDS)
+@pytest.mark.parametrize("shift", [0, 24, 26, 28, 32, 90])
+def test_scores_far_beyond_the_exponentials_range(fmt, shift):
+    """Scores of +-2^shift times small integers, exact in fp32: at 2^24 all weight is on the largest, however far
+    below zero, and equal ones share it.  log2 e enters once, rounded, so the lse is off relative to its size."""
+    dev = device()
+    n, page = 700, 64
+    x = Batch(dev, fmt, [n, n], 2, 1, 64, page)
+    c = torch.arange(2 * n) % 5 + 2                       # 2 .. 6: E2M1 and E4M3 values times a power of two
+    c[c == 5] = 4
+    k = torch.zeros(2 * n, 1, 64)
+    k[:, 0, 0] = c
+    v = torch.randn(2 * n, 1, 64, generator=torch.Generator().manual_seed(shift)).to(torch.bfloat16)
+    at = torch.arange(2 * n)
+    slots = x.table.cpu().long()[at // n, at % n // page] * page + at % n % page
+    B.kv_append(x.cache, k.to(torch.bfloat16).to(dev), v.to(dev), slots.to(dev))
+    x.k, x.v = R.stored(k.numpy(), fmt), R.stored(v.float().numpy(), fmt)
+    x.q = torch.zeros(2, 2, 64, dtype=torch.bfloat16)
+    x.q[0, 0, 0], x.q[0, 1, 0], x.q[1, 0, 0], x.q[1, 1, 0] = 1.0, -1.0, -0.75, 2.0
+    if shift == 0:
+        x.check(*x.call(scale=1.0), scale=1.0)
+        return
+    out, lse = x.call(scale=2.0 ** shift)
+    out, lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    for b in range(2):
+        for h in range(2):
+            s = float(x.q[b, h, 0]) * x.k[b * n:(b + 1) * n, 0, 0] * 2.0 ** shift
+            rows = x.v[b * n:(b + 1) * n, 0][s == s.max()]
+            o = rows.mean(0)
+            # As many equal terms, a sum and a quotient in fp32, and one rounding to bf16.
+            bound = 2.0 ** -8 * np.abs(o) + (len(rows) + 8) * 2.0 ** -24 * np.abs(rows).mean(0) + 1e-30
+            if fmt == B.NVFP4_KV_NVFP4:
+                bound += 2.0 ** -11 * np.abs(rows).mean(0)
+            assert (np.abs(out[b, h] - o) <= bound).all(), (b, h)
+            assert abs(lse[b, h] - s.max()) <= 2.0 ** -20 * abs(s.max())
+
+
 def test_small_terms_add_up():
     """One token at the maximum and 60,000 that each weigh 2^-20 of it: no term may be lost to a 16-bit range."""
     dev = device()
