@@ -307,7 +307,7 @@ __device__ __forceinline__ void add_part(float& top, float& sum, f32x4 (&acc)[N]
 // then added in order through LDS (6 floats a thread).
 template <int DP, int kThreads>
 __device__ __forceinline__ void join_parts(const AttnParams& a, int wfirst, int wlast, int rows, int b, int q0, float* lds) {
-  constexpr int kBatch = 8;
+  constexpr int kBatch = 12;
   constexpr int kQuads = DP / 4;
   const int parts = wlast - wfirst + 1, items = rows * kQuads;
   const int runs = min(items >= kThreads ? 1 : kThreads / items, parts);
