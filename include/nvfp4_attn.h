@@ -179,14 +179,16 @@ int nvfp4_kv_read(const nvfp4_kv_cache* cache /* host */, const int64_t* slots, 
  * A page id outside [0, pages) holds nothing: its tokens are left out of the sums
  * (an evicted page: -1).  A row left with no token, or only with scores of -inf,
  * gives zeros and lse = -inf.  Table entries past a sequence's last page are not
- * looked at, cache slots past its length have no effect whatever they hold.
+ * looked at, cache slots past its length have no effect whatever they hold.  An
+ * infinity or NaN in a query, or in a token that a row attends to, gives that
+ * head's row infinities or NaN, and so do scores past fp32's range.
  * Several rows may share pages: a few new tokens of one sequence are rows with
  * the same table and lengths n, n + 1, ...
  *
  * Scores, maxima, sums and outputs are held in fp32.  The exp() terms enter the
  * matrix cores rounded to within 2^-17 of each (bf16 and E4M3 caches: the sum of
  * two bf16 numbers) or 2^-12 (NVFP4: one f16 number); their sum takes them whole.
- * o is bf16, rounded once.  The work is split evenly over the GPU along all
+ * o is bf16, rounded once; out overlaps no input.  The work is split evenly over the GPU along all
  * sequences' lengths, whatever their mix, and joined in a fixed order.
  *
  * One call takes up to 2^31 tiles of 32 tokens, counted over all sequences, kv

@@ -129,6 +129,38 @@ def test_large_batch_of_rows():
     x.check(*x.call())
 
 
+def test_largest_batch():
+    """65,536 rows of one token or none, over pages that they share: each row is its token's value."""
+    dev = device()
+    b, page, pages = 65536, 16, 40
+    g = torch.Generator().manual_seed(5)
+    cache = B.KvCache(pages, page, 1, 64, B.NVFP4_KV_E4M3, device=dev)
+    kv = torch.randn(pages * page, 1, 64, generator=g).to(torch.bfloat16)
+    B.kv_append(cache, kv.to(dev), kv.to(dev), torch.arange(pages * page, device=dev))
+    table = torch.randint(0, pages, (b, 1), generator=g).to(torch.int32)
+    lens = torch.randint(0, 2, (b,), generator=g).to(torch.int32)
+    lens[0], lens[-1] = 1, 1
+    q = torch.randn(b, 1, 64, generator=g).to(torch.bfloat16)
+    out, lse = B.attn_decode(q.to(dev), cache, table.to(dev), lens.to(dev), lse=True)
+    stored = torch.from_numpy(R.stored(kv.float().numpy(), B.NVFP4_KV_E4M3))[:, 0]
+    mine = stored[table[:, 0].long() * page]
+    live = (lens == 1)[:, None]
+    assert torch.equal(out[:, 0].cpu(), torch.where(live, mine, 0.0).to(torch.bfloat16))
+    score = (q[:, 0].double() * mine.double()).sum(-1, keepdim=True) / 8
+    size = (q[:, 0].double() * mine.double()).abs().sum(-1, keepdim=True) / 8
+    lse = lse.double().cpu()
+    assert torch.isneginf(lse[~live]).all()
+    # 64 products, one product with the scale, the exponential's, the logarithm's and the sum's own rounding.
+    assert ((lse - score).abs() <= (80 * size + 16) * 2.0 ** -24)[live].all()
+
+
+@pytest.mark.parametrize("hq,hk,d", [(32768, 1, 16), (1024, 1024, 64), (32768, 1024, 16)])
+def test_most_heads(hq, hk, d):
+    dev = device()
+    x = Batch(dev, B.NVFP4_KV_NVFP4, [50], hq, hk, d, 16, seed=hk)
+    x.check(*x.call(), what=(hq, hk))
+
+
 @pytest.mark.parametrize("fmt", FORMATS, ids=IDS)
 def test_long_sequence_split_over_every_workgroup(fmt):
     dev = device()

@@ -177,3 +177,46 @@ def test_queries_in_place_and_empty():
     assert B.kv_append(cache, none, none, torch.empty(0, dtype=torch.int64, device=dev)) is None
     k, v = B.kv_read(cache, torch.empty(0, dtype=torch.int64, device=dev))
     assert k.shape == v.shape == (0, 1, 64)
+
+
+@pytest.mark.parametrize("fmt", FORMATS, ids=IDS)
+def test_capture_and_replay(fmt):
+    """Writing with rotary positions, reading back and turning, captured together and replayed among eager calls over
+    changing rows, positions and slots."""
+    dev = device()
+    g = torch.Generator().manual_seed(fmt)
+    tokens, hq, hk, d = 37, 5, 2, 128
+    table = B.rope_table(d, device=dev)
+    caches = [B.KvCache(6, 16, hk, d, fmt, device=dev) for _ in range(2)]
+    for c in caches:
+        c.pool.zero_()
+    qkv = torch.empty(tokens, hq + 2 * hk, d, dtype=torch.bfloat16, device=dev)
+    pos = torch.empty(tokens, dtype=torch.int32, device=dev)
+    slots = torch.empty(tokens, dtype=torch.int64, device=dev)
+
+    def step(cache):
+        q, k, v = qkv.split([hq, hk, hk], 1)
+        q_out = B.kv_append(cache, k, v, slots, positions=pos, table=table, q=q)
+        return q_out, *B.kv_read(cache, slots), B.rope(qkv, pos, table, inverse=True)
+
+    def new_inputs():
+        qkv.copy_(torch.randn(qkv.shape, generator=g))
+        pos.copy_(torch.randint(0, 2 ** 31 - 1, (tokens,), generator=g))
+        slots.copy_(torch.randperm(96, generator=g)[:tokens])
+
+    new_inputs()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        step(caches[0])
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph, stream=side):
+            captured = step(caches[0])
+    torch.cuda.synchronize()
+    for _ in range(4):
+        new_inputs()
+        graph.replay()
+        eager = step(caches[1])
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(captured, eager))
