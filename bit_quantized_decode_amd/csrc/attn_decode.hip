@@ -47,6 +47,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNegInf = -__builtin_inff();
 
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
@@ -109,50 +110,68 @@ struct Tile {
   uint32_t ks[2], vs[2][kVScales];
 };
 
+// Where a group's codes and scales lie, as buffers: of a group that is not there
+// (below 0) they are empty, and loads from them give zeros without reading.
+struct GroupBuffers {
+  __amdgpu_buffer_rsrc_t codes, scales;
+};
 template <int FMT, int DB>
-__device__ __forceinline__ void load_side(const uint8_t* p, int lane, uint32_t* w) {
+__device__ __forceinline__ GroupBuffers group_buffers(const KvCache& c, int group) {
+  using L = KvLayout<FMT, DB>;
+  const int64_t g = max(group, 0);
+  GroupBuffers r;
+  r.codes = __builtin_amdgcn_make_buffer_rsrc(c.codes + g * L::kCodeBytes, 0, group < 0 ? 0 : L::kCodeBytes, 0x00020000);
+  r.scales = __builtin_amdgcn_make_buffer_rsrc(c.scales + g * L::kScaleBytes, 0, group < 0 ? 0 : L::kScaleBytes, 0x00020000);
+  return r;
+}
+
+constexpr int kStreamed = 2;  // cache policy nt
+template <int FMT, int DB>
+__device__ __forceinline__ void load_side(__amdgpu_buffer_rsrc_t r, int side, int lane, uint32_t* w) {
   using L = KvLayout<FMT, DB>;
 #pragma unroll
   for (int i = 0; i < L::kPlanes16; ++i) {
-    const u32x4 x = load16_stream(p + i * 1024 + lane * 16);
+    const u32x4 x =
+        __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, lane * 16, side + i * 1024, kStreamed));
 #pragma unroll
     for (int j = 0; j < 4; ++j) w[4 * i + j] = x[j];
   }
   if constexpr (L::kPlane8) {
-    const uint2 x = *reinterpret_cast<const uint2*>(p + L::kPlanes16 * 1024 + lane * 8);
-    w[4 * L::kPlanes16] = x.x;
-    w[4 * L::kPlanes16 + 1] = x.y;
+    const u32x2 x = __builtin_bit_cast(
+        u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, lane * 8, side + L::kPlanes16 * 1024, kStreamed));
+    w[4 * L::kPlanes16] = x[0];
+    w[4 * L::kPlanes16 + 1] = x[1];
   }
 }
 
 template <int FMT, int DB>
-__device__ __forceinline__ void load_k(const KvCache& c, const int (&group)[2], int lane, Tile<FMT, DB>& t) {
+__device__ __forceinline__ void load_k(const GroupBuffers (&g)[2], int lane, Tile<FMT, DB>& t) {
   using L = KvLayout<FMT, DB>;
 #pragma unroll
   for (int a = 0; a < 2; ++a) {
-    load_side<FMT, DB>(c.codes + (int64_t)group[a] * L::kCodeBytes, lane, t.k[a]);
-    const uint8_t* s = c.scales + (int64_t)group[a] * L::kScaleBytes;
-    if constexpr (FMT == kKvE4m3) t.ks[a] = s[lane & 15];
+    load_side<FMT, DB>(g[a].codes, 0, lane, t.k[a]);
+    if constexpr (FMT == kKvE4m3) t.ks[a] = __builtin_amdgcn_raw_buffer_load_b8(g[a].scales, lane & 15, 0, 0);
     else if constexpr (FMT == kKvNvfp4) {
-      if constexpr (L::kKScaleLane == 1) t.ks[a] = s[lane];
-      else if constexpr (L::kKScaleLane == 2) t.ks[a] = *reinterpret_cast<const uint16_t*>(s + 2 * lane);
-      else t.ks[a] = *reinterpret_cast<const uint32_t*>(s + 4 * lane);
+      if constexpr (L::kKScaleLane == 1) t.ks[a] = __builtin_amdgcn_raw_buffer_load_b8(g[a].scales, lane, 0, 0);
+      else if constexpr (L::kKScaleLane == 2) t.ks[a] = __builtin_amdgcn_raw_buffer_load_b16(g[a].scales, 2 * lane, 0, 0);
+      else t.ks[a] = __builtin_amdgcn_raw_buffer_load_b32(g[a].scales, 4 * lane, 0, 0);
     }
   }
 }
 
 template <int FMT, int DB>
-__device__ __forceinline__ void load_v(const KvCache& c, const int (&group)[2], int lane, Tile<FMT, DB>& t) {
+__device__ __forceinline__ void load_v(const GroupBuffers (&g)[2], int lane, Tile<FMT, DB>& t) {
   using L = KvLayout<FMT, DB>;
 #pragma unroll
   for (int a = 0; a < 2; ++a) {
-    load_side<FMT, DB>(c.codes + (int64_t)group[a] * L::kCodeBytes + L::kSideBytes, lane, t.v[a]);
-    const uint8_t* s = c.scales + (int64_t)group[a] * L::kScaleBytes + L::kKScaleBytes;
-    if constexpr (FMT == kKvE4m3) t.vs[a][0] = *reinterpret_cast<const uint32_t*>(s + 4 * (lane >> 4));
+    load_side<FMT, DB>(g[a].codes, L::kSideBytes, lane, t.v[a]);
+    if constexpr (FMT == kKvE4m3)
+      t.vs[a][0] = __builtin_amdgcn_raw_buffer_load_b32(g[a].scales, 4 * (lane >> 4), L::kKScaleBytes, 0);
     else if constexpr (FMT == kKvNvfp4) {
-      const uint32_t* vs = reinterpret_cast<const uint32_t*>(s) + (lane >> 4) * (4 * DB);
 #pragma unroll
-      for (int u = 0; u < Tile<FMT, DB>::kVScales; ++u) t.vs[a][u] = vs[(L::kW * (lane & 15) + 4 * u) / 16];
+      for (int u = 0; u < Tile<FMT, DB>::kVScales; ++u)
+        t.vs[a][u] = __builtin_amdgcn_raw_buffer_load_b32(
+            g[a].scales, 16 * DB * (lane >> 4) + 4 * ((L::kW * (lane & 15) + 4 * u) / 16), L::kKScaleBytes, 0);
     }
   }
 }
@@ -550,24 +569,23 @@ __global__ __launch_bounds__(256 * waves_per_simd(FMT, DB), (waves_per_simd(FMT,
       group[0] = __builtin_amdgcn_readlane(looked_up, 2 * (it & 31));
       group[1] = __builtin_amdgcn_readlane(looked_up, 2 * (it & 31) + 1);
     };
-    // What to load for a step: a half that is not there reads the pool's first
-    // group, which every wavefront finds in the cache, and is masked.
-    const auto to_load = [](const int (&group)[2], int (&from)[2]) {
-      from[0] = max(group[0], 0);
-      from[1] = max(group[1], 0);
+    GroupBuffers from[2];
+    const auto to_load = [&](const int (&group)[2]) {
+      from[0] = group_buffers<FMT, DB>(a.cache, group[0]);
+      from[1] = group_buffers<FMT, DB>(a.cache, group[1]);
     };
 
     // K of the next step is loaded once this step's scores are formed, V of the
     // next once this step's V is in its operands: one tile of registers, and
-    // loads in flight all the time.  The last step loads its own tile again.
+    // loads in flight all the time.  The last step loads from empty buffers.
     Tile<FMT, DB> t;
-    int group[2], from[2];
+    int group[2];
     look_up(0, group);
-    to_load(group, from);
+    to_load(group);
     // (In the loop's own order, so that its waits count the same loads on entry.)
-    load_k<FMT, DB>(a.cache, from, lane, t);
+    load_k<FMT, DB>(from, lane, t);
     __builtin_amdgcn_sched_barrier(0);
-    load_v<FMT, DB>(a.cache, from, lane, t);
+    load_v<FMT, DB>(from, lane, t);
     __builtin_amdgcn_sched_barrier(0);
     float score_scale = a.scale * kLog2e * a.cache.k_scale;
     if constexpr (FMT == kKvNvfp4) {
@@ -601,7 +619,8 @@ __global__ __launch_bounds__(256 * waves_per_simd(FMT, DB), (waves_per_simd(FMT,
       const bool has0 = group[0] >= 0, has1 = group[1] >= 0;
       const bool whole = has0 && has1 && tok0 >= sp.begin && tok0 + kTile <= sp.end;
       if (it + 1 < count) look_up(it + 1, group);
-      to_load(group, from);
+      else group[0] = group[1] = -1;
+      to_load(group);
       uint32_t okbits = 0xffu;
       if (!whole) {
         okbits = 0;
@@ -626,7 +645,7 @@ __global__ __launch_bounds__(256 * waves_per_simd(FMT, DB), (waves_per_simd(FMT,
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[4 * half + i] = rounded_product(acc[i], score_scale);
       }
-      load_k<FMT, DB>(a.cache, from, lane, t);
+      load_k<FMT, DB>(from, lane, t);
       if (!whole) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = (okbits >> i) & 1u ? x[i] : kNegInf;
@@ -676,7 +695,7 @@ __global__ __launch_bounds__(256 * waves_per_simd(FMT, DB), (waves_per_simd(FMT,
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           op[j][i] = __builtin_amdgcn_perm(vt[2 * i + 1][j / 2], vt[2 * i][j / 2], j % 2 ? 0x07060302u : 0x05040100u);
-      load_v<FMT, DB>(a.cache, from, lane, t);
+      load_v<FMT, DB>(from, lane, t);
 #pragma unroll
       for (int j = 0; j < kW; ++j) {
         o[j] = mma<FMT>(op[j], hi, o[j]);
