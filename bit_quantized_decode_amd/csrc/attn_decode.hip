@@ -40,7 +40,15 @@ constexpr int kTile = 32;                  // tokens of a wavefront's step
 constexpr int kRows = 16;                  // query heads of a row tile
 constexpr int kCus = 256;
 constexpr int kLead = 3;                   // places before a unit's tiles
-constexpr int kShare = 6;                  // places of a workgroup's share, at least, if units are cut
+// Places of a workgroup's share, at least, if units are cut: a part for each adds to the
+// join what the share saves, so that the longest unit gets about as many parts as its join
+// reads in one round trip, within bounds; powers of two, for shifts.  (NVFP4, one kv head of
+// 128, shares of 4 / 9 / 16 / 32 / 64 places for 8 query heads: 4000 tokens 11.0 / 12.0 / 12.5 /
+// 14.3 / 17.9 us, 16,000 tokens 18.0 / 15.6 / 14.5 / 15.7 / 19.8, 131,072 tokens 32.1 / 32.3 /
+// 31.9 / 23.4 / 22.7.  Parts of 16 / 32 / 64 / 96 over 16,000 tokens: 1 query head 15.6 / 14.9 /
+// 13.0 / 12.8 us, 4 heads 14.8 / 13.5 / 13.3 / 14.3, 16 heads 16.6 / 17.4 / 21.5 / 26.5.)
+constexpr int kShareMinLog = 2, kShareMaxLog = 5, kPartsMinLog = 4, kPartsMaxLog = 6;
+constexpr int kJoinBatch = 12;             // parts that a thread of a join reads at once
 static_assert(kCus * 4 <= (int)kAttnCounterBytes, "one counter a workgroup");
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -61,7 +69,7 @@ struct AttnParams {
   unsigned* counters;
   float* part;         // partial sums, see part_offset()
   int64_t ldq, ldo, table_width;
-  int32_t batch, q_heads, group, row_tiles, window, part_rows, part_bytes;
+  int32_t batch, q_heads, group, row_tiles, window, part_rows, part_bytes, parts_log;
   float scale;
 };
 
@@ -325,11 +333,10 @@ __device__ __forceinline__ void add_part(float& top, float& sum, f32x4 (&acc)[N]
 
 // Joins the partial sums that workgroups wfirst .. wlast left of a unit.  The parts
 // are cut into runs over the threads that its values leave over; each thread adds
-// its run in workgroup order, kBatch parts a round trip to memory; the runs are
+// its run in workgroup order, kJoinBatch parts a round trip to memory; the runs are
 // then added in order through LDS (6 floats a thread).
 template <int DP, int kThreads>
 __device__ __forceinline__ void join_parts(const AttnParams& a, int wfirst, int wlast, int rows, int b, int q0, float* lds) {
-  constexpr int kBatch = 12;
   constexpr int kQuads = DP / 4;
   const int parts = wlast - wfirst + 1, items = rows * kQuads;
   const int runs = min(items >= kThreads ? 1 : kThreads / items, parts);
@@ -341,10 +348,10 @@ __device__ __forceinline__ void join_parts(const AttnParams& a, int wfirst, int 
     const int p0 = !live ? 0 : runs > 1 ? parts * run / runs : 0, p1 = !live ? 0 : runs > 1 ? parts * (run + 1) / runs : parts;
     float top = kNegInf, l = 0.0f;
     f32x4 acc[1] = {{0.0f, 0.0f, 0.0f, 0.0f}};
-    for (int i = p0; i < p1; i += kBatch) {
-      f32x4 ml[kBatch], v[kBatch][1];
+    for (int i = p0; i < p1; i += kJoinBatch) {
+      f32x4 ml[kJoinBatch], v[kJoinBatch][1];
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
+      for (int j = 0; j < kJoinBatch; ++j) {
         if (i + j < p1) {
           const int from = part_offset<DP>(a, wfirst + i + j, i + j == 0 ? 1 : 0, r);
           ml[j] = load_part(buf, from);
@@ -352,7 +359,7 @@ __device__ __forceinline__ void join_parts(const AttnParams& a, int wfirst, int 
         }
       }
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j)
+      for (int j = 0; j < kJoinBatch; ++j)
         if (i + j < p1) add_part<1>(top, l, acc, ml[j][0], ml[j][1], v[j]);
     }
     if (runs > 1) {
@@ -410,6 +417,18 @@ template <int CTRL, int ROWS>
 __device__ __forceinline__ int add_lanes(int v) {
   return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xf, true);
 }
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int max_lanes(int v) {
+  return max(v, __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xf, true));
+}
+__device__ __forceinline__ int lane_max(int v) {  // of values >= 0, in the last lane
+  v = max_lanes<0x111, 0xf>(v);
+  v = max_lanes<0x112, 0xf>(v);
+  v = max_lanes<0x114, 0xf>(v);
+  v = max_lanes<0x118, 0xf>(v);
+  v = max_lanes<0x142, 0xa>(v);
+  return max_lanes<0x143, 0xc>(v);
+}
 __device__ __forceinline__ int lane_scan(int v) {
   v = add_lanes<0x111, 0xf>(v);  // row_shr:1, 2, 4, 8
   v = add_lanes<0x112, 0xf>(v);
@@ -461,20 +480,29 @@ __global__ __launch_bounds__(256 * waves_per_simd(FMT, DB), (waves_per_simd(FMT,
     win_mine = win_unit * units_per_row;
     win_upto = lane_scan(win_mine);
   };
-  int mine, upto;                           // of each lane's `per` rows
+  int mine, upto, longest;                  // of each lane's `per` rows
   if (per == 1) {
     move_window(0, 0);
     mine = win_mine;
     upto = win_upto;
+    longest = win_unit;
   } else {
-    mine = 0;
+    mine = longest = 0;
 #pragma unroll 4
-    for (int i = 0; i < per; ++i) mine += places_in(lane * per + i, len_of(lane * per + i)) * units_per_row;
+    for (int i = 0; i < per; ++i) {
+      const int unit = places_in(lane * per + i, len_of(lane * per + i));
+      mine += unit * units_per_row;
+      longest = max(longest, unit);
+    }
     upto = lane_scan(mine);
   }
   const int total = __builtin_amdgcn_readlane(upto, 63);
+  // (The nearest power of two, of places in one of 2^parts_log parts.)
+  const unsigned longest_unit = (unsigned)__builtin_amdgcn_readlane(lane_max(longest), 63);
+  const int share_log =
+      min(max(31 - __builtin_clz((longest_unit + longest_unit / 2) >> a.parts_log | 1u), kShareMinLog), kShareMaxLog);
   const int w = blockIdx.x;
-  const Cut shares = cut_of(total, min((int)gridDim.x, max(total / kShare, a.batch * units_per_row)));
+  const Cut shares = cut_of(total, min((int)gridDim.x, max(total >> share_log, a.batch * units_per_row)));
   if (w >= shares.n) return;
   // The row that holds a place, where it starts and how long its units are; the
   // window moves there if it is elsewhere.
@@ -840,7 +868,7 @@ int64_t places_of(const AttnLaunch& a) {
 // Workgroups of a launch: one a CU, or fewer if the longest possible lengths have
 // no work for them.
 int workgroups_of(const AttnLaunch& a) {
-  const int64_t shares = places_of(a) / kShare, units = a.batch * a.cache.heads * row_tiles_of(a);
+  const int64_t shares = places_of(a) >> kShareMinLog, units = a.batch * a.cache.heads * row_tiles_of(a);
   const int64_t all = shares > units ? shares : units;
   return (int)(all < kCus ? all : kCus);
 }
@@ -853,6 +881,15 @@ int part_rows_of(const AttnLaunch& a) {
 size_t part_bytes_of(const AttnLaunch& a) {
   const size_t dp = (size_t)((a.cache.head_dim + 63) / 64) * 64;
   return (size_t)workgroups_of(a) * 2 * part_rows_of(a) * (dp + 4) * sizeof(float);
+}
+
+// Of the parts that a unit is cut into (see kShareMinLog): the power of two nearest to
+// those that its join reads in one round trip.
+int parts_log_of(const AttnLaunch& a) {
+  const int quads = (a.cache.head_dim + 63) / 64 * 16;
+  const int trip = kJoinBatch * (64 * waves_of(a) / (part_rows_of(a) * quads));
+  const int log = 31 - __builtin_clz((unsigned)(trip + trip / 2) | 1u);
+  return log < kPartsMinLog ? kPartsMinLog : log > kPartsMaxLog ? kPartsMaxLog : log;
 }
 
 template <int FMT, int DB>
@@ -876,6 +913,7 @@ void attn_launch(const AttnLaunch& a, hipStream_t s) {
   p.window = a.window;
   p.part_rows = part_rows_of(a);
   p.part_bytes = (int32_t)part_bytes_of(a);
+  p.parts_log = parts_log_of(a);
   p.scale = a.scale;
   hipLaunchKernelGGL((attn_kernel<FMT, DB>), dim3((unsigned)workgroups_of(a)), dim3(64 * waves_of(a)), 0, s, p);
 }
