@@ -384,9 +384,14 @@ __device__ __forceinline__ void join_parts(const AttnParams& a, int wfirst, int 
   }
 }
 
-// Wavefronts a SIMD that the registers leave room for; a workgroup fills a CU.
+// Wavefronts a SIMD; a workgroup fills a CU.  Two keep enough loads in flight, and more
+// only make the joins longer: 8 users of up to 4608 tokens of 64-wide E4M3 heads 11.1 us with
+// two, 11.3 with one, 12.2 with four; one user over 40,000 tokens of 128-wide NVFP4 heads 17.1,
+// 20.6, 17.9 with three.  Narrow NVFP4 heads, with the fewest bytes a step, want three: 32 users over
+// 16,384 tokens 61.3 us with two, 55.7 with three, 54.7 with four (and 8 users over up to
+// 8192: 12.5, 13.3, 14.3).  Wide bf16 heads have registers for one.
 constexpr int waves_per_simd(int fmt, int db) {
-  return fmt == kKvBf16 ? (db == 1 ? 4 : db == 4 ? 1 : 2) : db == 1 ? 4 : db == 2 ? 3 : 2;
+  return fmt == kKvBf16 && db == 4 ? 1 : fmt == kKvNvfp4 && db == 1 ? 3 : 2;
 }
 
 // The line cut into n runs of nearly equal length, the first `more` one longer.
