@@ -22,14 +22,24 @@
 //
 // Work split.  The 32-token tiles of all units (sequence, kv head, row tile) form
 // one line, each unit led by kLead blank places for what starting it costs.
-// The line is cut evenly over the workgroups (one a CU), cuts inside a short unit
-// moved to its nearer end, and each share over the wavefronts, whatever the
-// lengths are.  A wavefront walks its run of the line
-// by itself: it writes the units that lie inside its run, leaves the end of a
-// unit begun by an earlier wavefront in LDS, and keeps the beginning of one that
-// goes on in registers.  Once all are through, each beginning is joined with
-// what follows it in LDS.  What goes on in another workgroup becomes a partial
-// sum in memory, and the last workgroup of a unit to arrive joins those, in order.
+// The line is cut evenly over the workgroups (one a CU, fewer if little is to be done), cuts
+// inside a short unit moved to its nearer end, and each share over the wavefronts, whatever
+// the lengths are.  A wavefront walks its run of the line by itself: it writes the units
+// that lie inside its run, leaves the end of a unit begun by an earlier wavefront in
+// LDS, and keeps the beginning of one that goes on in registers.  Once all are
+// through, each beginning is joined with what follows it in LDS.  What goes on in
+// another workgroup becomes a partial sum in memory, and the last workgroup of a unit to
+// arrive joins those, in order.
+//
+// Bound by the cache's bytes where they are many, by a fixed 8 us where they are few: the
+// launch (3 us), lengths, page table and first tile, each waiting for the one before (3 us), and
+// the way of partial sums through memory (2 to 4 us).  8 kv heads of 128 for 40 query heads:
+// one user over 131,072 tokens bf16 85.3 us (537 MB, 6.3 TB/s); 32 users over up to 16,384
+// tokens NVFP4 50-55 us (274-308 MB, 5.5 TB/s); over 8192 each 51 us (302 MB, 5.9 TB/s);
+// one user over 100 / 1000 / 8000 tokens 7.0 / 9.3 / 12.1 us.  A streaming read runs at 6.65.
+// Non-temporal loads: 32 users of 16,384 NVFP4 tokens 96 us against 112, one of 131,072 bf16
+// tokens 90 against 100 (a cache that still lies in the MALL reads up to 5 % slower).  Page
+// sizes of 16 to 2048 tokens, in order or not, read alike.
 #include "attn_launchers.h"
 #include "device_common.h"
 
@@ -39,7 +49,9 @@ namespace {
 constexpr int kTile = 32;                  // tokens of a wavefront's step
 constexpr int kRows = 16;                  // query heads of a row tile
 constexpr int kCus = 256;
-constexpr int kLead = 3;                   // places before a unit's tiles
+// Places before a unit's tiles.  (With 2: 32 ragged users of NVFP4 52-56 us against 50-55;
+// with 4: 256 users of up to 512 tokens 23.0-24.4 us against 21.8-23.0.)
+constexpr int kLead = 3;
 // Places of a workgroup's share, at least, if units are cut: a part for each adds to the
 // join what the share saves, so that the longest unit gets about as many parts as its join
 // reads in one round trip, within bounds; powers of two, for shifts.  (NVFP4, one kv head of
@@ -526,7 +538,9 @@ __global__ __launch_bounds__(256 * waves_per_simd(FMT, DB), (waves_per_simd(FMT,
                __builtin_amdgcn_readlane(win_unit, at)};
   };
   // The workgroup's share [s0, s1), an end moved to a unit's end if that unit is
-  // short; the wavefront's run [g0, g1) of it, and the row where that starts.
+  // short; the wavefront's run [g0, g1) of it, and the row where that starts.  (Short: up
+  // to two tiles a wavefront.  With one, 256 users of up to 512 tokens take 24.6 us against
+  // 21.8; with three, one user over 600 tokens 10.0 us against 9.0.)
   int s0 = 0, s1 = 0, g0 = 0, g1 = 0;
   Cut runs{kWaves, 0, 0};
   Row r0{0, 0, 1};
