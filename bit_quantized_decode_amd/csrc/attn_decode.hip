@@ -332,14 +332,12 @@ __device__ __forceinline__ void write_out(const AttnParams& a, int b, int qh, in
 }
 
 // Adds (m, l, v) to running sums under the larger reference.
-template <int N>
-__device__ __forceinline__ void add_part(float& top, float& sum, f32x4 (&acc)[N], float m, float l, const f32x4 (&v)[N]) {
+__device__ __forceinline__ void add_part(float& top, float& sum, f32x4& acc, float m, float l, f32x4 v) {
   const float next = fmaxf(top, m);
   const float fo = top == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(top - next);
   const float fi = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m - next);
   sum = sum * fo + l * fi;
-#pragma unroll
-  for (int u = 0; u < N; ++u) acc[u] = acc[u] * fo + v[u] * fi;
+  acc = acc * fo + v * fi;
   top = next;
 }
 
@@ -359,20 +357,20 @@ __device__ __forceinline__ void join_parts(const AttnParams& a, int wfirst, int 
     const int r = live ? item / kQuads : 0, d = live ? 4 * (item - r * kQuads) : 0;
     const int p0 = !live ? 0 : runs > 1 ? parts * run / runs : 0, p1 = !live ? 0 : runs > 1 ? parts * (run + 1) / runs : parts;
     float top = kNegInf, l = 0.0f;
-    f32x4 acc[1] = {{0.0f, 0.0f, 0.0f, 0.0f}};
+    f32x4 acc{0.0f, 0.0f, 0.0f, 0.0f};
     for (int i = p0; i < p1; i += kJoinBatch) {
-      f32x4 ml[kJoinBatch], v[kJoinBatch][1];
+      f32x4 ml[kJoinBatch], v[kJoinBatch];
 #pragma unroll
       for (int j = 0; j < kJoinBatch; ++j) {
         if (i + j < p1) {
           const int from = part_offset<DP>(a, wfirst + i + j, i + j == 0 ? 1 : 0, r);
           ml[j] = load_part(buf, from);
-          v[j][0] = load_part(buf, from + (4 + d) * 4);
+          v[j] = load_part(buf, from + (4 + d) * 4);
         }
       }
 #pragma unroll
       for (int j = 0; j < kJoinBatch; ++j)
-        if (i + j < p1) add_part<1>(top, l, acc, ml[j][0], ml[j][1], v[j]);
+        if (i + j < p1) add_part(top, l, acc, ml[j][0], ml[j][1], v[j]);
     }
     if (runs > 1) {
       float* mine = lds + (run * items + item) * 6;
@@ -381,18 +379,17 @@ __device__ __forceinline__ void join_parts(const AttnParams& a, int wfirst, int 
         mine[0] = top;
         mine[1] = l;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) mine[2 + j] = acc[0][j];
+        for (int j = 0; j < 4; ++j) mine[2 + j] = acc[j];
       }
       __syncthreads();
       if (live && run == 0) {
         for (int i = 1; i < runs; ++i) {
           const float* other = lds + (i * items + item) * 6;
-          const f32x4 v[1] = {{other[2], other[3], other[4], other[5]}};
-          add_part<1>(top, l, acc, other[0], other[1], v);
+          add_part(top, l, acc, other[0], other[1], f32x4{other[2], other[3], other[4], other[5]});
         }
       }
     }
-    if (live && (runs == 1 || run == 0)) write_out(a, b, q0 + r, d, top, l, acc[0]);
+    if (live && (runs == 1 || run == 0)) write_out(a, b, q0 + r, d, top, l, acc);
   }
 }
 
