@@ -535,9 +535,13 @@ __global__ __launch_bounds__(256 * waves_per_simd(FMT, DB), (waves_per_simd(FMT,
                __builtin_amdgcn_readlane(win_unit, at)};
   };
   // The workgroup's share [s0, s1), an end moved to a unit's end if that unit is
-  // short; the wavefront's run [g0, g1) of it, and the row where that starts.  (Short: up
-  // to two tiles a wavefront.  With one, 256 users of up to 512 tokens take 24.6 us against
-  // 21.8; with three, one user over 600 tokens 10.0 us against 9.0.)
+  // short; the wavefront's run [g0, g1) of it, and the row where that starts.  (Short:
+  // where units are about as many as workgroups, up to two tiles a wavefront; where
+  // they are fewer, cutting gives work to idle CUs, and short is less.  64 users of up to
+  // 300 tokens, 4 kv heads of 192: 14.5 us with one tile a wavefront, 11.7 with two; 8 users of up
+  // to 768 tokens: 9.7 and 12.5.  256 users of up to 512 tokens, 8 heads of 128: 24.6 and 21.8.
+  // Heads of 64 are quicker to read than to join: 8 users of up to 400 tokens 7.7 and 7.0.)
+  const int short_unit = kLead + (2 * a.batch * units_per_row >= kCus ? 2 * kWaves : DB == 1 ? 16 : 8);
   int s0 = 0, s1 = 0, g0 = 0, g1 = 0;
   Cut runs{kWaves, 0, 0};
   Row r0{0, 0, 1};
@@ -552,7 +556,7 @@ __global__ __launch_bounds__(256 * waves_per_simd(FMT, DB), (waves_per_simd(FMT,
     const int place = k == 2 ? g0 : run_start(shares, w + k);
     r0 = row_at(min(place, total - 1));
     const int into = (int)((unsigned)(place - r0.start) % (unsigned)r0.unit);
-    const bool moved = k < 2 && place < total && r0.unit <= kLead + 2 * kWaves;
+    const bool moved = k < 2 && place < total && r0.unit <= short_unit;
     const int end = !moved ? place : 2 * into < r0.unit ? place - into : place - into + r0.unit;
     if (k == 0) s0 = end;
     else if (k == 1) s1 = end;
