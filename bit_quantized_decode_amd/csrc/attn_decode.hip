@@ -311,13 +311,14 @@ __device__ __forceinline__ float rounded_product(float a, float b) {
 
 __device__ __forceinline__ float lane_xor(float v, int off) { return __shfl_xor(v, off); }
 
-// f16 probabilities are held 2^kOffset above the reference, so that small ones
-// keep bits down to 2^-24 * 2^-kOffset of the largest; with the slack they
-// stay below 2^15.  bf16 has fp32's range and needs no offset.
+// f16 probabilities are held 2^kOffset above the reference, and stay below
+// 2^(kOffset + kSlack) = 2^15.  Those under 2^-14 lose bits: a term below 2^-25 of the
+// largest is taken to within 2^-36 of that (half of f16's last step, 2^-25, under the
+// offset).  bf16 has fp32's range and needs no offset.
 template <int FMT>
 struct Softmax {
-  static constexpr float kOffset = FMT == kKvNvfp4 ? 7.0f : 0.0f;
-  static constexpr float kSlack = 8.0f;
+  static constexpr float kOffset = FMT == kKvNvfp4 ? 11.0f : 0.0f;
+  static constexpr float kSlack = FMT == kKvNvfp4 ? 4.0f : 8.0f;
 };
 
 // Four outputs of row `qh` of sequence b from their sums, and (d == 0) its lse.
@@ -709,7 +710,9 @@ __global__ __launch_bounds__(256 * waves_per_simd(FMT, DB), (waves_per_simd(FMT,
       if (__any(top - ref > Softmax<FMT>::kOffset + Softmax<FMT>::kSlack)) {
         top = fmaxf(top, lane_xor(top, 16));
         top = fmaxf(top, lane_xor(top, 32));
-        const float next = fmaxf(ref, top - Softmax<FMT>::kOffset);
+        // (Scores past 2^27 have steps of 16 and more: the offset may round past the range.)
+        const float below = top - Softmax<FMT>::kOffset;
+        const float next = fmaxf(ref, top - below > Softmax<FMT>::kOffset + Softmax<FMT>::kSlack ? top : below);
         const float alpha = next == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(ref - next);
         ref = next;
         shift = ref == kNegInf ? 0.0f : ref;

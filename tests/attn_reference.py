@@ -91,12 +91,16 @@ def attend(q, k, v, scale):
     return p @ v / total, (m + np.log(total))[:, 0], p @ np.abs(v) / total, size
 
 
-def attend_bounds(size, n, d, o, pv, lse, fmt):
+def attend_bounds(size, n, d, o, pv, lse, fmt, v=None):
     """How far a bf16 output and an fp32 lse may be off.
 
     Scores: d exact products summed in fp32, then a product and a sum: (d + 4) half steps of sum |q k|.  A term
     exp(s - m) is off by that, by four half steps of the exponential, and by its rounding for the matrix cores (two bf16
-    parts, 2^-17; for format 2 one f16 number, 2^-12); sums over n tokens by n half steps.  A quotient of two such sums is off by twice as much of sum p |v|; then one rounding to bf16."""
+    parts, 2^-17; for format 2 one f16 number, 2^-12); sums over n tokens by n half steps.  A quotient of two such sums is off by twice as much of sum p |v|; then one rounding to bf16.
+    An f16 number's last step is 2^-24, and the row's largest term is held at 2^11 or more: smaller terms are off by half
+    a step, 2^-36 of the largest, however small they are.  The sum of terms is at least the largest, so that with the
+    values given ([n][d]) this comes to 2^-36 sum |v| at most."""
     ds = (d + 4) * U24 * size
     term = ds + 4 * U24 + (2.0 ** -12 if fmt == 2 else 2.0 ** -17) + (n + 8) * U24
-    return 2.0 ** -8 * np.abs(o) + 2 * term[:, None] * pv + 1e-30, ds + (n + 8) * U24 + 4 * U24 * (1 + np.abs(np.where(np.isfinite(lse), lse, 0)))
+    small = 2.0 ** -36 * np.abs(v).sum(0) if fmt == 2 and v is not None else 0.0
+    return 2.0 ** -8 * np.abs(o) + 2 * term[:, None] * pv + small + 1e-30, ds + (n + 8) * U24 + 4 * U24 * (1 + np.abs(np.where(np.isfinite(lse), lse, 0)))

@@ -59,7 +59,7 @@ class Batch:
             for h in range(self.hk):
                 rows = slice(h * g, (h + 1) * g)
                 o, l, pv, size = R.attend(self.q[b, rows].double().numpy(), self.k[start + j, h], self.v[start + j, h], scale)
-                bo, bl = R.attend_bounds(size, len(j), self.d, o, pv, l, self.fmt)
+                bo, bl = R.attend_bounds(size, len(j), self.d, o, pv, l, self.fmt, self.v[start + j, h])
                 empty = np.isneginf(l)
                 assert np.array_equal(np.isneginf(lse[b, rows]), empty), (what, b, h)
                 err = np.abs(out[b, rows] - o)
@@ -222,6 +222,24 @@ def test_scores_far_beyond_the_exponentials_range(fmt, shift):
                 bound += 2.0 ** -11 * np.abs(rows).mean(0)
             assert (np.abs(out[b, h] - o) <= bound).all(), (b, h)
             assert abs(lse[b, h] - s.max()) <= 2.0 ** -20 * abs(s.max())
+
+
+@pytest.mark.parametrize("fmt", FORMATS, ids=IDS)
+@pytest.mark.parametrize("gap", [10, 20, 25, 28, 31, 34, 36, 40, 60])
+def test_terms_far_below_the_largest(fmt, gap):
+    """A token at the maximum whose values are zero, and some 2^-gap of it or less that make up the whole output."""
+    dev = device()
+    x = Batch(dev, fmt, [40], 1, 1, 64, 64)
+    k, v = torch.zeros(40, 1, 64), torch.randn(40, 1, 64, generator=torch.Generator().manual_seed(gap)).to(torch.bfloat16)
+    k[7, 0, 0], k[30:, 0, 0] = 6.0, -0.5
+    v[7] = 0.0
+    slots = (x.table[0].long()[torch.arange(40, device=dev) // 64] * 64 + torch.arange(40, device=dev) % 64)
+    B.kv_append(x.cache, k.to(torch.bfloat16).to(dev), v.to(dev), slots)
+    x.k, x.v = R.stored(k.numpy(), fmt), R.stored(v.float().numpy(), fmt)
+    x.q = torch.zeros(1, 1, 64, dtype=torch.bfloat16)
+    x.q[0, 0, 0] = 1.0
+    scale = gap * np.log(2) / 6
+    x.check(*x.call(scale=scale), scale=scale)
 
 
 def test_small_terms_add_up():
