@@ -911,7 +911,8 @@ def _attn(q, cache, page_table, seq_lens, scale, window, out, lse, ws, stream, p
 
 def attn_decode_prepared(q, cache, page_table, seq_lens, scale=None, window=0, out=None, lse=None, ws=None, stream=None):
     """attn_decode() with its arguments marshalled once and a workspace of its own: returns a zero-argument callable
-    that returns what attn_decode() does.  Its calls, and replays of graphs that captured them, must not overlap."""
+    that returns what attn_decode() does.  Its calls, and replays of graphs that captured them, must not overlap.
+    The workspace is zeroed on the stream that is current here: a call on another waits for that one."""
     return _attn(q, cache, page_table, seq_lens, scale, window, out, lse, ws, stream, True)
 
 
