@@ -16,9 +16,12 @@
 // Operands.  bf16 and E4M3 caches multiply as bf16 (every E4M3 value times its
 // power of two is a bf16 number), NVFP4 as f16 (E2M1 times E4M3 is an f16
 // number); the queries, bf16, are shifted into f16's range by a power of two
-// per row.  Probabilities enter as one f16 number (half a step: 2^-12, an eighth
+// per row.  Probabilities enter as one f16 number (half a step: 2^-11, an eighth
 // of the output's own rounding) or as the sum of two bf16 numbers (2^-17; one
 // alone would add as much as the output's rounding); everything else is fp32.
+// (Two f16 numbers would take 2^-22.  Against one: 32 users of 8192 NVFP4 tokens 52.8-53.4 us
+// against 50.6-50.9, 256 of up to 512 tokens 24.1-24.5 against 22.0-23.3, and an output no
+// nearer to 64 bits, as its rounding to bf16 is the larger by far.)
 //
 // Work split.  The 32-token tiles of all units (sequence, kv head, row tile) form
 // one line, each unit led by kLead blank places for what starting it costs.

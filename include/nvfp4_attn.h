@@ -187,8 +187,9 @@ int nvfp4_kv_read(const nvfp4_kv_cache* cache /* host */, const int64_t* slots, 
  *
  * Scores, maxima, sums and outputs are held in fp32.  The exp() terms enter the
  * matrix cores rounded to within 2^-17 of each (bf16 and E4M3 caches: the sum of
- * two bf16 numbers) or 2^-12 (NVFP4: one f16 number; a term below 2^-25 of the
- * row's largest to within 2^-36 of that); their sum takes them whole.
+ * two bf16 numbers) or 2^-11 (NVFP4: one f16 number, an eighth of the rounding
+ * of o to bf16; a term below 2^-25 of the row's largest to within 2^-36 of that);
+ * their sum takes them whole.
  * o is bf16, rounded once; out overlaps no input.  The work is split evenly over the GPU along all
  * sequences' lengths, whatever their mix, and joined in a fixed order.
  *
