@@ -11,7 +11,8 @@
 // query q, which is exactly the k split of the second product O^T = V^T P^T, so
 // probabilities go from one to the other inside their lane.  Because a lane belongs to
 // one query, the reference and the sum are lane values; the reference only
-// moves when a score passes it by 2^kSlack, and only then do lanes talk.
+// moves when a term would pass 2^kSlack times the one that it was set by, and only
+// then do lanes talk.
 //
 // Operands.  bf16 and E4M3 caches multiply as bf16 (every E4M3 value times its
 // power of two is a bf16 number), NVFP4 as f16 (E2M1 times E4M3 is an f16
@@ -314,13 +315,14 @@ __device__ __forceinline__ float rounded_product(float a, float b) {
 
 __device__ __forceinline__ float lane_xor(float v, int off) { return __shfl_xor(v, off); }
 
-// f16 probabilities are held 2^kOffset above the reference, and stay below
-// 2^(kOffset + kSlack) = 2^15.  Those under 2^-14 lose bits: a term below 2^-25 of the
-// largest is taken to within 2^-36 of that (half of f16's last step, 2^-25, under the
-// offset).  bf16 has fp32's range and needs no offset.
+// The largest term is set to 2^kOffset, and none passes 2^(kOffset + kSlack).  f16: 2^15;
+// terms under 2^-14 lose bits: one below 2^-25 of the largest is taken to within 2^-36 of that
+// (half of f16's last step, 2^-25, under the offset).  bf16 has fp32's range: no term passes 1,
+// so that sums of n terms stay below n times the largest value, as the definition's do
+// (with terms up to 2^8, values from 2^119 / n on gave infinity; same times).
 template <int FMT>
 struct Softmax {
-  static constexpr float kOffset = FMT == kKvNvfp4 ? 11.0f : 0.0f;
+  static constexpr float kOffset = FMT == kKvNvfp4 ? 11.0f : -8.0f;
   static constexpr float kSlack = FMT == kKvNvfp4 ? 4.0f : 8.0f;
 };
 

@@ -189,7 +189,9 @@ int nvfp4_kv_read(const nvfp4_kv_cache* cache /* host */, const int64_t* slots, 
  * matrix cores rounded to within 2^-17 of each (bf16 and E4M3 caches: the sum of
  * two bf16 numbers) or 2^-11 (NVFP4: one f16 number, an eighth of the rounding
  * of o to bf16; a term below 2^-25 of the row's largest to within 2^-36 of that);
- * their sum takes them whole.
+ * their sum takes them whole.  No term of a bf16 or E4M3 cache is above 1: sums
+ * over n tokens stay finite for values up to 2^127 / n.  Its terms keep those
+ * 2^-17 down to 2^-100 of the row's largest.
  * o is bf16, rounded once; out overlaps no input.  The work is split evenly over the GPU along all
  * sequences' lengths, whatever their mix, and joined in a fixed order.
  *

@@ -46,3 +46,44 @@ def test_rounding_of_a_weight(fmt):
         bound = weight * 6 * p / (1 + p) + ((HEAD + 4) * 6 * scale + 8) * R.U24 * 2 * (3 + 6 * p) / (1 + p) + 2.0 ** -8 * abs(o)
         got = B.attn_decode(q, cache, table, length, scale=scale)[0, 0].double().cpu().numpy()
         assert (np.abs(got - o) <= bound).all(), (j, got[0], o, bound)
+
+
+@pytest.mark.parametrize("fmt", FORMATS[:2], ids=IDS[:2])
+@pytest.mark.parametrize("rise", [0.0, 7.9, 300.0])
+def test_largest_values(fmt, rise):
+    """Values of 2^127 / n, the first 32 of n tokens `rise` (in base 2) below the others: sums of n terms stay finite.
+
+    As many sequences as fill the GPU, so that a wavefront takes a whole one and meets the rise inside its run.  All weights add up
+    to one: each output is its column's value, within its rounding, the terms' and those of two sums of n."""
+    dev = device()
+    n, b = 512, 2048
+    m = 2.0 ** 127 / n
+    k, v = torch.zeros(n, HEAD), torch.full((n, HEAD), m)
+    k[32:, 0] = 1.0
+    v[:, 1::2] = -m / 2
+    cache, table = one_sequence(dev, fmt, k, v)
+    q = torch.zeros(b, 1, HEAD, dtype=torch.bfloat16, device=dev)
+    q[:, 0, 0] = 1.0
+    scale = float(np.float32(max(rise, 1e-6) * np.log(2)))
+    out, lse = B.attn_decode(q, cache, table.expand(b, -1).contiguous(), torch.full((b,), n, dtype=torch.int32, device=dev),
+                             scale=scale, lse=True)
+    want = v[0].double().numpy()
+    err = np.abs(out[:, 0].double().cpu().numpy() - want)
+    assert (err <= (2.0 ** -8 + 2 * (2.0 ** -17 + (n + 8) * R.U24)) * np.abs(want)).all(), err.max() / m
+    exact = scale + np.log(n - 32 + 32 * np.exp(-scale))
+    assert (np.abs(lse.double().cpu().numpy() - exact) <= (n + 16) * R.U24 * (1 + exact)).all()
+
+
+@pytest.mark.parametrize("fmt", FORMATS[:2], ids=IDS[:2])
+@pytest.mark.parametrize("n", [1, 3])
+def test_smallest_values(fmt, n):
+    """Values down to the formats' smallest normal ones (2^-126, and 2^-119 of E4M3), equal for all tokens: products with terms
+    of 2^-8 and more keep 15 bits below 2^-126, which leaves each output within a step of bf16."""
+    dev = device()
+    small = 2.0 ** -126 if fmt == B.NVFP4_KV_BF16 else 2.0 ** -119
+    v = (torch.arange(1, HEAD + 1) % 2 + 1.0).mul(small).expand(n, HEAD).contiguous()
+    cache, table = one_sequence(dev, fmt, torch.zeros(n, HEAD), v)
+    out = B.attn_decode(torch.ones(1, 1, HEAD, dtype=torch.bfloat16, device=dev), cache, table,
+                        torch.tensor([n], dtype=torch.int32, device=dev))
+    want = v[0].double().numpy()
+    assert (np.abs(out[0, 0].double().cpu().numpy() - want) <= 2.0 ** -7 * want).all()
