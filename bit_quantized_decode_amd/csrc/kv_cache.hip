@@ -64,6 +64,12 @@ __device__ __forceinline__ void encode16(const float (&v)[16], uint32_t amax, fl
       p = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i + 2] * inv, v[4 * i + 3] * inv, p, true);
       w[i] = finite ? (uint32_t)p : 0x7f7f7f7fu;
     }
+    // Under the largest exponent the code 0x78 (256) would stand for 2^128: it becomes 0x77 (240), the
+    // largest finite value.  (No code is above 0x78 there: adding 8 carries into the sign's bit for 0x78 alone.)
+    if (e == kKvE4m3MaxExp) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] -= ((w[i] & 0x7f7f7f7fu) + 0x08080808u) >> 7 & 0x01010101u;
+    }
     scale = (uint32_t)(e + kKvE4m3Bias);
   } else {
     const float q = __uint_as_float(amax) / (6.0f * st);

@@ -34,6 +34,7 @@ enum { kKvBf16 = 0, kKvE4m3 = 1, kKvNvfp4 = 2 };
 constexpr int kKvGroup = 16;  // tokens of a group
 constexpr int kKvE4m3Bias = 127;
 constexpr int kKvE4m3MinExp = -110;  // the smallest exponent of an E4M3 row: every value stays a normal bf16
+constexpr int kKvE4m3MaxExp = 120;   // the largest: that of a row up to fp32's maximum
 
 template <int FMT, int DB>
 struct KvLayout {

@@ -100,8 +100,9 @@ int nvfp4_rope(const nvfp4_rope_args* args /* host */, void* stream);
  *   NVFP4_KV_BF16   bf16, rounded to nearest even (2 bytes a value);
  *   NVFP4_KV_E4M3   codes e4m3(v / X) with X the smallest power of two for which
  *                   the largest |v| / X is at most 448, its exponent at least
- *                   -110 (-110 for a zero row) (1 byte a value + 1 a row).  A row
- *                   with an infinity or NaN reads back as NaN throughout;
+ *                   -110 (-110 for a zero row) (1 byte a value + 1 a row); codes that
+ *                   would stand for 2^128 saturate at the largest finite, 1.875 *
+ *                   2^127.  A row with an infinity or NaN reads back as NaN throughout;
  *   NVFP4_KV_NVFP4  nvfp4_quantize()'s rule with the tensor scale given (k_scale,
  *                   v_scale): per 16 values a scale E4M3FN nearest to
  *                   amax / (6 s_t), codes E2M1 nearest to |v| / (e4m3(scale) s_t)
