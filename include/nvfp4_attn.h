@@ -180,9 +180,12 @@ int nvfp4_kv_read(const nvfp4_kv_cache* cache /* host */, const int64_t* slots, 
  * A page id outside [0, pages) holds nothing: its tokens are left out of the sums
  * (an evicted page: -1).  A row left with no token, or only with scores of -inf,
  * gives zeros and lse = -inf.  Table entries past a sequence's last page are not
- * looked at, cache slots past its length have no effect whatever they hold.  An
- * infinity or NaN in a query, or in a token that a row attends to, gives that
- * head's row infinities or NaN, and so do scores past fp32's range.
+ * looked at, cache slots past its length have no effect whatever they hold.
+ * Infinities and NaN that a row attends to act as in the formulas: a query's or
+ * key's make the scores that they enter infinite or NaN (a product with zero), and
+ * so do scores past fp32's range; a token of score -inf weighs nothing, one of
+ * score +inf or NaN makes its query head's row and lse NaN.  A value's make the
+ * outputs that they enter infinite or NaN, even where the token weighs nothing.
  * Several rows may share pages: a few new tokens of one sequence are rows with
  * the same table and lengths n, n + 1, ...
  *
