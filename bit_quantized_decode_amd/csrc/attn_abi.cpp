@@ -92,7 +92,7 @@ nvfp4::KvCache cache_of(const nvfp4_kv_cache* c) {
   const int db = (int)((c->head_dim + 63) / 64);
   const size_t code_bytes = nvfp4::kv_code_bytes(c->format, db);
   r.codes = static_cast<uint8_t*>(c->pool);
-  r.scales = r.codes + (size_t)groups_of(c) * code_bytes;
+  r.scales = r.codes ? r.codes + (size_t)groups_of(c) * code_bytes : nullptr;  // no pool: sizes only
   r.slots = c->pages * c->page_size;
   r.pages = (int32_t)c->pages;
   r.heads = (int32_t)c->kv_heads;
