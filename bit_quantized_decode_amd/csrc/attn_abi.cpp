@@ -138,7 +138,7 @@ int check_attn(const nvfp4_attn_args* a, bool need_buffers) {
   if (!nvfp4::attn_fits(attn_of(a)))
     return fail(NVFP4_ERR_SHAPE, "batch x query rows x table too large: the call would have 2^31 tiles of 32 tokens or more");
   if (!need_buffers || a->batch == 0) return NVFP4_OK;
-  if (!(a->scale > 0.0f) || !std::isfinite(a->scale)) return fail(NVFP4_ERR_ARG, "scale must be positive and finite");
+  if (!(a->scale > 0.0f && a->scale <= 0x1p127f)) return fail(NVFP4_ERR_ARG, "scale must be positive and at most 2^127");
   NVFP4_TRY(check_ld(a->ldq, a->q_heads * a->cache->head_dim, "ldq"));
   NVFP4_TRY(check_ld(a->ldo, a->q_heads * a->cache->head_dim, "ldo"));
   if (!a->q || !a->out || !a->seq_lens || (a->table_width > 0 && !a->page_table))

@@ -44,6 +44,8 @@
 // Non-temporal loads: 32 users of 16,384 NVFP4 tokens 96 us against 112, one of 131,072 bf16
 // tokens 90 against 100 (a cache that still lies in the MALL reads up to 5 % slower).  Page
 // sizes of 16 to 2048 tokens, in order or not, read alike.
+#include <cmath>
+
 #include "attn_launchers.h"
 #include "device_common.h"
 
@@ -66,9 +68,10 @@ constexpr int kLead = 3;
 constexpr int kShareMinLog = 2, kShareMaxLog = 5, kPartsMinLog = 4, kPartsMaxLog = 6;
 constexpr int kJoinBatch = 12;             // parts that a thread of a join reads at once
 static_assert(kCus * 4 <= (int)kAttnCounterBytes, "one counter a workgroup");
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr double kLog2e = 1.4426950408889634;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNegInf = -__builtin_inff();
+constexpr float kFltMax = 3.40282347e38f;
 
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -86,7 +89,8 @@ struct AttnParams {
   float* part;         // partial sums, see part_offset()
   int64_t ldq, ldo, table_width;
   int32_t batch, q_heads, group, row_tiles, window, part_rows, part_bytes, parts_log;
-  float scale;
+  float score_factor;  // score_factor * 2^score_exp = scale * log2 e * the keys' tensor scale
+  int score_exp;
 };
 
 // The tokens that a row attends to.
@@ -644,7 +648,7 @@ __global__ __launch_bounds__(256 * waves_per_simd(FMT, DB), (waves_per_simd(FMT,
     __builtin_amdgcn_sched_barrier(0);
     load_v<FMT, DB>(from, lane, t);
     __builtin_amdgcn_sched_barrier(0);
-    float score_scale = a.scale * kLog2e * a.cache.k_scale;
+    int score_exp = a.score_exp;
     if constexpr (FMT == kKvNvfp4) {
       // bf16 -> f16: a power of two per row puts its largest magnitude at
       // 2^14 .. 2^15; values down to 2^-28 of it stay exact.
@@ -654,16 +658,19 @@ __global__ __launch_bounds__(256 * waves_per_simd(FMT, DB), (waves_per_simd(FMT,
       uint32_t big = (uint32_t)(pair[0] > pair[1] ? pair[0] : pair[1]) << 16;
       big = max(big, (uint32_t)__shfl_xor((int)big, 16));
       big = max(big, (uint32_t)__shfl_xor((int)big, 32));
+      // (Below 2^-112 the power stays 2^126: the smallest bf16 number, 2^-133, is then 2^-7.)
       int e = (int)(big >> 23) - 127 - 14;
-      e = e < -100 ? -100 : e > 112 ? 112 : e;
-      const float down = __uint_as_float((uint32_t)(127 - e) << 23), up = __uint_as_float((uint32_t)(127 + e) << 23);
+      e = e < -126 ? -126 : e > 112 ? 112 : e;
+      const float down = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
       for (int i = 0; i < kE / 2; ++i) {
         const f16x2 p{(_Float16)(bf16_lo(qv[i]) * down), (_Float16)(bf16_hi(qv[i]) * down)};
         qv[i] = __builtin_bit_cast(uint32_t, p);
       }
-      score_scale *= up;
+      score_exp += e;
     }
+    // One product of the scales, whatever their sizes; where it passes fp32's range, zero products stay zero.
+    const float score_scale = fminf(__builtin_amdgcn_ldexpf(a.score_factor, score_exp), kFltMax);
 
 #pragma unroll
     for (int i = 0; i < kW; ++i) o[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -942,7 +949,7 @@ void attn_launch(const AttnLaunch& a, hipStream_t s) {
   p.part_rows = part_rows_of(a);
   p.part_bytes = (int32_t)part_bytes_of(a);
   p.parts_log = parts_log_of(a);
-  p.scale = a.scale;
+  p.score_factor = (float)std::frexp(a.scale * kLog2e * a.cache.k_scale, &p.score_exp);
   hipLaunchKernelGGL((attn_kernel<FMT, DB>), dim3((unsigned)workgroups_of(a)), dim3(64 * waves_of(a)), 0, s, p);
 }
 

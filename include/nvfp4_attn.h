@@ -218,7 +218,7 @@ typedef struct nvfp4_attn_args {
   const int32_t* page_table;/* [batch][table_width] */
   int64_t table_width;      /* >= 0; table_width * page_size <= 2^30 */
   const int32_t* seq_lens;  /* [batch] */
-  float scale;              /* > 0 and finite */
+  float scale;              /* > 0, at most 2^127 */
   int64_t window;           /* >= 0; 0: none */
   uint16_t* out;            /* bf16 [batch][ldo] */
   int64_t ldo;

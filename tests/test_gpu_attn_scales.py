@@ -34,3 +34,17 @@ def test_tensor_scales(k_scale, v_scale):
     x = scaled(dev, B.NVFP4_KV_NVFP4, k_scale, v_scale)
     scale = 1 / (k_scale * 11)
     x.check(*x.call(scale=scale), scale=float(np.float32(scale)))
+
+
+@pytest.mark.parametrize("fmt,size,k_scale", [
+    (0, 2.0 ** -126, 1.0), (0, 2.0 ** 120, 1.0), (1, 2.0 ** -126, 1.0), (1, 2.0 ** 120, 1.0),
+    (2, 2.0 ** -96, 1.0), (2, 2.0 ** -112, 1.0), (2, 2.0 ** -120, 1.0), (2, 2.0 ** -126, 2.0 ** 30), (2, 2.0 ** -130, 2.0 ** 64),
+    (2, 2.0 ** -64, 2.0 ** -56), (2, 2.0 ** -40, 2.0 ** 64), (2, 2.0 ** 60, 2.0 ** 60), (2, 2.0 ** 120, 1.0),
+    (2, 2.0 ** 120, 2.0 ** -64), (2, 2.0 ** -10, 2.0 ** -64)])
+def test_query_sizes(fmt, size, k_scale):
+    """Queries of any size (below 2^-126 they keep fewer bits themselves) with a softmax scale that makes scores of about one,
+    whatever intermediate products of the scales would be."""
+    dev = device()
+    x = scaled(dev, fmt, k_scale, 1.0, size, seed=3)
+    scale = float(np.float32(2.0 ** -4 / size / k_scale))
+    x.check(*x.call(scale=scale), scale=scale)
