@@ -1,0 +1,77 @@
+"""GPU: attention calls on several streams at once, queued behind one another, eager, prepared and captured."""
+import pytest
+import torch
+
+from bit_quantized_decode_amd import binding as B
+from helpers import device
+from test_gpu_attn_decode import FORMATS, Batch
+
+pytestmark = pytest.mark.gpu
+
+WAIT = 2_000_000      # clock ticks, about a millisecond: what follows on that stream is queued behind it
+
+
+def test_every_round_of_overlapping_streams():
+    """Ten rounds on three streams, nothing waited for in between; each round's outputs are checked."""
+    dev = device()
+    xs = [Batch(dev, f, [3000, 100], 10, 2, 128, 64, seed=s) for s, f in enumerate(FORMATS)]
+    qs = [x.q.to(dev) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    got = [[] for _ in xs]
+    for _ in range(10):
+        for x, q, s, g in zip(xs, qs, streams, got):
+            g.append(B.attn_decode(q, x.cache, x.table, x.seq, lse=True, stream=s))
+    torch.cuda.synchronize()
+    for x, g in zip(xs, got):
+        x.check(*g[0])
+        for out, lse in g[1:]:
+            assert torch.equal(out, g[0][0]) and torch.equal(lse, g[0][1])
+
+
+def test_a_larger_workspace_while_calls_are_queued():
+    """Calls that need more and more of their stream's workspace, all queued before the first one runs."""
+    dev = device()
+    xs = [Batch(dev, B.NVFP4_KV_NVFP4, [3000, 100], 2, 2, 64, 64, seed=1),
+          Batch(dev, B.NVFP4_KV_E4M3, [5000] * 4, 10, 2, 128, 64, seed=2),
+          Batch(dev, B.NVFP4_KV_BF16, [6000, 900], 32, 2, 256, 64, seed=3)]
+    qs = [x.q.to(dev) for x in xs]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    got, sizes = [], []
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(WAIT)
+        for x, q in zip(xs, qs):
+            got.append(B.attn_decode(q, x.cache, x.table, x.seq, lse=True))
+            sizes += [w.numel() for key, w in B._workspaces.items() if key[-1] == s.cuda_stream]
+            filler = torch.full((4 << 20,), 0xff, dtype=torch.uint8, device=dev)   # takes memory that the old one gave back
+        for x, q in zip(xs, qs):
+            got.append(B.attn_decode(q, x.cache, x.table, x.seq, lse=True))
+    torch.cuda.synchronize()
+    del filler
+    assert sizes[0] < sizes[1] < sizes[2]
+    for x, a, b in zip(xs, got[:3], got[3:]):
+        x.check(*a)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_prepared_calls_at_once():
+    """Two prepared calls over one cache on two streams, and a third that shares the second's stream."""
+    dev = device()
+    x = Batch(dev, B.NVFP4_KV_NVFP4, [4000, 0, 700], 10, 2, 128, 64, seed=4)
+    q = x.q.to(dev)
+    torch.cuda.synchronize()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    calls = [B.attn_decode_prepared(q, x.cache, x.table, x.seq, lse=True, stream=s) for s in (a, b, b)]
+    kept = []
+    for _ in range(8):
+        for s in (a, b):
+            with torch.cuda.stream(s):
+                torch.cuda._sleep(WAIT // 20)
+        outs = [call() for call in calls]
+        torch.cuda.synchronize()
+        kept.append([[t.clone() for t in out] for out in outs])
+    x.check(*kept[0][0])
+    for outs in kept:
+        for out, lse in outs:
+            assert torch.equal(out, kept[0][0][0]) and torch.equal(lse, kept[0][0][1])
