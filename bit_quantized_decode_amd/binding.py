@@ -728,10 +728,21 @@ def _caller(fn, args, device, stream, outputs, keep):
 
 
 class RopeTable:
-    """A device table of rotary frequencies (nvfp4_rope_freqs), with the layout and magnitude that go with it."""
+    """A device table of rotary frequencies (nvfp4_rope_freqs, or the caller's own: 64-bit fractions of a turn, at least
+    rot_dim / 2 of them), with the layout and magnitude that go with it."""
 
     def __init__(self, freqs, rot_dim, layout, magnitude):
         self.freqs, self.rot_dim, self.layout, self.magnitude = freqs, rot_dim, layout, magnitude
+
+    def address(self):
+        """The table's address, after a check that it holds what the kernels read."""
+        f = self.freqs
+        if f.dtype not in (torch.int64, torch.uint64):
+            raise TypeError(f"a rotary table's frequencies must be 64-bit integers, not {f.dtype}")
+        if not f.is_contiguous() or f.numel() < self.rot_dim // 2:
+            raise ValueError(f"a rotary table for rot_dim {self.rot_dim} must hold {self.rot_dim // 2} contiguous frequencies, "
+                             f"not {tuple(f.shape)} with strides {f.stride()}")
+        return f.data_ptr()
 
 
 def rope_freqs(rot_dim, base=10000.0, scaling=None):
@@ -765,13 +776,14 @@ def rope_prepared(x, positions, table, out=None, dtype=None, inverse=False, stre
     """rope() with its arguments marshalled once: returns a zero-argument callable that returns `out`."""
     ldx = _rows(x, "x", _ACTIVATIONS)
     tokens, heads, head_dim = x.shape
+    freqs = table.address()
     dev = _device_of(x=x, positions=positions, freqs=table.freqs, out=out)
     if out is None:
         out = _new(lambda: torch.empty((tokens, heads, head_dim), dtype=dtype or x.dtype, device=dev), dev, stream)
     ldy = _rows(out, "out", _ACTIVATIONS, heads, head_dim, tokens)
     a = RopeArgs(tokens=tokens, heads=heads, head_dim=head_dim, rot_dim=table.rot_dim, layout=table.layout,
                  inverse=int(inverse), magnitude=table.magnitude,
-                 positions=_vector(positions, "positions", torch.int32, (tokens,)), freqs=table.freqs.data_ptr(),
+                 positions=_vector(positions, "positions", torch.int32, (tokens,)), freqs=freqs,
                  x=x.data_ptr(), x_dtype=_dtype_code(x), ldx=ldx, y=out.data_ptr(), y_dtype=_dtype_code(out), ldy=ldy)
     return _caller(lib().nvfp4_rope, (ctypes.byref(a),), dev, stream, out, (a, x, positions, table, out))
 
@@ -806,6 +818,7 @@ def kv_append_prepared(cache, k, v, slots, positions=None, table=None, q=None, q
     tokens = k.shape[0]
     ldk = _rows(k, "k", _ACTIVATIONS, cache.kv_heads, cache.head_dim)
     ldv = _rows(v, "v", (k.dtype,), cache.kv_heads, cache.head_dim, tokens)
+    freqs = None if table is None else table.address()
     dev = _device_of(pool=cache.pool, k=k, v=v, slots=slots, positions=positions if table is not None else None,
                      freqs=None if table is None else table.freqs, q=q, q_out=q_out)
     a = KvAppendArgs(cache=ctypes.pointer(cache.desc), tokens=tokens, slots=_vector(slots, "slots", torch.int64, (tokens,)),
@@ -814,7 +827,7 @@ def kv_append_prepared(cache, k, v, slots, positions=None, table=None, q=None, q
         if positions is None:
             raise ValueError("a rotary table needs positions")
         # A table that turns nothing (rot_dim 0) has no memory of its own: any aligned address stands for it.
-        a.freqs = table.freqs.data_ptr() or cache.pool.data_ptr()
+        a.freqs = freqs or cache.pool.data_ptr()
         a.positions = _vector(positions, "positions", torch.int32, (tokens,))
         a.rot_dim, a.layout, a.magnitude = table.rot_dim, table.layout, table.magnitude
     if q is not None:

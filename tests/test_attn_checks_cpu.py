@@ -2,6 +2,7 @@
 import ctypes
 
 import pytest
+import torch
 
 from bit_quantized_decode_amd import binding as B
 from test_attn_abi_cpu import L, attn, desc  # noqa: F401
@@ -13,3 +14,20 @@ def test_softmax_scale(L, scale, status):  # noqa: F811
     """Up to 2^127, with which the product with log2 e is still a number (a call without a workspace stops there)."""
     d = desc()
     assert L.nvfp4_attn_decode(ctypes.byref(attn(d, scale=scale, workspace=None)), None) == status
+
+
+@pytest.mark.parametrize("freqs,error", [
+    (torch.zeros(31, dtype=torch.int64), ValueError), (torch.zeros(1, dtype=torch.int64).expand(32), ValueError),
+    (torch.zeros(64, dtype=torch.int64)[::2], ValueError), (torch.zeros(0, dtype=torch.int64), ValueError),
+    (torch.zeros(32, dtype=torch.float64), TypeError), (torch.zeros(64, dtype=torch.int32), TypeError),
+    (torch.zeros(32, dtype=torch.int64), None), (torch.zeros(40, dtype=torch.int64), None),
+    (torch.zeros(4, 8, dtype=torch.int64), None), (torch.zeros(32, dtype=torch.int64).view(torch.uint64), None)])
+def test_a_table_of_the_callers_own(freqs, error):
+    """A table that does not hold rot_dim / 2 frequencies is refused (a right one is refused for lying on the CPU)."""
+    table = B.RopeTable(freqs, 64, B.NVFP4_ROPE_HALF, 1.0)
+    x, pos = torch.zeros(2, 1, 64), torch.zeros(2, dtype=torch.int32)
+    cache = B.KvCache(2, 16, 1, 64, B.NVFP4_KV_BF16, device="cpu")
+    for call in (lambda: B.rope(x, pos, table),
+                 lambda: B.kv_append(cache, x, x, torch.zeros(2, dtype=torch.int64), positions=pos, table=table)):
+        with pytest.raises(error or ValueError, match="rotary table" if error else "GPU"):
+            call()
