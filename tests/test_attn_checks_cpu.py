@@ -31,3 +31,15 @@ def test_a_table_of_the_callers_own(freqs, error):
                  lambda: B.kv_append(cache, x, x, torch.zeros(2, dtype=torch.int64), positions=pos, table=table)):
         with pytest.raises(error or ValueError, match="rotary table" if error else "GPU"):
             call()
+
+
+@pytest.mark.parametrize("prepared", [False, True])
+def test_a_workspace_that_is_not_contiguous(prepared):
+    """An expanded workspace has less memory than elements: refused (a contiguous one is refused for lying on the CPU)."""
+    cache = B.KvCache(2, 16, 1, 64, B.NVFP4_KV_BF16, device="cpu")
+    q, table, lens = torch.zeros(2, 1, 64, dtype=torch.bfloat16), torch.zeros(2, 1, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    call = B.attn_decode_prepared if prepared else B.attn_decode
+    for ws, match in ((torch.zeros(1, dtype=torch.uint8).expand(1 << 24), "contiguous"),
+                      (torch.zeros(1 << 10, 4, dtype=torch.uint8)[:, :2], "contiguous"), (torch.zeros(1 << 10), "GPU")):
+        with pytest.raises(ValueError, match=match):
+            call(q, cache, table, lens, ws=ws)
