@@ -880,7 +880,7 @@ def _attn_workspace(nbytes, device, stream):
         return torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
 
     with torch.cuda.device(device):
-        if torch.cuda.is_current_stream_capturing():
+        if _new(torch.cuda.is_current_stream_capturing, device, stream):   # of the stream that the call runs on
             return _new(make, device, stream)
         s = torch.cuda.current_stream() if stream is None else stream
         key = (str(device), "attn", s.cuda_stream)

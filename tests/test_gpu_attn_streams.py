@@ -75,3 +75,37 @@ def test_prepared_calls_at_once():
     for outs in kept:
         for out, lse in outs:
             assert torch.equal(out, kept[0][0][0]) and torch.equal(lse, kept[0][0][1])
+
+
+def test_capture_by_a_call_told_its_stream():
+    """A call told the capturing stream, while another is current: its graph has a workspace of its own, whatever the stream's eager
+    one holds (here counters that no call has left so, put back afterwards)."""
+    dev = device()
+    x = Batch(dev, B.NVFP4_KV_NVFP4, [4000, 0, 700], 10, 2, 128, 64, seed=5)
+    q = x.q.to(dev)
+    s, other = torch.cuda.Stream(), torch.cuda.Stream()
+    want = B.attn_decode(q, x.cache, x.table, x.seq, lse=True)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        B.attn_decode(q, x.cache, x.table, x.seq)             # the stream has an eager workspace
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=s):
+        with torch.cuda.stream(other):
+            out, lse = B.attn_decode(q, x.cache, x.table, x.seq, lse=True, stream=s)
+    torch.cuda.synchronize()
+    eager = [w for key, w in B._workspaces.items() if key[-1] == s.cuda_stream][0]
+    for step in range(3):
+        out.fill_(7.0)
+        lse.fill_(7.0)
+        eager[:1024] = 255
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        eager[:1024] = 0
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1]), step
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            again = B.attn_decode(q, x.cache, x.table, x.seq, lse=True)
+        torch.cuda.synchronize()
+        assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
