@@ -43,6 +43,7 @@ NVFP4_ROPE_YARN = 2
 NVFP4_KV_BF16 = 0
 NVFP4_KV_E4M3 = 1
 NVFP4_KV_NVFP4 = 2
+NVFP4_ATTN_COUNTER_BYTES = 1024
 
 EXPORTED_ATTN = (
     "nvfp4_rope_freqs", "nvfp4_rope", "nvfp4_kv_cache_bytes", "nvfp4_kv_append", "nvfp4_kv_read",
@@ -912,22 +913,35 @@ def _attn(q, cache, page_table, seq_lens, scale, window, out, lse, ws, stream, p
         a.lse = _vector(lse, "lse", torch.float32, (batch, q_heads))
     need = ctypes.c_size_t()
     check(lib().nvfp4_attn_decode_workspace_bytes(ctypes.byref(a), ctypes.byref(need)))
+    captured = False
     if ws is None and need.value:
         if prepared:
             ws = _new(lambda: torch.zeros(need.value, dtype=torch.uint8, device=dev), dev, stream)
+            captured = _new(torch.cuda.is_current_stream_capturing, dev, stream)
         else:
             ws = _attn_workspace(need.value, dev, stream)
     if ws is not None:
         a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
     outputs = (out, lse) if isinstance(lse, torch.Tensor) else out
-    return _caller(lib().nvfp4_attn_decode, (ctypes.byref(a),), dev, stream, outputs,
+    call = _caller(lib().nvfp4_attn_decode, (ctypes.byref(a),), dev, stream, outputs,
                    (a, cache, q, page_table, seq_lens, out, lse, ws))
+    if not captured:
+        return call
+
+    # Prepared under capture: the zeros above are a node of that graph, so that a call outside it, or in another
+    # graph, may come before they are written.  Each call clears the counters itself.
+    def clear_and_call():
+        _new(ws[:NVFP4_ATTN_COUNTER_BYTES].zero_, dev, stream)
+        return call()
+
+    clear_and_call.keep = call.keep
+    return clear_and_call
 
 
 def attn_decode_prepared(q, cache, page_table, seq_lens, scale=None, window=0, out=None, lse=None, ws=None, stream=None):
     """attn_decode() with its arguments marshalled once and a workspace of its own: returns a zero-argument callable
     that returns what attn_decode() does.  Its calls, and replays of graphs that captured them, must not overlap.
-    The workspace is zeroed on the stream that is current here: a call on another waits for that one."""
+    The workspace is zeroed on `stream`, or the stream that is current here: a call on another waits for that one."""
     return _attn(q, cache, page_table, seq_lens, scale, window, out, lse, ws, stream, True)
 
 

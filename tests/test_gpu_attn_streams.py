@@ -109,3 +109,30 @@ def test_capture_by_a_call_told_its_stream():
             again = B.attn_decode(q, x.cache, x.table, x.seq, lse=True)
         torch.cuda.synchronize()
         assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
+
+
+def test_prepared_under_capture():
+    """A call prepared inside a capture, called there, before that graph ever ran, in a second graph, and among replays."""
+    dev = device()
+    x = Batch(dev, B.NVFP4_KV_BF16, [4000, 0, 700], 10, 2, 128, 64, seed=6)
+    q = x.q.to(dev)
+    want = B.attn_decode(q, x.cache, x.table, x.seq, lse=True)
+    torch.cuda.synchronize()
+    first, second = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(first):
+        call = B.attn_decode_prepared(q, x.cache, x.table, x.seq, lse=True)
+        call()
+    with torch.cuda.graph(second):
+        out, lse = call()
+    torch.cuda.synchronize()
+    ws = call.keep[-1]
+    for step in range(3):
+        for run in (call, second.replay, first.replay, call):
+            out.fill_(7.0)
+            lse.fill_(7.0)
+            if step == 0 and run is not first.replay:
+                ws[:1024] = 255                 # as memory may be that nothing has written yet
+            run()
+            torch.cuda.synchronize()
+            assert torch.equal(out, want[0]) and torch.equal(lse, want[1]), (step, run)
+    assert not ws[:1024].any()
