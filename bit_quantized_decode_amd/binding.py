@@ -647,7 +647,9 @@ def moe_grouped_prepared(*args, **kw):
 # ---- the attention side (include/nvfp4_attn.h) ---------------------------------
 #
 # Every call here runs on the device of its tensors, whichever is current, on
-# `stream` or that device's current stream.  Each *_prepared() checks and
+# `stream` or that device's current stream.  A call told its stream keeps the
+# memory of its tensors from reuse until it has run; what it makes belongs to that
+# stream, as if made with it current.  Each *_prepared() checks and
 # marshals its arguments once and returns a zero-argument callable that makes
 # the library call and returns the outputs, the same buffers each time.
 
@@ -712,6 +714,12 @@ _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
 def _caller(fn, args, device, stream, outputs, keep):
     """The callable of a prepared call: fn(*args, stream) on the tensors' device."""
     index, given = device.index, None if stream is None else stream.cuda_stream
+    if stream is not None:
+        # The caller may let go of its tensors while the call is still queued there: their memory waits for that stream.
+        for t in keep:
+            t = getattr(t, "pool", getattr(t, "freqs", t))      # of a cache, of a table
+            if isinstance(t, torch.Tensor):
+                t.record_stream(stream)
 
     def call():
         # The current stream is looked up per call, so that a call under graph capture lands on the capturing stream.

@@ -136,3 +136,40 @@ def test_prepared_under_capture():
             torch.cuda.synchronize()
             assert torch.equal(out, want[0]) and torch.equal(lse, want[1]), (step, run)
     assert not ws[:1024].any()
+
+
+def test_inputs_let_go_while_a_call_is_queued():
+    """Calls told another stream than the current one; every input is dropped, and its memory asked for again, before they run."""
+    dev = device()
+    x = Batch(dev, B.NVFP4_KV_E4M3, [400, 37], 4, 2, 64, 64, seed=7)
+    table = B.rope_table(64, device=dev)
+    pos = torch.tensor([399, 36], dtype=torch.int32, device=dev)
+    slots = torch.stack([x.table[i, p // 64].long() * 64 + p % 64 for i, p in enumerate((399, 36))])
+    kv = torch.randn(2, 2, 64, device=dev).to(torch.bfloat16)
+    q = x.q.to(dev)
+    k, v = (t.clone() for t in B.kv_read(x.cache, slots))
+
+    def chain(stream, *inputs):
+        pool, table_pages, seq, turns, p, at, new, query = inputs
+        cache = B.KvCache(x.cache.pages, 64, 2, 64, x.fmt, device=dev, pool=pool)
+        rope = B.RopeTable(turns, 64, table.layout, table.magnitude)
+        turned = B.kv_append(cache, new, new, at, positions=p, table=rope, q=query, stream=stream)
+        return (B.rope(new, p, rope, stream=stream), turned, *B.kv_read(cache, at, stream=stream),
+                *B.attn_decode(turned, cache, table_pages, seq, lse=True, stream=stream))
+
+    inputs = [x.cache.pool, x.table, x.seq, table.freqs, pos, slots, kv, q]
+    want = chain(None, *(t.clone() for t in inputs))
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    copies = [t.clone() for t in inputs]
+    sizes = [t.numel() * t.element_size() for t in copies]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20 * WAIT)
+    got = chain(s, *copies)
+    del copies
+    taken = [torch.full((n,), 0, dtype=torch.uint8, device=dev) for n in sizes for _ in range(2)]
+    torch.cuda.synchronize()
+    del taken
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    assert not torch.equal(want[2], k) and not torch.equal(want[3], v)
