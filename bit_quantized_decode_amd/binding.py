@@ -653,8 +653,8 @@ def moe_grouped_prepared(*args, **kw):
 # marshals its arguments once and returns a zero-argument callable that makes
 # the library call and returns the outputs, the same buffers each time.
 
-def _device_of(**tensors):
-    """The one GPU that all given tensors are on."""
+def _device_of(stream, **tensors):
+    """The one GPU that all given tensors, and `stream` if it is given, are on."""
     dev = None
     for name, t in tensors.items():
         if t is None:
@@ -664,6 +664,8 @@ def _device_of(**tensors):
         if dev is not None and t.device != dev:
             raise ValueError(f"{name} is on {t.device}, other arguments on {dev}")
         dev = t.device
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
     return dev
 
 
@@ -786,7 +788,7 @@ def rope_prepared(x, positions, table, out=None, dtype=None, inverse=False, stre
     ldx = _rows(x, "x", _ACTIVATIONS)
     tokens, heads, head_dim = x.shape
     freqs = table.address()
-    dev = _device_of(x=x, positions=positions, freqs=table.freqs, out=out)
+    dev = _device_of(stream, x=x, positions=positions, freqs=table.freqs, out=out)
     if out is None:
         out = _new(lambda: torch.empty((tokens, heads, head_dim), dtype=dtype or x.dtype, device=dev), dev, stream)
     ldy = _rows(out, "out", _ACTIVATIONS, heads, head_dim, tokens)
@@ -828,7 +830,7 @@ def kv_append_prepared(cache, k, v, slots, positions=None, table=None, q=None, q
     ldk = _rows(k, "k", _ACTIVATIONS, cache.kv_heads, cache.head_dim)
     ldv = _rows(v, "v", (k.dtype,), cache.kv_heads, cache.head_dim, tokens)
     freqs = None if table is None else table.address()
-    dev = _device_of(pool=cache.pool, k=k, v=v, slots=slots, positions=positions if table is not None else None,
+    dev = _device_of(stream, pool=cache.pool, k=k, v=v, slots=slots, positions=positions if table is not None else None,
                      freqs=None if table is None else table.freqs, q=q, q_out=q_out)
     a = KvAppendArgs(cache=ctypes.pointer(cache.desc), tokens=tokens, slots=_vector(slots, "slots", torch.int64, (tokens,)),
                      k=k.data_ptr(), v=v.data_ptr(), dtype=_dtype_code(k), ldk=ldk, ldv=ldv)
@@ -859,7 +861,7 @@ def kv_append(cache, k, v, slots, positions=None, table=None, q=None, q_out=None
 def kv_read_prepared(cache, slots, k_out=None, v_out=None, dtype=torch.bfloat16, stream=None):
     """kv_read() with its arguments marshalled once: returns a zero-argument callable that returns (k_out, v_out)."""
     tokens = slots.shape[0]
-    dev = _device_of(pool=cache.pool, slots=slots, k_out=k_out, v_out=v_out)
+    dev = _device_of(stream, pool=cache.pool, slots=slots, k_out=k_out, v_out=v_out)
     shape = (tokens, cache.kv_heads, cache.head_dim)
     if k_out is None and v_out is None:
         k_out, v_out = (_new(lambda: torch.empty(shape, dtype=dtype, device=dev), dev, stream) for _ in range(2))
@@ -904,7 +906,7 @@ def _attn(q, cache, page_table, seq_lens, scale, window, out, lse, ws, stream, p
     batch, q_heads, head_dim = q.shape
     if ws is not None and not ws.is_contiguous():
         raise ValueError(f"ws must be contiguous, not {tuple(ws.shape)} with strides {ws.stride()}")
-    dev = _device_of(pool=cache.pool, q=q, page_table=page_table, seq_lens=seq_lens, out=out, ws=ws,
+    dev = _device_of(stream, pool=cache.pool, q=q, page_table=page_table, seq_lens=seq_lens, out=out, ws=ws,
                      lse=lse if isinstance(lse, torch.Tensor) else None)
     if page_table.dim() != 2:
         raise ValueError(f"page_table must be [batch][pages], not {tuple(page_table.shape)}")

@@ -173,3 +173,22 @@ def test_inputs_let_go_while_a_call_is_queued():
     del taken
     assert all(torch.equal(a, b) for a, b in zip(want, got))
     assert not torch.equal(want[2], k) and not torch.equal(want[3], v)
+
+
+def test_a_stream_of_another_device():
+    """Refused, by every call that can be told its stream, before anything is made there or launched."""
+    dev = device()
+
+    class Elsewhere:
+        device, cuda_stream = torch.device("cuda", torch.cuda.device_count()), 0
+
+    s, table = Elsewhere(), B.rope_table(64, device=dev)
+    cache = B.KvCache(2, 16, 1, 64, B.NVFP4_KV_BF16, device=dev)
+    x = torch.zeros(2, 1, 64, dtype=torch.bfloat16, device=dev)
+    ints, slots = torch.ones(2, dtype=torch.int32, device=dev), torch.zeros(2, dtype=torch.int64, device=dev)
+    for call in (lambda: B.rope(x, ints, table, stream=s), lambda: B.kv_append(cache, x, x, slots, stream=s),
+                 lambda: B.kv_read(cache, slots, stream=s),
+                 lambda: B.attn_decode(x, cache, ints[:, None], ints, stream=s),
+                 lambda: B.attn_decode_prepared(x, cache, ints[:, None], ints, stream=s)):
+        with pytest.raises(ValueError, match="stream is on"):
+            call()
