@@ -267,7 +267,8 @@ def prepare(case, seed):
             return st
         cache = B.KvCache(st["pages"], case["page"], case["kv_heads"], d, fmt[case["fmt"]], device="cuda")
         if case["op"] == "cache":
-            st["write"] = B.kv_append_prepared(cache, st["k"], st["v"], st["slots"], positions=st["pos"], table=table)
+            st["write"] = B.kv_append_prepared(cache, st["k"], st["v"], st["slots"],
+                                               positions=None if table is None else st["pos"], table=table)
             st["read"] = B.kv_read_prepared(cache, st["slots"], dtype=torch.bfloat16)
             return st
         B.kv_append(cache, st.pop("k"), st.pop("v"), torch.arange(st["pages"] * case["page"], device="cuda"))
