@@ -7,6 +7,7 @@ the library is not built, every call raises -- there is no fallback path.
 """
 import ctypes
 import os
+import warnings
 
 import torch
 
@@ -824,8 +825,7 @@ class KvCache:
         self.pages, self.page_size, self.kv_heads, self.head_dim, self.fmt = pages, page_size, kv_heads, head_dim, fmt
 
 
-def kv_append_prepared(cache, k, v, slots, positions=None, table=None, q=None, q_out=None, stream=None):
-    """kv_append() with its arguments marshalled once: returns a zero-argument callable that returns q_out."""
+def _kv_append(cache, k, v, slots, positions, table, q, q_out, stream):
     tokens = k.shape[0]
     ldk = _rows(k, "k", _ACTIVATIONS, cache.kv_heads, cache.head_dim)
     ldv = _rows(v, "v", (k.dtype,), cache.kv_heads, cache.head_dim, tokens)
@@ -841,6 +841,8 @@ def kv_append_prepared(cache, k, v, slots, positions=None, table=None, q=None, q
         a.freqs = freqs or cache.pool.data_ptr()
         a.positions = _vector(positions, "positions", torch.int32, (tokens,))
         a.rot_dim, a.layout, a.magnitude = table.rot_dim, table.layout, table.magnitude
+    elif positions is not None:
+        warnings.warn("positions without a rotary table are not used: the keys are stored as they are", stacklevel=3)
     if q is not None:
         a.ldq = _rows(q, "q", (k.dtype,), None, cache.head_dim, tokens)
         if q_out is None:
@@ -851,11 +853,16 @@ def kv_append_prepared(cache, k, v, slots, positions=None, table=None, q=None, q
                    (a, cache, k, v, slots, positions, table, q, q_out))
 
 
+def kv_append_prepared(cache, k, v, slots, positions=None, table=None, q=None, q_out=None, stream=None):
+    """kv_append() with its arguments marshalled once: returns a zero-argument callable that returns q_out."""
+    return _kv_append(cache, k, v, slots, positions, table, q, q_out, stream)
+
+
 def kv_append(cache, k, v, slots, positions=None, table=None, q=None, q_out=None, stream=None):
     """Write k, v [tokens][kv_heads][head_dim] (fp32 or bf16) into the cache at slots (int64; outside the pool:
     skipped).  With table (and positions, int32) k is turned first, and q [tokens][q_heads][head_dim] into q_out
-    (bf16), which is returned."""
-    return kv_append_prepared(cache, k, v, slots, positions, table, q, q_out, stream)()
+    (bf16), which is returned.  Without a table k is stored as it is, and positions only raise a warning."""
+    return _kv_append(cache, k, v, slots, positions, table, q, q_out, stream)()
 
 
 def kv_read_prepared(cache, slots, k_out=None, v_out=None, dtype=torch.bfloat16, stream=None):
