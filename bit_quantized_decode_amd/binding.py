@@ -788,6 +788,8 @@ def rope_prepared(x, positions, table, out=None, dtype=None, inverse=False, stre
     """rope() with its arguments marshalled once: returns a zero-argument callable that returns `out`."""
     ldx = _rows(x, "x", _ACTIVATIONS)
     tokens, heads, head_dim = x.shape
+    if out is not None and dtype is not None and out.dtype != dtype:
+        raise TypeError(f"out is {out.dtype}, dtype {dtype}")
     freqs = table.address()
     dev = _device_of(stream, x=x, positions=positions, freqs=table.freqs, out=out)
     if out is None:

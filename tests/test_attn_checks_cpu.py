@@ -43,3 +43,15 @@ def test_a_workspace_that_is_not_contiguous(prepared):
                       (torch.zeros(1 << 10, 4, dtype=torch.uint8)[:, :2], "contiguous"), (torch.zeros(1 << 10), "GPU")):
         with pytest.raises(ValueError, match=match):
             call(q, cache, table, lens, ws=ws)
+
+
+def test_rope_out_of_another_dtype():
+    """Given both, out and dtype have to agree (and if they do, the call is refused for lying on the CPU)."""
+    table = B.RopeTable(torch.zeros(32, dtype=torch.int64), 64, B.NVFP4_ROPE_HALF, 1.0)
+    x, pos, out = torch.zeros(2, 1, 64), torch.zeros(2, dtype=torch.int32), torch.zeros(2, 1, 64, dtype=torch.bfloat16)
+    for call in (B.rope, B.rope_prepared):
+        with pytest.raises(TypeError, match="dtype"):
+            call(x, pos, table, out=out, dtype=torch.float32)
+        for dtype in (None, torch.bfloat16):
+            with pytest.raises(ValueError, match="GPU"):
+                call(x, pos, table, out=out, dtype=dtype)
