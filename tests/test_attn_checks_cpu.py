@@ -55,3 +55,12 @@ def test_rope_out_of_another_dtype():
         for dtype in (None, torch.bfloat16):
             with pytest.raises(ValueError, match="GPU"):
                 call(x, pos, table, out=out, dtype=dtype)
+
+
+@pytest.mark.parametrize("lse", [1, "yes", [True]])
+def test_lse_of_another_kind(lse):
+    cache = B.KvCache(2, 16, 1, 64, B.NVFP4_KV_BF16, device="cpu")
+    q, table, lens = torch.zeros(2, 1, 64, dtype=torch.bfloat16), torch.zeros(2, 1, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    for call in (B.attn_decode, B.attn_decode_prepared):
+        with pytest.raises(TypeError, match="lse"):
+            call(q, cache, table, lens, lse=lse)
