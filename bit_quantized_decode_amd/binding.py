@@ -913,7 +913,7 @@ def _attn_workspace(nbytes, device, stream):
 def _attn(q, cache, page_table, seq_lens, scale, window, out, lse, ws, stream, prepared):
     ldq = _rows(q, "q", (torch.bfloat16,), None, cache.head_dim)
     batch, q_heads, head_dim = q.shape
-    if not (lse is None or isinstance(lse, (bool, torch.Tensor))):
+    if not isinstance(lse, torch.Tensor) and lse is not True and lse:
         raise TypeError(f"lse must be True, False or a tensor, not {lse!r}")
     if ws is not None and not ws.is_contiguous():
         raise ValueError(f"ws must be contiguous, not {tuple(ws.shape)} with strides {ws.stride()}")
