@@ -171,11 +171,13 @@ int nvfp4_rope_freqs(const nvfp4_rope_config* c, uint64_t* freqs, float* magnitu
   const long double two_pi = 6.283185307179586476925286766559L;
   const long double rot = (long double)c->rot_dim, log_base = logl((long double)c->base);
   long double low = 0.0L, high = 0.0L;
+  bool slow = false;  // every pair turns less than beta_slow times
   if (yarn && c->rot_dim > 0) {
     // The (fractional) pair that makes `turns` turns over the original positions.
     const auto pair = [&](double turns) { return rot * logl((long double)c->original_max / (turns * two_pi)) / (2.0L * log_base); };
     low = floorl(pair(c->beta_fast));
     high = ceill(pair(c->beta_slow));
+    slow = pair(c->beta_slow) < 0.0L;
     low = low < 0.0L ? 0.0L : low;
     high = high > rot - 1.0L ? rot - 1.0L : high;
   }
@@ -186,7 +188,7 @@ int nvfp4_rope_freqs(const nvfp4_rope_config* c, uint64_t* freqs, float* magnitu
       long double width = high - low, ramp;
       width = width < 0.001L ? 0.001L : width;
       ramp = ((long double)i - low) / width;
-      ramp = ramp < 0.0L ? 0.0L : ramp > 1.0L ? 1.0L : ramp;
+      ramp = slow ? 1.0L : ramp < 0.0L ? 0.0L : ramp > 1.0L ? 1.0L : ramp;
       f = f * (1.0L - ramp) + f / (long double)c->factor * ramp;
     }
     freqs[i] = (uint64_t)roundl(f * 18446744073709551616.0L);  // f < 0.16

@@ -50,7 +50,8 @@ typedef enum nvfp4_rope_scaling {
   NVFP4_ROPE_YARN = 2       /* the Ignis README's long contexts: f_i kept for pairs that turn more than
                                beta_fast times over original_max positions, f_i / factor for those under
                                beta_slow turns, a linear ramp over the pair index between (its ends
-                               rounded outwards to whole pairs); magnitude = 0.1 ln(factor) + 1 */
+                               rounded outwards to whole pairs, within [0, rot_dim - 1]);
+                               magnitude = 0.1 ln(factor) + 1 */
 } nvfp4_rope_scaling;
 
 typedef struct nvfp4_rope_config {

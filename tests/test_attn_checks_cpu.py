@@ -64,3 +64,15 @@ def test_lse_of_another_kind(lse):
     for call in (B.attn_decode, B.attn_decode_prepared):
         with pytest.raises(TypeError, match="lse"):
             call(q, cache, table, lens, lse=lse)
+
+
+@pytest.mark.parametrize("rot,base,trained,fast,slow", [(64, 1e4, 4, 32.0, 1.0), (16, 1e6, 6.28, 2.0, 1.0), (128, 1e4, 100, 1e3, 40.0),
+                                                        (32, 1e4, 1e-3, 32.0, 1.0)])
+def test_yarn_with_every_pair_slow(L, rot, base, trained, fast, slow):  # noqa: F811
+    """Trained over so few positions that even the first pair turns less than beta_slow times: all pairs are f / factor."""
+    assert trained / (2 * 3.141592653589793) < slow
+    got, magnitude = B.rope_freqs(rot, base, ("yarn", 8.0, trained, fast, slow))
+    want, _ = B.rope_freqs(rot, base, ("linear", 8.0))
+    # Two roundings of the table's last bit, and of its extended-precision operations.
+    assert ((got - want).abs().double() <= 1 + want.double() * 2.0 ** -58).all()
+    assert magnitude == pytest.approx(0.1 * 2.0794415416798357 + 1.0, rel=2.0 ** -24)
