@@ -887,8 +887,8 @@ def kv_read_prepared(cache, slots, k_out=None, v_out=None, dtype=torch.bfloat16,
 
 
 def kv_read(cache, slots, k_out=None, v_out=None, dtype=torch.bfloat16, stream=None):
-    """The values the cache holds at slots (int64): (k, v), each [tokens][kv_heads][head_dim].  Given one of
-    k_out and v_out, only that one is read.  Rows of slots outside the pool are left as they were."""
+    """The values the cache holds at slots (int64): (k, v), each [tokens][kv_heads][head_dim], new tensors of `dtype`.
+    Given one of k_out and v_out, only that one is read, in its own dtype.  Rows of slots outside the pool are left as they were."""
     return kv_read_prepared(cache, slots, k_out, v_out, dtype, stream)()
 
 

@@ -37,10 +37,12 @@
 //
 // Bound by the cache's bytes where they are many, by a fixed 8 us where they are few: the
 // launch (3 us), lengths, page table and first tile, each waiting for the one before (3 us), and
-// the way of partial sums through memory (2 to 4 us).  8 kv heads of 128 for 40 query heads:
-// one user over 131,072 tokens bf16 85.3 us (537 MB, 6.3 TB/s); 32 users over up to 16,384
-// tokens NVFP4 50-55 us (274-308 MB, 5.5 TB/s); over 8192 each 51 us (302 MB, 5.9 TB/s);
-// one user over 100 / 1000 / 8000 tokens 7.0 / 9.3 / 12.1 us.  A streaming read runs at 6.65.
+// the way of partial sums through memory (2 to 4 us).  8 kv heads of 128 for 40 query heads,
+// inputs cold (warm in brackets): one user over 131,072 tokens bf16 87-91 us (85-89; 537 MB, 5.9 to
+// 6.3 TB/s); 32 users over up to 16,384 tokens NVFP4 51-59 us (50-57; 274-308 MB, 5.2 to 5.4 TB/s, by
+// the lengths); over 8192 each 52 us (302 MB, 5.8 TB/s); one user over 100 / 1000 / 8000 tokens 7.2 /
+// 9.4 / 12.9 us (7.0 / 9.2 / 12.3).  A streaming read runs at 6.65.  Dequantising NVFP4 takes 2.5 % of
+// the long batches, an eighth of short users' (against a copy with a trivial conversion).
 // Non-temporal loads: 32 users of 16,384 NVFP4 tokens 96 us against 112, one of 131,072 bf16
 // tokens 90 against 100 (a cache that still lies in the MALL reads up to 5 % slower).  Page
 // sizes of 16 to 2048 tokens, in order or not, read alike.

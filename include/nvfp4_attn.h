@@ -188,7 +188,8 @@ int nvfp4_kv_read(const nvfp4_kv_cache* cache /* host */, const int64_t* slots, 
  * score +inf or NaN makes its query head's row and lse NaN.  A value's make the
  * outputs that they enter infinite or NaN, even where the token weighs nothing.
  * Several rows may share pages: a few new tokens of one sequence are rows with
- * the same table and lengths n, n + 1, ...
+ * the same table and lengths n, n + 1, ...  Each row, and each sixteen query heads
+ * of one kv head, reads its cache by itself.
  *
  * Scores, maxima, sums and outputs are held in fp32.  The exp() terms enter the
  * matrix cores rounded to within 2^-17 of each (bf16 and E4M3 caches: the sum of
