@@ -951,8 +951,12 @@ def _attn(q, cache, page_table, seq_lens, scale, window, out, lse, ws, stream, p
 
     # Prepared under capture: the zeros above are a node of that graph, so that a call outside it, or in another
     # graph, may come before they are written.  Each call clears the counters itself.
+    @torch.inference_mode()     # where the workspace may have been made, and may be written
+    def clear():
+        ws[:NVFP4_ATTN_COUNTER_BYTES].zero_()
+
     def clear_and_call():
-        _new(ws[:NVFP4_ATTN_COUNTER_BYTES].zero_, dev, stream)
+        _new(clear, dev, stream)
         return call()
 
     clear_and_call.keep = call.keep

@@ -192,3 +192,29 @@ def test_a_stream_of_another_device():
                  lambda: B.attn_decode_prepared(x, cache, ints[:, None], ints, stream=s)):
         with pytest.raises(ValueError, match="stream is on"):
             call()
+
+
+def test_prepared_under_capture_in_inference_mode():
+    """As a serving program does (torch wants graphs of that mode captured and replayed there); called outside it too."""
+    dev = device()
+    x = Batch(dev, B.NVFP4_KV_NVFP4, [4000, 0, 700], 10, 2, 128, 64, seed=8)
+    q = x.q.to(dev)
+    graph = torch.cuda.CUDAGraph()
+    with torch.inference_mode():
+        want = B.attn_decode(q, x.cache, x.table, x.seq, lse=True)
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            call = B.attn_decode_prepared(q, x.cache, x.table, x.seq, lse=True)
+            out, lse = call()
+
+    def replay():
+        with torch.inference_mode():
+            graph.replay()
+
+    for run in (call, replay, replay, call, replay):
+        with torch.inference_mode():
+            out.fill_(7.0)
+            lse.fill_(7.0)
+        run()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1]), run
