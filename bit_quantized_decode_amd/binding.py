@@ -652,7 +652,8 @@ def moe_grouped_prepared(*args, **kw):
 # memory of its tensors from reuse until it has run; what it makes belongs to that
 # stream, as if made with it current.  Each *_prepared() checks and
 # marshals its arguments once and returns a zero-argument callable that makes
-# the library call and returns the outputs, the same buffers each time.
+# the library call and returns the outputs, the same buffers each time; called with
+# another stream current than when it was made, it keeps their memory likewise.
 
 def _device_of(stream, **tensors):
     """The one GPU that all given tensors, and `stream` if it is given, are on."""
@@ -717,20 +718,30 @@ _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
 def _caller(fn, args, device, stream, outputs, keep):
     """The callable of a prepared call: fn(*args, stream) on the tensors' device."""
     index, given = device.index, None if stream is None else stream.cuda_stream
-    if stream is not None:
-        # The caller may let go of its tensors while the call is still queued there: their memory waits for that stream.
+    known = {_current_raw_stream(index)}
+
+    def claim(s):
+        # The caller may let go of the callable, or of its tensors, while a call is still queued on a stream that is not theirs:
+        # their memory waits for that stream.
         for t in keep:
             t = getattr(t, "pool", getattr(t, "freqs", t))      # of a cache, of a table
             if isinstance(t, torch.Tensor):
-                t.record_stream(stream)
+                t.record_stream(s)
+
+    if stream is not None:
+        claim(stream)
 
     def call():
         # The current stream is looked up per call, so that a call under graph capture lands on the capturing stream.
+        handle = _current_raw_stream(index) if given is None else given
+        if given is None and handle not in known:
+            claim(torch.cuda.current_stream(index))
+            known.add(handle)
         if torch.cuda.current_device() == index:
-            status = fn(*args, _current_raw_stream(index) if given is None else given)
+            status = fn(*args, handle)
         else:
             with torch.cuda.device(index):
-                status = fn(*args, _current_raw_stream(index) if given is None else given)
+                status = fn(*args, handle)
         if status != NVFP4_OK:
             check(status)
         return outputs

@@ -218,3 +218,25 @@ def test_prepared_under_capture_in_inference_mode():
         run()
         torch.cuda.synchronize()
         assert torch.equal(out, want[0]) and torch.equal(lse, want[1]), run
+
+
+def test_a_prepared_call_let_go_while_it_is_queued():
+    """Prepared on one stream and called on another; the callable, and with it its workspace, is dropped before the call has
+    run, and its memory asked for again: neither the outputs nor what is made there meanwhile is touched."""
+    dev = device()
+    x = Batch(dev, B.NVFP4_KV_NVFP4, [9000, 0, 700], 10, 2, 128, 64, seed=9)
+    q = x.q.to(dev)
+    want = B.attn_decode(q, x.cache, x.table, x.seq, lse=True)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    call = B.attn_decode_prepared(q, x.cache, x.table, x.seq, lse=True)
+    need = call.keep[-1].numel()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20 * WAIT)
+        out, lse = call()
+    del call
+    taken = [torch.full((need,), 3, dtype=torch.uint8, device=dev) for _ in range(4)]
+    torch.cuda.synchronize()
+    assert all((t == 3).all() for t in taken)
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
