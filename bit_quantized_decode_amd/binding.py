@@ -1,5 +1,5 @@
-"""Python binding of libnvfp4.so: the functions of include/nvfp4.h and
-include/nvfp4_attn.h, same names.
+"""Python binding of libnvfp4.so: the functions of include/nvfp4.h,
+include/nvfp4_attn.h and include/nvfp4_attn_long.h, same names.
 
 Argument marshalling only: torch tensors supply device memory and the current
 stream; every step of the computation runs in the library's HIP kernels.  If
@@ -49,6 +49,15 @@ NVFP4_ATTN_COUNTER_BYTES = 1024
 EXPORTED_ATTN = (
     "nvfp4_rope_freqs", "nvfp4_rope", "nvfp4_kv_cache_bytes", "nvfp4_kv_append", "nvfp4_kv_read",
     "nvfp4_attn_decode_workspace_bytes", "nvfp4_attn_decode",
+)
+
+# include/nvfp4_attn_long.h
+NVFP4_SELECT_COUNTER_BYTES = 4096
+
+EXPORTED_ATTN_LONG = (
+    "nvfp4_attn_shared_workspace_bytes", "nvfp4_attn_shared", "nvfp4_kv_bounds", "nvfp4_kv_select_workspace_bytes",
+    "nvfp4_kv_select", "nvfp4_attn_decode_heads", "nvfp4_attn_weigh_workspace_bytes", "nvfp4_attn_weigh",
+    "nvfp4_kv_evict_workspace_bytes", "nvfp4_kv_evict",
 )
 
 
@@ -151,6 +160,39 @@ class AttnArgs(ctypes.Structure):
     ]
 
 
+class AttnSharedArgs(ctypes.Structure):
+    """Mirror of struct nvfp4_attn_shared_args."""
+    _fields_ = [("attn", AttnArgs), ("prefix_table", ctypes.c_void_p), ("prefix_width", ctypes.c_int64),
+                ("prefix_len", ctypes.c_void_p)]
+
+
+class AttnWeighArgs(ctypes.Structure):
+    """Mirror of struct nvfp4_attn_weigh_args."""
+    _fields_ = [("attn", AttnArgs), ("weights", ctypes.c_void_p), ("decay", ctypes.c_float), ("weights_out", ctypes.c_void_p)]
+
+
+class KvSelectArgs(ctypes.Structure):
+    """Mirror of struct nvfp4_kv_select_args."""
+    _fields_ = [
+        ("cache", ctypes.POINTER(KvCacheDesc)), ("batch", ctypes.c_int64), ("q_heads", ctypes.c_int64),
+        ("q", ctypes.c_void_p), ("ldq", ctypes.c_int64), ("bounds", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+        ("table_width", ctypes.c_int64), ("seq_lens", ctypes.c_void_p), ("budget", ctypes.c_int64),
+        ("pages_out", ctypes.c_void_p), ("lens_out", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class KvEvictArgs(ctypes.Structure):
+    """Mirror of struct nvfp4_kv_evict_args."""
+    _fields_ = [
+        ("batch", ctypes.c_int64), ("kv_heads", ctypes.c_int64), ("page_size", ctypes.c_int64), ("weights", ctypes.c_void_p),
+        ("page_table", ctypes.c_void_p), ("table_width", ctypes.c_int64), ("seq_lens", ctypes.c_void_p),
+        ("budget", ctypes.c_int64), ("sink", ctypes.c_int64), ("recent", ctypes.c_int64), ("table_out", ctypes.c_void_p),
+        ("lens_out", ctypes.c_void_p), ("weights_out", ctypes.c_void_p), ("freed", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
 _lib = None
 
 
@@ -199,6 +241,16 @@ def lib():
         "nvfp4_kv_read": (I, [ctypes.POINTER(KvCacheDesc), P, i64, P, i64, P, i64, I, P]),
         "nvfp4_attn_decode_workspace_bytes": (I, [ctypes.POINTER(AttnArgs), ctypes.POINTER(sz)]),
         "nvfp4_attn_decode": (I, [ctypes.POINTER(AttnArgs), P]),
+        "nvfp4_attn_shared_workspace_bytes": (I, [ctypes.POINTER(AttnSharedArgs), ctypes.POINTER(sz)]),
+        "nvfp4_attn_shared": (I, [ctypes.POINTER(AttnSharedArgs), P]),
+        "nvfp4_kv_bounds": (I, [ctypes.POINTER(KvCacheDesc), P, i64, P, P]),
+        "nvfp4_kv_select_workspace_bytes": (I, [ctypes.POINTER(KvSelectArgs), ctypes.POINTER(sz)]),
+        "nvfp4_kv_select": (I, [ctypes.POINTER(KvSelectArgs), P]),
+        "nvfp4_attn_decode_heads": (I, [ctypes.POINTER(AttnArgs), P]),
+        "nvfp4_attn_weigh_workspace_bytes": (I, [ctypes.POINTER(AttnWeighArgs), ctypes.POINTER(sz)]),
+        "nvfp4_attn_weigh": (I, [ctypes.POINTER(AttnWeighArgs), P]),
+        "nvfp4_kv_evict_workspace_bytes": (I, [ctypes.POINTER(KvEvictArgs), ctypes.POINTER(sz)]),
+        "nvfp4_kv_evict": (I, [ctypes.POINTER(KvEvictArgs), P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -747,7 +799,23 @@ def _caller(fn, args, device, stream, outputs, keep):
         return outputs
 
     call.keep = keep   # the tensors and structures must outlive the callable
+    call.outputs = outputs
     return call
+
+
+def _clearing(call, ws, counter_bytes, device, stream):
+    """The callable of a call prepared under capture.  Its workspace was zeroed by a node of that graph, so that a call
+    outside it, or in another graph, may come before that is written: each call clears the counters itself."""
+    @torch.inference_mode()     # where the workspace may have been made, and may be written
+    def clear():
+        ws[:counter_bytes].zero_()
+
+    def clear_and_call():
+        _new(clear, device, stream)
+        return call()
+
+    clear_and_call.keep, clear_and_call.outputs = call.keep, call.outputs
+    return clear_and_call
 
 
 class RopeTable:
@@ -903,10 +971,10 @@ def kv_read(cache, slots, k_out=None, v_out=None, dtype=torch.bfloat16, stream=N
     return kv_read_prepared(cache, slots, k_out, v_out, dtype, stream)()
 
 
-def _attn_workspace(nbytes, device, stream):
-    """The workspace of attention calls without one of their own.  Calls on one stream run one after the other and
-    share; calls on others have another.  Under capture the graph gets one of its own, zeroed by a
-    node of the graph: replays may overlap with anything."""
+def _attn_workspace(nbytes, device, stream, kind="attn"):
+    """The workspace of attention calls without one of their own (kind "select": of page selections).  Calls on one
+    stream run one after the other and share; calls on others have another.  Under capture the graph gets one of its
+    own, zeroed by a node of the graph: replays may overlap with anything."""
     def make():
         return torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
 
@@ -914,64 +982,67 @@ def _attn_workspace(nbytes, device, stream):
         if _new(torch.cuda.is_current_stream_capturing, device, stream):   # of the stream that the call runs on
             return _new(make, device, stream)
         s = torch.cuda.current_stream() if stream is None else stream
-        key = (str(device), "attn", s.cuda_stream)
+        key = (str(device), kind, s.cuda_stream)
         ws = _workspaces.get(key)
         if ws is None or ws.numel() < nbytes:
             ws = _workspaces[key] = _new(make, device, stream)
         return ws
 
 
-def _attn(q, cache, page_table, seq_lens, scale, window, out, lse, ws, stream, prepared):
+def _workspace_of(need, ws, device, stream, prepared, kind):
+    """(the workspace of a call that needs `need` bytes, whether it was made for a call prepared under capture)."""
+    if ws is not None or not need:
+        return ws, False
+    if not prepared:
+        return _attn_workspace(need, device, stream, kind), False
+    ws = _new(lambda: torch.zeros(need, dtype=torch.uint8, device=device), device, stream)
+    return ws, _new(torch.cuda.is_current_stream_capturing, device, stream)
+
+
+def _check_ws(ws):
+    if ws is not None and not ws.is_contiguous():
+        raise ValueError(f"ws must be contiguous, not {tuple(ws.shape)} with strides {ws.stride()}")
+
+
+def _attn(q, cache, page_table, seq_lens, scale, window, out, lse, ws, stream, prepared, fn="nvfp4_attn_decode", wrap=None,
+          result=None, **tensors):
+    """The callable of an attention: `fn` with AttnArgs, or with wrap(AttnArgs), a structure that has them as `attn`; tensors:
+    those that wrap() uses, and result: one more that the call returns."""
     ldq = _rows(q, "q", (torch.bfloat16,), None, cache.head_dim)
     batch, q_heads, head_dim = q.shape
     if not isinstance(lse, torch.Tensor) and lse is not True and lse:
         raise TypeError(f"lse must be True, False or a tensor, not {lse!r}")
-    if ws is not None and not ws.is_contiguous():
-        raise ValueError(f"ws must be contiguous, not {tuple(ws.shape)} with strides {ws.stride()}")
+    _check_ws(ws)
     dev = _device_of(stream, pool=cache.pool, q=q, page_table=page_table, seq_lens=seq_lens, out=out, ws=ws,
-                     lse=lse if isinstance(lse, torch.Tensor) else None)
-    if page_table.dim() != 2:
+                     lse=lse if isinstance(lse, torch.Tensor) else None, **tensors)
+    heads = page_table.dim() == 3 and fn == "nvfp4_attn_decode"
+    if page_table.dim() != 2 and not heads:
         raise ValueError(f"page_table must be [batch][pages], not {tuple(page_table.shape)}")
     if out is None:
         out = _new(lambda: torch.empty((batch, q_heads, head_dim), dtype=torch.bfloat16, device=dev), dev, stream)
     if lse is True:
         lse = _new(lambda: torch.empty((batch, q_heads), dtype=torch.float32, device=dev), dev, stream)
+    width = page_table.shape[-1]
     a = AttnArgs(cache=ctypes.pointer(cache.desc), batch=batch, q_heads=q_heads, q=q.data_ptr(), ldq=ldq,
-                 page_table=_vector(page_table, "page_table", torch.int32, (batch, page_table.shape[1])),
-                 table_width=page_table.shape[1], seq_lens=_vector(seq_lens, "seq_lens", torch.int32, (batch,)),
+                 page_table=_vector(page_table, "page_table", torch.int32,
+                                    (batch, cache.kv_heads, width) if heads else (batch, width)),
+                 table_width=width, seq_lens=_vector(seq_lens, "seq_lens", torch.int32, (batch,)),
                  scale=head_dim ** -0.5 if scale is None else scale, window=window, out=out.data_ptr(),
                  ldo=_rows(out, "out", (torch.bfloat16,), q_heads, head_dim, batch))
     if isinstance(lse, torch.Tensor):
         a.lse = _vector(lse, "lse", torch.float32, (batch, q_heads))
+    args = a if wrap is None else wrap(a)
     need = ctypes.c_size_t()
-    check(lib().nvfp4_attn_decode_workspace_bytes(ctypes.byref(a), ctypes.byref(need)))
-    captured = False
-    if ws is None and need.value:
-        if prepared:
-            ws = _new(lambda: torch.zeros(need.value, dtype=torch.uint8, device=dev), dev, stream)
-            captured = _new(torch.cuda.is_current_stream_capturing, dev, stream)
-        else:
-            ws = _attn_workspace(need.value, dev, stream)
+    check(getattr(lib(), f"{fn}_workspace_bytes")(ctypes.byref(args), ctypes.byref(need)))
+    ws, captured = _workspace_of(need.value, ws, dev, stream, prepared, "attn")
     if ws is not None:
-        a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
-    outputs = (out, lse) if isinstance(lse, torch.Tensor) else out
-    call = _caller(lib().nvfp4_attn_decode, (ctypes.byref(a),), dev, stream, outputs,
-                   (a, cache, q, page_table, seq_lens, out, lse, ws))
-    if not captured:
-        return call
-
-    # Prepared under capture: the zeros above are a node of that graph, so that a call outside it, or in another
-    # graph, may come before they are written.  Each call clears the counters itself.
-    @torch.inference_mode()     # where the workspace may have been made, and may be written
-    def clear():
-        ws[:NVFP4_ATTN_COUNTER_BYTES].zero_()
-
-    def clear_and_call():
-        _new(clear, dev, stream)
-        return call()
-
-    clear_and_call.keep = call.keep
-    return clear_and_call
+        attn = a if wrap is None else args.attn
+        attn.workspace, attn.workspace_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
+    outputs = (out,) + ((lse,) if isinstance(lse, torch.Tensor) else ()) + (() if result is None else (result,))
+    call = _caller(getattr(lib(), "nvfp4_attn_decode_heads" if heads else fn), (ctypes.byref(args),), dev, stream,
+                   outputs if len(outputs) > 1 else out,
+                   (a, args, cache, q, page_table, seq_lens, out, lse, ws, *tensors.values()))
+    return _clearing(call, ws, NVFP4_ATTN_COUNTER_BYTES, dev, stream) if captured else call
 
 
 def attn_decode_prepared(q, cache, page_table, seq_lens, scale=None, window=0, out=None, lse=None, ws=None, stream=None):
@@ -983,7 +1054,167 @@ def attn_decode_prepared(q, cache, page_table, seq_lens, scale=None, window=0, o
 
 def attn_decode(q, cache, page_table, seq_lens, scale=None, window=0, out=None, lse=None, ws=None, stream=None):
     """Attention of one new token per sequence over the cache: q bf16 [batch][q_heads][head_dim], page_table int32
-    [batch][pages], seq_lens int32 [batch] (with the new token), scale 1 / sqrt(head_dim) by default.  Returns out
-    (bf16 like q), or (out, lse) if lse is True or a float32 [batch][q_heads] tensor.  ws: a workspace, zeroed
-    before its first use, that no other running call has."""
+    [batch][pages], or [batch][kv_heads][pages] for pages of each kv head's own (as kv_select() gives them), seq_lens int32
+    [batch] (with the new token), scale 1 / sqrt(head_dim) by default.  Returns out (bf16 like q), or (out, lse) if lse is
+    True or a float32 [batch][q_heads] tensor.  ws: a workspace, zeroed before its first use, that no other running call has."""
     return _attn(q, cache, page_table, seq_lens, scale, window, out, lse, ws, stream, False)()
+
+
+# ---- reading less of a long cache (include/nvfp4_attn_long.h) --------------------
+#
+# As the calls above; *_prepared() as there, a workspace of its own for each.
+
+def _attn_shared(q, cache, prefix_pages, prefix_len, page_table, seq_lens, scale, out, lse, ws, stream, prepared):
+    if prefix_pages.dim() != 1:
+        raise ValueError(f"prefix_pages must be [pages], not {tuple(prefix_pages.shape)}")
+    width = prefix_pages.shape[0]
+
+    def wrap(a):
+        return AttnSharedArgs(attn=a, prefix_table=_vector(prefix_pages, "prefix_pages", torch.int32, (width,)),
+                              prefix_width=width, prefix_len=_vector(prefix_len, "prefix_len", torch.int32, (1,)))
+    return _attn(q, cache, page_table, seq_lens, scale, 0, out, lse, ws, stream, prepared, "nvfp4_attn_shared", wrap,
+                 prefix_pages=prefix_pages, prefix_len=prefix_len)
+
+
+def attn_shared_prepared(q, cache, prefix_pages, prefix_len, page_table, seq_lens, scale=None, out=None, lse=None, ws=None,
+                         stream=None):
+    """attn_shared() prepared, as attn_decode_prepared() is."""
+    return _attn_shared(q, cache, prefix_pages, prefix_len, page_table, seq_lens, scale, out, lse, ws, stream, True)
+
+
+def attn_shared(q, cache, prefix_pages, prefix_len, page_table, seq_lens, scale=None, out=None, lse=None, ws=None, stream=None):
+    """attn_decode() where every sequence's tokens follow a prefix that all share, which is read once: prefix_pages int32
+    [pages], prefix_len int32 [1] (its tokens); page_table and seq_lens are of the sequences' own tokens after it, the
+    new one among them.  A length below 0: a free place of the batch (zeros, lse -inf)."""
+    return _attn_shared(q, cache, prefix_pages, prefix_len, page_table, seq_lens, scale, out, lse, ws, stream, False)()
+
+
+def kv_bounds_prepared(cache, pages, bounds=None, stream=None):
+    """kv_bounds() with its arguments marshalled once: returns a zero-argument callable that returns bounds."""
+    if pages.dim() != 1:
+        raise ValueError(f"pages must be [n], not {tuple(pages.shape)}")
+    dev = _device_of(stream, pool=cache.pool, pages=pages, bounds=bounds)
+    shape = (cache.pages, cache.kv_heads, 2, cache.head_dim)
+    if bounds is None:
+        bounds = _new(lambda: torch.zeros(shape, dtype=torch.bfloat16, device=dev), dev, stream)
+    n = pages.shape[0]
+    args = (ctypes.byref(cache.desc), _vector(pages, "pages", torch.int32, (n,)), n,
+            _vector(bounds, "bounds", torch.bfloat16, shape))
+    return _caller(lib().nvfp4_kv_bounds, args, dev, stream, bounds, (cache, pages, bounds))
+
+
+def kv_bounds(cache, pages, bounds=None, stream=None):
+    """The smallest and largest key of each channel in the pages (int32 ids; outside the pool: skipped), which must be
+    full: written to bounds bf16 [cache.pages][kv_heads][2][head_dim], by default a new tensor of zeros.  Returns bounds."""
+    return kv_bounds_prepared(cache, pages, bounds, stream)()
+
+
+def _kv_select(q, cache, bounds, page_table, seq_lens, budget, pages_out, lens_out, ws, stream, prepared):
+    ldq = _rows(q, "q", (torch.bfloat16,), None, cache.head_dim)
+    batch, q_heads, head_dim = q.shape
+    if page_table.dim() != 2:
+        raise ValueError(f"page_table must be [batch][pages], not {tuple(page_table.shape)}")
+    _check_ws(ws)
+    dev = _device_of(stream, pool=cache.pool, q=q, bounds=bounds, page_table=page_table, seq_lens=seq_lens,
+                     pages_out=pages_out, lens_out=lens_out, ws=ws)
+    shape = (batch, cache.kv_heads, budget)
+    a = KvSelectArgs(cache=ctypes.pointer(cache.desc), batch=batch, q_heads=q_heads, q=q.data_ptr(), ldq=ldq,
+                     bounds=_vector(bounds, "bounds", torch.bfloat16, (cache.pages, cache.kv_heads, 2, head_dim)),
+                     page_table=_vector(page_table, "page_table", torch.int32, (batch, page_table.shape[1])),
+                     table_width=page_table.shape[1], seq_lens=_vector(seq_lens, "seq_lens", torch.int32, (batch,)),
+                     budget=budget)
+    need = ctypes.c_size_t()
+    check(lib().nvfp4_kv_select_workspace_bytes(ctypes.byref(a), ctypes.byref(need)))
+    if pages_out is None:
+        pages_out = _new(lambda: torch.empty(shape, dtype=torch.int32, device=dev), dev, stream)
+    if lens_out is None:
+        lens_out = _new(lambda: torch.empty((batch,), dtype=torch.int32, device=dev), dev, stream)
+    a.pages_out = _vector(pages_out, "pages_out", torch.int32, shape)
+    a.lens_out = _vector(lens_out, "lens_out", torch.int32, (batch,))
+    ws, captured = _workspace_of(need.value, ws, dev, stream, prepared, "select")
+    if ws is not None:
+        a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
+    call = _caller(lib().nvfp4_kv_select, (ctypes.byref(a),), dev, stream, (pages_out, lens_out),
+                   (a, cache, q, bounds, page_table, seq_lens, pages_out, lens_out, ws))
+    return _clearing(call, ws, NVFP4_SELECT_COUNTER_BYTES, dev, stream) if captured else call
+
+
+def kv_select_prepared(q, cache, bounds, page_table, seq_lens, budget, pages_out=None, lens_out=None, ws=None, stream=None):
+    """kv_select() prepared, as attn_decode_prepared() is; its .outputs are the buffers that it fills."""
+    return _kv_select(q, cache, bounds, page_table, seq_lens, budget, pages_out, lens_out, ws, stream, True)
+
+
+def kv_select(q, cache, bounds, page_table, seq_lens, budget, pages_out=None, lens_out=None, ws=None, stream=None):
+    """The pages that each kv head's queries q (as in attn_decode()) attend to: the last one, and those of the others that
+    bounds (kv_bounds()) rank highest, `budget` at most.  Returns (pages int32 [batch][kv_heads][budget], lens int32
+    [batch]), a page table and lengths for attn_decode().  ws: as in attn_decode()."""
+    return _kv_select(q, cache, bounds, page_table, seq_lens, budget, pages_out, lens_out, ws, stream, False)()
+
+
+def _attn_weigh(q, cache, page_table, seq_lens, weights, decay, weights_out, scale, window, out, lse, ws, stream, prepared):
+    if weights_out is None:
+        weights_out = weights
+    if weights_out is None or (weights is None and decay != 0):
+        raise ValueError("without weights, decay must be 0 and weights_out given")
+    shape = (q.shape[0], cache.kv_heads, page_table.shape[-1])
+
+    def wrap(a):
+        return AttnWeighArgs(attn=a, decay=decay, weights_out=_vector(weights_out, "weights_out", torch.float32, shape),
+                             weights=None if weights is None else _vector(weights, "weights", torch.float32, shape))
+    return _attn(q, cache, page_table, seq_lens, scale, window, out, lse, ws, stream, prepared, "nvfp4_attn_weigh", wrap,
+                 weights_out, weights=weights, weights_out=weights_out)
+
+
+def attn_weigh_prepared(q, cache, page_table, seq_lens, weights, decay=1.0, weights_out=None, scale=None, window=0, out=None,
+                        lse=None, ws=None, stream=None):
+    """attn_weigh() prepared, as attn_decode_prepared() is."""
+    return _attn_weigh(q, cache, page_table, seq_lens, weights, decay, weights_out, scale, window, out, lse, ws, stream, True)
+
+
+def attn_weigh(q, cache, page_table, seq_lens, weights, decay=1.0, weights_out=None, scale=None, window=0, out=None, lse=None,
+               ws=None, stream=None):
+    """attn_decode(), and the attention weight that its query heads give to each page added to decay * weights: float32
+    [batch][kv_heads][pages], updated in place unless weights_out is given.  Returns (out, weights_out), or (out, lse,
+    weights_out) with lse.  weights may be None if decay is 0."""
+    return _attn_weigh(q, cache, page_table, seq_lens, weights, decay, weights_out, scale, window, out, lse, ws, stream, False)()
+
+
+def kv_evict_prepared(weights, page_table, seq_lens, page_size, budget, sink=0, recent=1, table_out=None, lens_out=None,
+                      freed=None, weights_out=None, stream=None):
+    """kv_evict() with its arguments marshalled once: returns a zero-argument callable that returns its outputs."""
+    if weights.dim() != 3:
+        raise ValueError(f"weights must be [batch][kv_heads][pages], not {tuple(weights.shape)}")
+    batch, kv_heads, width = weights.shape
+    dev = _device_of(stream, weights=weights, page_table=page_table, seq_lens=seq_lens, table_out=table_out,
+                     lens_out=lens_out, freed=freed, weights_out=weights_out)
+    a = KvEvictArgs(batch=batch, kv_heads=kv_heads, page_size=page_size,
+                    weights=_vector(weights, "weights", torch.float32, (batch, kv_heads, width)),
+                    page_table=_vector(page_table, "page_table", torch.int32, (batch, width)), table_width=width,
+                    seq_lens=_vector(seq_lens, "seq_lens", torch.int32, (batch,)), budget=budget, sink=sink, recent=recent)
+    need = ctypes.c_size_t()
+    check(lib().nvfp4_kv_evict_workspace_bytes(ctypes.byref(a), ctypes.byref(need)))
+
+    def output(t, name, dtype, *shape):
+        if t is None:
+            t = _new(lambda: torch.empty(shape, dtype=dtype, device=dev), dev, stream)
+        setattr(a, name, _vector(t, name, dtype, shape))
+        return t
+
+    outputs = (output(table_out, "table_out", torch.int32, batch, budget), output(lens_out, "lens_out", torch.int32, batch),
+               output(freed, "freed", torch.int32, batch, width),
+               output(weights_out, "weights_out", torch.float32, batch, kv_heads, budget))
+    ws = _new(lambda: torch.empty(need.value, dtype=torch.uint8, device=dev), dev, stream) if need.value else None
+    if ws is not None:
+        a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel()
+    return _caller(lib().nvfp4_kv_evict, (ctypes.byref(a),), dev, stream, outputs,
+                   (a, weights, page_table, seq_lens, ws, *outputs))
+
+
+def kv_evict(weights, page_table, seq_lens, page_size, budget, sink=0, recent=1, table_out=None, lens_out=None, freed=None,
+             weights_out=None, stream=None):
+    """Keeps up to `budget` pages of each sequence: the last `recent`, the first `sink`, and the others by their weights
+    (attn_weigh()) over all kv heads.  Returns (table_out int32 [batch][budget], lens_out int32 [batch], freed int32
+    [batch][pages], weights_out float32 [batch][kv_heads][budget]): the kept pages in order with the lengths and weights
+    that go with them, and the pages dropped; -1 and 0 behind them."""
+    return kv_evict_prepared(weights, page_table, seq_lens, page_size, budget, sink, recent, table_out, lens_out, freed,
+                             weights_out, stream)()

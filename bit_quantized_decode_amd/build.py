@@ -15,7 +15,8 @@ LIB = os.path.join(HERE, "libnvfp4.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 
 SOURCES = ["pack.hip", "quantize.hip", "gemv.hip", "skinny.hip", "prefill.hip", "moe.hip", "w4a4.hip", "abi.cpp",
-           "rope.hip", "kv_cache.hip", "attn_decode.hip", "attn_abi.cpp"]
+           "rope.hip", "kv_cache.hip", "attn_decode.hip", "attn_abi.cpp",
+           "attn_shared.hip", "attn_pages.hip", "kv_bounds.hip", "kv_select.hip", "attn_long_abi.cpp"]
 # The benchmark's ceiling probes: a library of their own, not part of the product.
 PROBES_SRC = "probes.hip"
 PROBES_LIB = os.path.join(HERE, "libnvfp4_probes.so")

@@ -82,4 +82,72 @@ bool attn_fits(const AttnLaunch& a);
 size_t attn_workspace_bytes(const AttnLaunch& a);
 hipError_t launch_attn_decode(const AttnLaunch& a, hipStream_t s);
 
+// ---- reading less of a long cache (attn_long_abi.cpp) ----
+
+// Page tables of [batch][kv_heads][table_width].
+hipError_t launch_attn_heads(const AttnLaunch& a, hipStream_t s);
+
+struct AttnSharedLaunch {
+  AttnLaunch attn;         // of the sequences' own tokens, its workspace the call's
+  const int32_t* prefix_table;
+  int64_t prefix_width;
+  const int32_t* prefix_len;
+};
+// Whether the prefix's tiles can be numbered in 31 bits too.
+bool attn_shared_fits(const AttnSharedLaunch& a);
+size_t attn_shared_workspace_bytes(const AttnSharedLaunch& a);
+hipError_t launch_attn_shared(const AttnSharedLaunch& a, hipStream_t s);
+
+struct AttnWeighLaunch {
+  AttnLaunch attn;
+  const float* weights;    // [batch][kv_heads][table_width]; nullptr if decay == 0
+  float decay;
+  float* weights_out;
+};
+size_t attn_weigh_workspace_bytes(const AttnWeighLaunch& a);
+hipError_t launch_attn_weigh(const AttnWeighLaunch& a, hipStream_t s);
+
+struct KvBoundsLaunch {
+  KvCache cache;
+  int format;
+  int64_t n;
+  const int32_t* pages;
+  uint16_t* bounds;        // [pages][heads][2][head_dim]
+};
+hipError_t launch_kv_bounds(const KvBoundsLaunch& a, hipStream_t s);
+
+struct KvSelectLaunch {
+  int64_t batch;
+  int32_t heads, head_dim, group, pages, page_size;
+  const uint16_t* q;
+  int64_t ldq;
+  const uint16_t* bounds;
+  const int32_t* table;
+  int64_t table_width;
+  const int32_t* lens;
+  int64_t budget;
+  int32_t* pages_out;      // [batch][heads][budget]
+  int32_t* lens_out;       // [batch]
+  void* ws;
+};
+size_t kv_select_workspace_bytes(const KvSelectLaunch& a);
+hipError_t launch_kv_select(const KvSelectLaunch& a, hipStream_t s);
+
+struct KvEvictLaunch {
+  int64_t batch;
+  int32_t heads, page_size;
+  const float* weights;    // [batch][heads][table_width]
+  const int32_t* table;
+  int64_t table_width;
+  const int32_t* lens;
+  int64_t budget, sink, recent;
+  int32_t* table_out;      // [batch][budget]
+  int32_t* lens_out;       // [batch]
+  int32_t* freed;          // nullptr, or [batch][table_width]
+  float* weights_out;      // nullptr, or [batch][heads][budget]
+  void* ws;
+};
+size_t kv_evict_workspace_bytes(const KvEvictLaunch& a);
+hipError_t launch_kv_evict(const KvEvictLaunch& a, hipStream_t s);
+
 }  // namespace nvfp4

@@ -1,0 +1,105 @@
+// Attention of one new token per sequence over pages chosen for each kv head (nvfp4_attn_decode_heads), and
+// attention that adds up the weight that each page has had (nvfp4_attn_weigh).
+//
+// Both are attn_kernel (attn_kernel.h).  The first looks its pages up in a table of its own for each kv head.
+// The second keeps the sum of the terms of every sixteen tokens, a byproduct of the pass over the cache: in log2, with
+// the row's reference in it, since that may still move.  A second launch, when the rows' lse is known, turns
+// the sums of a page into its weight:
+//   weight_i = sum over the group's rows r and the page's sixteens t of 2^(mass_rt - lse_r log2 e).
+// Sums of sixteen tokens are 4 bytes a row, for 16 * 2 * head_dim values of the cache; they are read from the cache that
+// they were just written to.
+#include "attn_kernel.h"
+
+namespace nvfp4 {
+namespace {
+
+struct WeighParams {
+  AttnParams attn;
+  const float* mass;
+  const float* weights;
+  float* weights_out;
+  int64_t groups;
+  float decay;
+};
+
+// LANES lanes take one page of one kv head.
+template <int LANES>
+__global__ __launch_bounds__(256) void weigh_kernel(const WeighParams w) {
+  const AttnParams& a = w.attn;
+  const int64_t item = ((int64_t)blockIdx.x * 256 + threadIdx.x) / LANES;
+  const int lane = threadIdx.x % LANES;
+  const int64_t unit = item / a.table_width;                 // (sequence, kv head)
+  if (unit >= (int64_t)a.batch * a.cache.heads) return;
+  const int b = (int)(unit / a.cache.heads), head = (int)(unit - (int64_t)b * a.cache.heads);
+  const int page = (int)(item - unit * a.table_width);
+  const Span sp = span_of(a, a.lens[b]);
+  // The page's tokens inside the span (offsets below 2^30), as sixteens from the span's base on.
+  const int from = max(page * a.cache.page_size, sp.begin), to = min((page + 1) * a.cache.page_size, sp.end);
+  float sum = 0.0f;
+  if (from < to) {
+    const int first = (from - sp.base) / kKvGroup, n = (to - 1 - sp.base) / kKvGroup + 1 - first;
+    for (int rt = 0; rt < a.row_tiles; ++rt) {
+      const float* mass = w.mass + ((unit * a.row_tiles + rt) * w.groups + first) * a.part_rows;
+      const int rows = min(a.group - rt * kRows, kRows);
+      const float* lse = a.lse + (int64_t)b * a.q_heads + head * a.group + rt * kRows;
+      for (int e = lane; e < n * a.part_rows; e += LANES) {
+        const int r = e % a.part_rows;
+        const float l = r < rows ? lse[r] : kNegInf;
+        if (l != kNegInf) sum += __builtin_amdgcn_exp2f(mass[e] - l * (float)kLog2e);   // a row without a token: nothing
+      }
+    }
+  }
+#pragma unroll
+  for (int off = LANES / 2; off >= 1; off >>= 1) sum += __shfl_xor(sum, off);
+  if (lane == 0) w.weights_out[item] = w.decay == 0.0f ? sum : w.decay * w.weights[item] + sum;
+}
+
+int64_t mass_groups_of(const AttnLaunch& a) {
+  const int64_t most = a.table_width * a.cache.gpp;
+  return a.window > 0 && a.window / kKvGroup + 2 < most ? a.window / kKvGroup + 2 : most;
+}
+
+size_t rounded(size_t bytes) { return (bytes + 255) & ~(size_t)255; }
+
+size_t mass_bytes(const AttnLaunch& a) {
+  return rounded((size_t)(a.batch * a.cache.heads * row_tiles_of(a)) * (size_t)mass_groups_of(a) * part_rows_of(a) * sizeof(float));
+}
+
+}  // namespace
+
+hipError_t launch_attn_heads(const AttnLaunch& a, hipStream_t s) {
+  ModeParams<kHeads> p;
+  fill_params(a, p);
+  return attn_launch(a, p, s);
+}
+
+size_t attn_weigh_workspace_bytes(const AttnWeighLaunch& a) {
+  return rounded(attn_workspace_bytes(a.attn)) + mass_bytes(a.attn) + (size_t)a.attn.batch * a.attn.q_heads * sizeof(float);
+}
+
+hipError_t launch_attn_weigh(const AttnWeighLaunch& a, hipStream_t s) {
+  ModeParams<kWeigh> p;
+  fill_params(a.attn, p);
+  uint8_t* mass = static_cast<uint8_t*>(a.attn.ws) + rounded(attn_workspace_bytes(a.attn));
+  p.mass = reinterpret_cast<float*>(mass);
+  p.groups = mass_groups_of(a.attn);
+  if (!p.lse) p.lse = reinterpret_cast<float*>(mass + mass_bytes(a.attn));
+  const hipError_t e = attn_launch(a.attn, p, s);
+  if (e != hipSuccess || a.attn.table_width == 0) return e;
+  WeighParams w;
+  w.attn = p;
+  w.mass = p.mass;
+  w.weights = a.weights;
+  w.weights_out = a.weights_out;
+  w.groups = p.groups;
+  w.decay = a.decay;
+  // Lanes a page: sixteen where they find up to eight sums each, a wavefront beyond.
+  const int64_t pages = a.attn.batch * a.attn.cache.heads * a.attn.table_width;
+  if (a.attn.cache.gpp * p.part_rows <= 128)
+    hipLaunchKernelGGL((weigh_kernel<16>), dim3((unsigned)((pages + 15) / 16)), dim3(256), 0, s, w);
+  else
+    hipLaunchKernelGGL((weigh_kernel<64>), dim3((unsigned)((pages + 3) / 4)), dim3(256), 0, s, w);
+  return hipGetLastError();
+}
+
+}  // namespace nvfp4

@@ -1,0 +1,332 @@
+// Attention of one new token per sequence where all sequences share a long prefix (nvfp4_attn_shared).
+//
+// Softmax sums over the prefix and over a sequence's own tokens join as any two stretches of one row do:
+// with references r, r' and sums l, l' of terms 2^(s - r), the joined sums are those of the larger
+// reference, the other's times 2^(r' - r).  So the prefix is one problem of its own: for each kv head, the
+// queries of all sequences and of its group are the rows of a matrix, and its keys and values are read once for
+// all of them.  A first launch leaves the prefix's partial sums; a second, attn_kernel over the own
+// tokens, joins them to each row as it writes it.
+//
+// The tiles and operands are those of attn_kernel.h.  Here a wavefront holds RT tiles of sixteen rows: one
+// 32-token tile of the cache is read, and dequantised, once for 16 RT rows, and RT independent chains of
+// matrix instructions and exponentials fill each other's waits.  The four (or eight) wavefronts of a
+// workgroup take the tiles of its share in turn and join through LDS at its end.
+#include "attn_kernel.h"
+
+namespace nvfp4 {
+namespace {
+
+struct PrefixParams {
+  KvCache cache;
+  const uint16_t* q;
+  int64_t ldq;
+  Prefix prefix;
+  int32_t rows;        // of a kv head: batch * group
+  int32_t group;
+  float score_factor;
+  int score_exp;
+};
+
+// Row tiles of a wavefront: as many as the rows fill, and registers hold.
+constexpr int max_row_tiles(int db) { return db >= 3 ? 2 : 4; }
+constexpr int prefix_waves(int fmt, int db, int rt) { return rt == 1 ? waves_per_simd(fmt, db) : 1; }
+
+template <int FMT, int DB, int RT>
+__global__ __launch_bounds__(256 * prefix_waves(FMT, DB, RT), (prefix_waves(FMT, DB, RT))) void prefix_kernel(const PrefixParams a) {
+  using L = KvLayout<FMT, DB>;
+  constexpr int kWaves = 4 * prefix_waves(FMT, DB, RT), kThreads = 64 * kWaves, kBlock = kRows * RT;
+  constexpr int kDp = 64 * DB, kE = L::kE, kW = L::kW, kSteps = kE / 8, kQuads = kE / 4;
+  struct Sums {
+    float ml[kWaves][kBlock][2];
+    float o[kWaves][kBlock][kDp + 4] __attribute__((aligned(16)));
+  };
+  __shared__ Sums lds;
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int qn = lane & 15, h = lane >> 4, d0 = kE * h;
+  const int len = prefix_len(a.prefix), tiles = (len + kTile - 1) / kTile;
+  const Cut shares = prefix_cut(a.prefix, tiles);
+  if ((int)blockIdx.x >= shares.n) return;
+  // Neighbouring shares on one XCD, whose L2 then serves a kv head's other blocks of rows.
+  const int xcd = blockIdx.x & 7, each = shares.n >> 3, more = shares.n & 7;
+  const int w = xcd * each + min(xcd, more) + (int)(blockIdx.x >> 3);
+  const int s1 = run_start(shares, w + 1);
+
+  for (int s = run_start(shares, w); s < s1;) {
+    const int unit = (int)((unsigned)s / (unsigned)tiles), t0 = s - unit * tiles, t1 = min(tiles, t0 + s1 - s);
+    const int head = unit / a.prefix.row_blocks, row0 = (unit - head * a.prefix.row_blocks) * kBlock;
+    const int count = max((t1 - t0 - wave + kWaves - 1) / kWaves, 0);
+
+    // Queries: lane (q, h) holds values E h .. E h + E - 1 of its row of each tile; rows and values that are not
+    // there: zeros, from addresses inside.
+    uint32_t qv[RT][kE / 2];
+    float score_scale[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      const int row = row0 + kRows * rt + qn, d_here = a.cache.head_dim - d0;
+      const bool in = row < a.rows && d_here > 0;
+      const int b = in ? row / a.group : 0, qh = head * a.group + (in ? row - b * a.group : 0);
+      const uint16_t* qp = a.q + (int64_t)b * a.ldq + qh * a.cache.head_dim + (in ? d0 : 0);
+      const int last = in ? d_here - 8 : 0;
+#pragma unroll
+      for (int i = 0; i < kE / 8; ++i) {
+        const u32x4 x = load16(qp + min(8 * i, last));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) qv[rt][4 * i + j] = in && 8 * i <= last ? x[j] : 0u;
+      }
+      score_scale[rt] = query_scale<FMT>(qv[rt], a.score_factor, a.score_exp);
+    }
+
+    // Page lookups, as in attn_kernel, of this wavefront's tiles.
+    int looked_up = -1;
+    const auto look_up = [&](int it, int (&group)[2]) {
+      if ((it & 31) == 0) {
+        const int tok = (t0 + wave + kWaves * (it + (lane >> 1))) * kTile + (lane & 1) * kKvGroup;
+        looked_up = -1;
+        if (it + (lane >> 1) < count && tok < len) {
+          const int tg = tok / kKvGroup, pg = tg / a.cache.gpp;
+          const int page = a.prefix.table[pg];
+          if (page >= 0 && page < a.cache.pages)
+            looked_up = (page * a.cache.heads + head) * a.cache.gpp + (tg - pg * a.cache.gpp);
+        }
+      }
+      group[0] = __builtin_amdgcn_readlane(looked_up, 2 * (it & 31));
+      group[1] = __builtin_amdgcn_readlane(looked_up, 2 * (it & 31) + 1);
+    };
+    GroupBuffers from[2];
+    const auto to_load = [&](const int (&group)[2]) {
+      from[0] = group_buffers<FMT, DB>(a.cache, group[0]);
+      from[1] = group_buffers<FMT, DB>(a.cache, group[1]);
+    };
+
+    f32x4 o[RT][kW];
+    float ref[RT], sum[RT], shift[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+#pragma unroll
+      for (int i = 0; i < kW; ++i) o[rt][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      ref[rt] = kNegInf;
+      sum[rt] = shift[rt] = 0.0f;
+    }
+    Tile<FMT, DB> t;
+    int group[2];
+    look_up(0, group);
+    to_load(group);
+    load_k<FMT, DB>(from, lane, t);
+    __builtin_amdgcn_sched_barrier(0);
+    load_v<FMT, DB>(from, lane, t);
+    __builtin_amdgcn_sched_barrier(0);
+
+    for (int it = 0; it < count; ++it) {
+      const int tok0 = (t0 + wave + kWaves * it) * kTile;
+      const bool has0 = group[0] >= 0, has1 = group[1] >= 0;
+      const bool whole = has0 && has1 && tok0 + kTile <= len;
+      if (it + 1 < count) look_up(it + 1, group);
+      else group[0] = group[1] = -1;
+      to_load(group);
+      uint32_t okbits = 0xffu;
+      if (!whole) {
+        okbits = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int tok = tok0 + (i / 4) * kKvGroup + 4 * h + i % 4;
+          okbits |= ((i / 4 ? has1 : has0) && tok < len) ? 1u << i : 0u;
+        }
+      }
+
+      float x[RT][8];
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        f32x4 acc[RT];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) acc[rt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) {
+          uint32_t op[4];
+          k_operand<FMT, DB>(t, half, k, op);
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) acc[rt] = mma<FMT>(op, &qv[rt][4 * k], acc[rt]);
+        }
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[rt][4 * half + i] = rounded_product(acc[rt][i], score_scale[rt]);
+      }
+      load_k<FMT, DB>(from, lane, t);
+
+      uint32_t hi[RT][4], lo[RT][4];
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        if (!whole) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[rt][i] = (okbits >> i) & 1u ? x[rt][i] : kNegInf;
+        }
+        float top = x[rt][0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) top = fmaxf(top, x[rt][i]);
+        if (__any(top - ref[rt] > Softmax<FMT>::kOffset + Softmax<FMT>::kSlack)) {
+          const float alpha = move_reference<FMT>(top, ref[rt]);
+          shift[rt] = ref[rt] == kNegInf ? 0.0f : ref[rt];
+          sum[rt] *= alpha;
+#pragma unroll
+          for (int i = 0; i < kW; ++i) o[rt][i] *= alpha;
+        }
+        float p[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          p[i] = __builtin_amdgcn_exp2f(x[rt][i] - shift[rt]);
+          sum[rt] += p[i];
+        }
+        split_terms<FMT>(p, hi[rt], lo[rt]);
+      }
+
+      if (!whole) clear_masked<FMT, DB>(t, okbits);
+      uint32_t vt[8][2 * DB];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v_token<FMT, DB>(t, i / 4, i % 4, vt[i]);
+      uint32_t op[kW][4];
+#pragma unroll
+      for (int j = 0; j < kW; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          op[j][i] = __builtin_amdgcn_perm(vt[2 * i + 1][j / 2], vt[2 * i][j / 2], j % 2 ? 0x07060302u : 0x05040100u);
+      load_v<FMT, DB>(from, lane, t);
+#pragma unroll
+      for (int j = 0; j < kW; ++j)
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+          o[rt][j] = mma<FMT>(op[j], hi[rt], o[rt][j]);
+          if constexpr (FMT != kKvNvfp4) o[rt][j] = mma<FMT>(op[j], lo[rt], o[rt][j]);
+        }
+    }
+
+    // The wavefronts' sums, joined by all threads into the piece.
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      const int r = kRows * rt + qn;
+      sum[rt] += lane_xor(sum[rt], 16);
+      sum[rt] += lane_xor(sum[rt], 32);
+      if (h == 0) {
+        lds.ml[wave][r][0] = ref[rt];
+        lds.ml[wave][r][1] = sum[rt];
+      }
+      // o[rt][j][i] is d = W (4h + i) + j of row q.
+#pragma unroll
+      for (int u = 0; u < kQuads; ++u) {
+        const int i = 4 * u / kW, j = 4 * u % kW;
+        *reinterpret_cast<f32x4*>(&lds.o[wave][r][d0 + 4 * u]) = f32x4{o[rt][j][i], o[rt][j + 1][i], o[rt][j + 2][i], o[rt][j + 3][i]};
+      }
+    }
+    __syncthreads();
+    float* piece = a.prefix.part + (int64_t)(unit + w) * kBlock * (kDp + 4);
+    const int rows = min(a.rows - row0, kBlock);
+    for (int e = tid; e < rows * (kDp / 4); e += kThreads) {
+      const int r = e / (kDp / 4), d = 4 * (e - r * (kDp / 4));
+      float top = lds.ml[0][r][0], l = 0.0f;
+#pragma unroll
+      for (int i = 1; i < kWaves; ++i) top = fmaxf(top, lds.ml[i][r][0]);
+      f32x4 acc{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int i = 0; i < kWaves; ++i) {
+        const float m = lds.ml[i][r][0];
+        const float f = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m - top);
+        l += lds.ml[i][r][1] * f;
+        acc += *reinterpret_cast<const f32x4*>(&lds.o[i][r][d]) * f;
+      }
+      if (d == 0) *reinterpret_cast<f32x4*>(piece + r * (kDp + 4)) = f32x4{top, l, 0.0f, 0.0f};
+      *reinterpret_cast<f32x4*>(piece + r * (kDp + 4) + 4 + d) = acc;
+    }
+    __syncthreads();
+    s += t1 - t0;
+  }
+}
+
+int head_rows_of(const AttnSharedLaunch& a) { return (int)(a.attn.batch * (a.attn.q_heads / a.attn.cache.heads)); }
+
+int padded_of(const AttnSharedLaunch& a) { return (a.attn.cache.head_dim + 63) / 64; }
+
+int block_tiles_of(const AttnSharedLaunch& a) {
+  const int tiles = (head_rows_of(a) + kRows - 1) / kRows, most = max_row_tiles(padded_of(a));
+  return tiles == 1 ? 1 : tiles == 2 || most == 2 ? 2 : 4;
+}
+
+int64_t prefix_units_of(const AttnSharedLaunch& a) {
+  const int block = kRows * block_tiles_of(a);
+  return (int64_t)a.attn.cache.heads * ((head_rows_of(a) + block - 1) / block);
+}
+
+int64_t prefix_tiles_of(const AttnSharedLaunch& a) { return (a.prefix_width * a.attn.cache.page_size + kTile - 1) / kTile; }
+
+int prefix_grid_of(const AttnSharedLaunch& a) {
+  const int64_t shares = (prefix_units_of(a) * prefix_tiles_of(a) + kPrefixShare - 1) / kPrefixShare;
+  return (int)(shares < kCus ? shares : kCus);
+}
+
+size_t own_bytes(const AttnSharedLaunch& a) { return (attn_workspace_bytes(a.attn) + 255) & ~(size_t)255; }
+
+template <int FMT, int DB>
+void prefix_launch(const AttnSharedLaunch& a, const PrefixParams& p, hipStream_t s) {
+  const dim3 grid((unsigned)p.prefix.grid);
+  switch (p.prefix.block_rows / kRows) {
+    case 1: hipLaunchKernelGGL((prefix_kernel<FMT, DB, 1>), grid, dim3(256 * prefix_waves(FMT, DB, 1)), 0, s, p); break;
+    case 2: hipLaunchKernelGGL((prefix_kernel<FMT, DB, 2>), grid, dim3(256 * prefix_waves(FMT, DB, 2)), 0, s, p); break;
+    default:
+      if constexpr (max_row_tiles(DB) == 4)
+        hipLaunchKernelGGL((prefix_kernel<FMT, DB, 4>), grid, dim3(256 * prefix_waves(FMT, DB, 4)), 0, s, p);
+  }
+}
+
+template <int FMT>
+void prefix_launch_db(const AttnSharedLaunch& a, const PrefixParams& p, hipStream_t s) {
+  switch (padded_of(a)) {
+    case 1: prefix_launch<FMT, 1>(a, p, s); break;
+    case 2: prefix_launch<FMT, 2>(a, p, s); break;
+    case 3: prefix_launch<FMT, 3>(a, p, s); break;
+    default: prefix_launch<FMT, 4>(a, p, s); break;
+  }
+}
+
+}  // namespace
+
+bool attn_shared_fits(const AttnSharedLaunch& a) {
+  if (a.attn.batch * a.attn.q_heads > (int64_t(1) << 30)) return false;
+  return prefix_units_of(a) * (prefix_tiles_of(a) + 1) < (int64_t(1) << 31);
+}
+
+size_t attn_shared_workspace_bytes(const AttnSharedLaunch& a) {
+  if (prefix_grid_of(a) == 0) return own_bytes(a);
+  return own_bytes(a) + (size_t)(prefix_units_of(a) + prefix_grid_of(a)) * (kRows * block_tiles_of(a)) * (64 * padded_of(a) + 4) * sizeof(float);
+}
+
+hipError_t launch_attn_shared(const AttnSharedLaunch& a, hipStream_t s) {
+  PrefixParams p;
+  p.cache = a.attn.cache;
+  p.q = a.attn.q;
+  p.ldq = a.attn.ldq;
+  p.rows = head_rows_of(a);
+  p.group = a.attn.q_heads / a.attn.cache.heads;
+  p.score_factor = score_factor_of(a.attn, p.score_exp);
+  p.prefix.len = a.prefix_len;
+  p.prefix.table = a.prefix_table;
+  p.prefix.part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.attn.ws) + own_bytes(a));
+  p.prefix.most = (int32_t)(a.prefix_width * a.attn.cache.page_size);
+  p.prefix.units = (int32_t)prefix_units_of(a);
+  p.prefix.row_blocks = p.prefix.units / a.attn.cache.heads;
+  p.prefix.block_rows = kRows * block_tiles_of(a);
+  p.prefix.grid = prefix_grid_of(a);
+  if (p.prefix.grid > 0) {
+    switch (a.attn.format) {
+      case kKvBf16: prefix_launch_db<kKvBf16>(a, p, s); break;
+      case kKvE4m3: prefix_launch_db<kKvE4m3>(a, p, s); break;
+      default: prefix_launch_db<kKvNvfp4>(a, p, s); break;
+    }
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  ModeParams<kSuffix> own;
+  fill_params(a.attn, own);
+  own.prefix = p.prefix;
+  return attn_launch(a.attn, own, s);
+}
+
+}  // namespace nvfp4
