@@ -118,7 +118,7 @@ enum Mode {
   kPlain,
   kHeads,    // the page table is [batch][kv_heads][table_width]
   kWeigh,    // the terms of every sixteen tokens are summed and kept, for the weights of pages
-  kSuffix    // a prefix that all sequences share, attended to by an earlier launch, is joined to each row
+  kRaw       // rows are left as reference, sum and sums, for a later join
 };
 template <int MODE>
 struct ModeParams : AttnParams {};
@@ -131,29 +131,10 @@ struct ModeParams<kWeigh> : AttnParams {
   int64_t groups;      // sixteens of a unit, at most
 };
 
-// The shared prefix's partial sums.  Its units are (kv head, block of rows), a kv head's rows those of
-// all sequences, (sequence, query head of the group) in order.  The line of all units' tiles is
-// cut evenly over `grid` workgroups, fewer where there is little to do; the piece of unit u that workgroup w
-// leaves has the number u + w (along the line, each piece has one more workgroup or one more unit behind it).
-struct Prefix {
-  const int32_t* len;
-  const int32_t* table;
-  float* part;         // [piece][block_rows][DP + 4]: reference, sum, two unused, the padded head's sums
-  int32_t most;        // tokens that the table holds
-  int32_t units, row_blocks, block_rows, grid;
-};
-constexpr int kPrefixShare = 4;   // tiles of a workgroup's share, at least: one a wavefront
-__device__ __forceinline__ int prefix_len(const Prefix& p) {
-  const int len = *p.len;
-  return len < 0 ? 0 : len > p.most ? p.most : len;
-}
-__device__ __forceinline__ Cut prefix_cut(const Prefix& p, int tiles) {
-  const int line = p.units * tiles;
-  return cut_of(line, min(p.grid, (line + kPrefixShare - 1) / kPrefixShare));
-}
+// kRaw: [batch][q_heads][DP + 4], as partial sums are.
 template <>
-struct ModeParams<kSuffix> : AttnParams {
-  Prefix prefix;
+struct ModeParams<kRaw> : AttnParams {
+  float* raw;
 };
 
 // The tokens that a row attends to.
@@ -459,6 +440,18 @@ __device__ __forceinline__ void write_out(const AttnParams& a, int b, int qh, in
   if (d == 0 && a.lse) a.lse[(int64_t)b * a.q_heads + qh] = some ? (ref + __builtin_amdgcn_logf(l)) * kLn2 : kNegInf;
 }
 
+// The same as MODE has it.
+template <int DP, int MODE>
+__device__ __forceinline__ void write_row(const ModeParams<MODE>& a, int b, int qh, int d, float ref, float l, f32x4 acc) {
+  if constexpr (MODE == kRaw) {
+    float* to = a.raw + ((int64_t)b * a.q_heads + qh) * (DP + 4);
+    if (d == 0) *reinterpret_cast<f32x4*>(to) = f32x4{ref, l, 0.0f, 0.0f};
+    *reinterpret_cast<f32x4*>(to + 4 + d) = acc;
+  } else {
+    write_out(a, b, qh, d, ref, l, acc);
+  }
+}
+
 // Adds (m, l, v) to running sums under the larger reference.
 __device__ __forceinline__ void add_part(float& top, float& sum, f32x4& acc, float m, float l, f32x4 v) {
   const float next = fmaxf(top, m);
@@ -467,40 +460,6 @@ __device__ __forceinline__ void add_part(float& top, float& sum, f32x4& acc, flo
   sum = sum * fo + l * fi;
   acc = acc * fo + v * fi;
   top = next;
-}
-
-// Joins what the shared prefix left of row `qh` of sequence b to its sums, values d0 .. d0 + 4 N - 1.
-template <int DP, int N>
-__device__ __forceinline__ void add_prefix(const ModeParams<kSuffix>& a, int b, int qh, int d0, float& ref, float& l, f32x4 (&acc)[N]) {
-  const int tiles = (prefix_len(a.prefix) + kTile - 1) / kTile;
-  if (a.lens[b] < 0 || tiles == 0) return;   // a free place of the batch, or no prefix
-  const int head = qh / a.group, row = b * a.group + qh - head * a.group;
-  const int block = row / a.prefix.block_rows, r = row - block * a.prefix.block_rows;
-  const int unit = head * a.prefix.row_blocks + block;
-  const Cut c = prefix_cut(a.prefix, tiles);
-  const int w0 = run_of(c, unit * tiles), w1 = run_of(c, unit * tiles + tiles - 1);
-  constexpr int kBatch = N >= 16 ? 2 : N >= 8 ? 4 : 8;   // pieces a round trip, as registers allow
-  for (int w = w0; w <= w1; w += kBatch) {
-    f32x4 ml[kBatch], v[kBatch][N];
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      const float* from = a.prefix.part + ((int64_t)(unit + min(w + j, w1)) * a.prefix.block_rows + r) * (DP + 4);
-      ml[j] = *reinterpret_cast<const f32x4*>(from);
-#pragma unroll
-      for (int u = 0; u < N; ++u) v[j][u] = *reinterpret_cast<const f32x4*>(from + 4 + d0 + 4 * u);
-    }
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      if (w + j > w1) break;
-      const float m = ml[j][0], next = fmaxf(ref, m);
-      const float fo = ref == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(ref - next);
-      const float fi = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m - next);
-      l = l * fo + ml[j][1] * fi;
-#pragma unroll
-      for (int u = 0; u < N; ++u) acc[u] = acc[u] * fo + v[j][u] * fi;
-      ref = next;
-    }
-  }
 }
 
 // Joins the partial sums that workgroups wfirst .. wlast left of a unit.  The parts
@@ -551,14 +510,7 @@ __device__ __forceinline__ void join_parts(const ModeParams<MODE>& a, int wfirst
         }
       }
     }
-    if (live && (runs == 1 || run == 0)) {
-      if constexpr (MODE == kSuffix) {
-        f32x4 one[1] = {acc};
-        add_prefix<DP>(a, b, q0 + r, d, top, l, one);
-        acc = one[0];
-      }
-      write_out(a, b, q0 + r, d, top, l, acc);
-    }
+    if (live && (runs == 1 || run == 0)) write_row<DP>(a, b, q0 + r, d, top, l, acc);
   }
 }
 
@@ -916,9 +868,8 @@ __global__ __launch_bounds__(256 * waves_per_simd(FMT, DB), (waves_per_simd(FMT,
       f32x4 acc[kQuads];
 #pragma unroll
       for (int u = 0; u < kQuads; ++u) acc[u] = quad(u);
-      if constexpr (MODE == kSuffix) add_prefix<kDp>(a, b, q0 + qn, d0, ref, sum, acc);
 #pragma unroll
-      for (int u = 0; u < kQuads; ++u) write_out(a, b, q0 + qn, d0 + 4 * u, ref, sum, acc[u]);
+      for (int u = 0; u < kQuads; ++u) write_row<kDp>(a, b, q0 + qn, d0 + 4 * u, ref, sum, acc[u]);
     }
     g = stop;
   }
@@ -951,9 +902,8 @@ __global__ __launch_bounds__(256 * waves_per_simd(FMT, DB), (waves_per_simd(FMT,
       for (int u = 0; u < kQuads; ++u) acc[u] += *reinterpret_cast<const f32x4*>(&lds.o[i][qn][d0 + 4 * u]) * f;
     }
     if (qn < tail.rows) {
-      if constexpr (MODE == kSuffix) add_prefix<kDp>(a, tail.b, tail.q0 + qn, d0, top, sum, acc);
 #pragma unroll
-      for (int u = 0; u < kQuads; ++u) write_out(a, tail.b, tail.q0 + qn, d0 + 4 * u, top, sum, acc[u]);
+      for (int u = 0; u < kQuads; ++u) write_row<kDp>(a, tail.b, tail.q0 + qn, d0 + 4 * u, top, sum, acc[u]);
     }
   }
   const int has_first = lds.has_first, has_last = lds.has_last;

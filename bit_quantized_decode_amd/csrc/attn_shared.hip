@@ -4,8 +4,8 @@
 // with references r, r' and sums l, l' of terms 2^(s - r), the joined sums are those of the larger
 // reference, the other's times 2^(r' - r).  So the prefix is one problem of its own: for each kv head, the
 // queries of all sequences and of its group are the rows of a matrix, and its keys and values are read once for
-// all of them.  A first launch leaves the prefix's partial sums; a second, attn_kernel over the own
-// tokens, joins them to each row as it writes it.
+// all of them.  One launch leaves the prefix's partial sums, attn_kernel those of the own tokens, and a third
+// joins them row by row.
 //
 // The tiles and operands are those of attn_kernel.h.  Here a wavefront holds RT tiles of sixteen rows: one
 // 32-token tile of the cache is read, and dequantised, once for 16 RT rows, and RT independent chains of
@@ -15,6 +15,27 @@
 
 namespace nvfp4 {
 namespace {
+
+// The shared prefix's partial sums.  Its units are (kv head, block of rows), a kv head's rows those of
+// all sequences, (sequence, query head of the group) in order.  The line of all units' tiles is
+// cut evenly over `grid` workgroups, fewer where there is little to do; the piece of unit u that workgroup w
+// leaves has the number u + w (along the line, each piece has one more workgroup or one more unit behind it).
+struct Prefix {
+  const int32_t* len;
+  const int32_t* table;
+  float* part;         // [piece][block_rows][DP + 4]: reference, sum, two unused, the padded head's sums
+  int32_t most;        // tokens that the table holds
+  int32_t units, row_blocks, block_rows, grid;
+};
+constexpr int kPrefixShare = 4;   // tiles of a workgroup's share, at least: one a wavefront
+__device__ __forceinline__ int prefix_len(const Prefix& p) {
+  const int len = *p.len;
+  return len < 0 ? 0 : len > p.most ? p.most : len;
+}
+__device__ __forceinline__ Cut prefix_cut(const Prefix& p, int tiles) {
+  const int line = p.units * tiles;
+  return cut_of(line, min(p.grid, (line + kPrefixShare - 1) / kPrefixShare));
+}
 
 struct PrefixParams {
   KvCache cache;
@@ -28,8 +49,8 @@ struct PrefixParams {
 };
 
 // Row tiles of a wavefront: as many as the rows fill, and registers hold.
-constexpr int max_row_tiles(int db) { return db >= 3 ? 2 : 4; }
-constexpr int prefix_waves(int fmt, int db, int rt) { return rt == 1 ? waves_per_simd(fmt, db) : 1; }
+constexpr int max_row_tiles(int db) { return 2; }
+constexpr int prefix_waves(int fmt, int db, int rt) { return rt == 1 ? waves_per_simd(fmt, db) : db <= 2 ? 2 : 1; }
 
 template <int FMT, int DB, int RT>
 __global__ __launch_bounds__(256 * prefix_waves(FMT, DB, RT), (prefix_waves(FMT, DB, RT))) void prefix_kernel(const PrefixParams a) {
@@ -154,23 +175,35 @@ __global__ __launch_bounds__(256 * prefix_waves(FMT, DB, RT), (prefix_waves(FMT,
       }
       load_k<FMT, DB>(from, lane, t);
 
-      uint32_t hi[RT][4], lo[RT][4];
+      if (!whole) {
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        if (!whole) {
+        for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
           for (int i = 0; i < 8; ++i) x[rt][i] = (okbits >> i) & 1u ? x[rt][i] : kNegInf;
-        }
-        float top = x[rt][0];
+      }
+      // One branch for all row tiles: between it and the next step everything is one stretch of independent chains.
+      float top[RT];
+      bool move = false;
 #pragma unroll
-        for (int i = 1; i < 8; ++i) top = fmaxf(top, x[rt][i]);
-        if (__any(top - ref[rt] > Softmax<FMT>::kOffset + Softmax<FMT>::kSlack)) {
-          const float alpha = move_reference<FMT>(top, ref[rt]);
+      for (int rt = 0; rt < RT; ++rt) {
+        top[rt] = x[rt][0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) top[rt] = fmaxf(top[rt], x[rt][i]);
+        move |= top[rt] - ref[rt] > Softmax<FMT>::kOffset + Softmax<FMT>::kSlack;
+      }
+      if (__any(move)) {
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+          const float alpha = move_reference<FMT>(top[rt], ref[rt]);
           shift[rt] = ref[rt] == kNegInf ? 0.0f : ref[rt];
           sum[rt] *= alpha;
 #pragma unroll
           for (int i = 0; i < kW; ++i) o[rt][i] *= alpha;
         }
+      }
+      uint32_t hi[RT][4], lo[RT][4];
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
         float p[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -241,6 +274,88 @@ __global__ __launch_bounds__(256 * prefix_waves(FMT, DB, RT), (prefix_waves(FMT,
   }
 }
 
+struct JoinParams {
+  Prefix prefix;
+  const float* raw;        // of the own tokens
+  const int32_t* lens;
+  uint16_t* out;
+  float* lse;
+  int64_t ldo;
+  int32_t batch, q_heads, group, head_dim;
+  float v_scale;
+};
+
+// Each row by THREADS threads: its quads of values times as many runs of its pieces.  A run's pieces are read kPieces at a
+// time and added in order, the runs after one another.
+template <int DP, int THREADS>
+__global__ __launch_bounds__(256) void join_kernel(const JoinParams a) {
+  constexpr int kQuads = DP / 4, kRuns = THREADS / kQuads, kPieces = 4, kRowsHere = 256 / THREADS;
+  __shared__ float s_ml[kRowsHere][kRuns][2];
+  __shared__ f32x4 s_o[kRowsHere][kRuns][kQuads];
+  const int t = threadIdx.x % THREADS, at = threadIdx.x / THREADS, run = t / kQuads, d = 4 * (t - run * kQuads);
+  const int64_t row = (int64_t)blockIdx.x * kRowsHere + at;
+  const bool live = row < (int64_t)a.batch * a.q_heads && run < kRuns;
+  const int b = live ? (int)(row / a.q_heads) : 0, qh = live ? (int)(row - (int64_t)b * a.q_heads) : 0;
+  const int tiles = (prefix_len(a.prefix) + kTile - 1) / kTile;
+  float top = kNegInf, l = 0.0f;
+  f32x4 acc{0.0f, 0.0f, 0.0f, 0.0f};
+  if (live && tiles > 0 && a.lens[b] >= 0) {       // below 0: a free place of the batch
+    const int head = qh / a.group, r = b * a.group + qh - head * a.group;
+    const int block = r / a.prefix.block_rows, unit = head * a.prefix.row_blocks + block;
+    const Cut c = prefix_cut(a.prefix, tiles);
+    const int w0 = run_of(c, unit * tiles), n = run_of(c, unit * tiles + tiles - 1) + 1 - w0;
+    const int i1 = n * (run + 1) / kRuns;
+    const float* from = a.prefix.part + ((int64_t)(unit + w0) * a.prefix.block_rows + (r - block * a.prefix.block_rows)) * (DP + 4);
+    const int64_t stride = (int64_t)a.prefix.block_rows * (DP + 4);
+    for (int i = n * run / kRuns; i < i1; i += kPieces) {
+      f32x4 ml[kPieces], v[kPieces];
+#pragma unroll
+      for (int j = 0; j < kPieces; ++j) {
+        const float* p = from + min(i + j, i1 - 1) * stride;
+        ml[j] = *reinterpret_cast<const f32x4*>(p);
+        v[j] = *reinterpret_cast<const f32x4*>(p + 4 + d);
+      }
+#pragma unroll
+      for (int j = 0; j < kPieces; ++j)
+        if (i + j < i1) add_part(top, l, acc, ml[j][0], ml[j][1], v[j]);
+    }
+  }
+  if (live && run == 0) {
+    const float* own = a.raw + row * (DP + 4);
+    add_part(top, l, acc, own[0], own[1], *reinterpret_cast<const f32x4*>(own + 4 + d));
+  }
+  if (kRuns > 1) {
+    if (live) {
+      if (d == 0) {
+        s_ml[at][run][0] = top;
+        s_ml[at][run][1] = l;
+      }
+      s_o[at][run][d / 4] = acc;
+    }
+    __syncthreads();
+    if (live && run == 0) {
+#pragma unroll
+      for (int i = 1; i < kRuns; ++i) add_part(top, l, acc, s_ml[at][i][0], s_ml[at][i][1], s_o[at][i][d / 4]);
+    }
+  }
+  if (!live || run > 0) return;
+  const bool some = l > 0.0f || l != l;  // NaN stays NaN
+  const float f = some ? a.v_scale / l : 0.0f;
+  if (d < a.head_dim) {
+    uint16_t* to = a.out + (int64_t)b * a.ldo + (int64_t)qh * a.head_dim + d;
+    *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(acc[0] * f, acc[1] * f), pack_bf16x2(acc[2] * f, acc[3] * f));
+  }
+  if (d == 0 && a.lse) a.lse[row] = some ? (top + __builtin_amdgcn_logf(l)) * kLn2 : kNegInf;
+}
+
+template <int DP>
+void join_launch(const JoinParams& p, hipStream_t s) {
+  // A wavefront a row where its pieces are few, a workgroup where there are more than it reads at once.
+  const int64_t rows = (int64_t)p.batch * p.q_heads, pieces = p.prefix.grid / p.prefix.units + 1;
+  if (pieces <= 8 * (256 / DP)) hipLaunchKernelGGL((join_kernel<DP, 64>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, s, p);
+  else hipLaunchKernelGGL((join_kernel<DP, 256>), dim3((unsigned)rows), dim3(256), 0, s, p);
+}
+
 int head_rows_of(const AttnSharedLaunch& a) { return (int)(a.attn.batch * (a.attn.q_heads / a.attn.cache.heads)); }
 
 int padded_of(const AttnSharedLaunch& a) { return (a.attn.cache.head_dim + 63) / 64; }
@@ -262,7 +377,13 @@ int prefix_grid_of(const AttnSharedLaunch& a) {
   return (int)(shares < kCus ? shares : kCus);
 }
 
-size_t own_bytes(const AttnSharedLaunch& a) { return (attn_workspace_bytes(a.attn) + 255) & ~(size_t)255; }
+size_t rounded(size_t bytes) { return (bytes + 255) & ~(size_t)255; }
+
+size_t row_bytes(const AttnSharedLaunch& a) { return (64 * padded_of(a) + 4) * sizeof(float); }
+
+// The workspace: attn_kernel's, the own tokens' sums, the prefix's pieces.
+size_t raw_at(const AttnSharedLaunch& a) { return rounded(attn_workspace_bytes(a.attn)); }
+size_t pieces_at(const AttnSharedLaunch& a) { return raw_at(a) + rounded((size_t)(a.attn.batch * a.attn.q_heads) * row_bytes(a)); }
 
 template <int FMT, int DB>
 void prefix_launch(const AttnSharedLaunch& a, const PrefixParams& p, hipStream_t s) {
@@ -294,11 +415,12 @@ bool attn_shared_fits(const AttnSharedLaunch& a) {
 }
 
 size_t attn_shared_workspace_bytes(const AttnSharedLaunch& a) {
-  if (prefix_grid_of(a) == 0) return own_bytes(a);
-  return own_bytes(a) + (size_t)(prefix_units_of(a) + prefix_grid_of(a)) * (kRows * block_tiles_of(a)) * (64 * padded_of(a) + 4) * sizeof(float);
+  if (prefix_grid_of(a) == 0) return attn_workspace_bytes(a.attn);
+  return pieces_at(a) + (size_t)(prefix_units_of(a) + prefix_grid_of(a)) * (kRows * block_tiles_of(a)) * row_bytes(a);
 }
 
 hipError_t launch_attn_shared(const AttnSharedLaunch& a, hipStream_t s) {
+  if (prefix_grid_of(a) == 0) return launch_attn_decode(a.attn, s);   // no prefix
   PrefixParams p;
   p.cache = a.attn.cache;
   p.q = a.attn.q;
@@ -308,25 +430,43 @@ hipError_t launch_attn_shared(const AttnSharedLaunch& a, hipStream_t s) {
   p.score_factor = score_factor_of(a.attn, p.score_exp);
   p.prefix.len = a.prefix_len;
   p.prefix.table = a.prefix_table;
-  p.prefix.part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.attn.ws) + own_bytes(a));
+  p.prefix.part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.attn.ws) + pieces_at(a));
   p.prefix.most = (int32_t)(a.prefix_width * a.attn.cache.page_size);
   p.prefix.units = (int32_t)prefix_units_of(a);
   p.prefix.row_blocks = p.prefix.units / a.attn.cache.heads;
   p.prefix.block_rows = kRows * block_tiles_of(a);
   p.prefix.grid = prefix_grid_of(a);
-  if (p.prefix.grid > 0) {
-    switch (a.attn.format) {
-      case kKvBf16: prefix_launch_db<kKvBf16>(a, p, s); break;
-      case kKvE4m3: prefix_launch_db<kKvE4m3>(a, p, s); break;
-      default: prefix_launch_db<kKvNvfp4>(a, p, s); break;
-    }
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+  switch (a.attn.format) {
+    case kKvBf16: prefix_launch_db<kKvBf16>(a, p, s); break;
+    case kKvE4m3: prefix_launch_db<kKvE4m3>(a, p, s); break;
+    default: prefix_launch_db<kKvNvfp4>(a, p, s); break;
   }
-  ModeParams<kSuffix> own;
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  ModeParams<kRaw> own;
   fill_params(a.attn, own);
-  own.prefix = p.prefix;
-  return attn_launch(a.attn, own, s);
+  own.raw = reinterpret_cast<float*>(static_cast<uint8_t*>(a.attn.ws) + raw_at(a));
+  e = attn_launch(a.attn, own, s);
+  if (e != hipSuccess) return e;
+  JoinParams j;
+  j.prefix = p.prefix;
+  j.raw = own.raw;
+  j.lens = a.attn.lens;
+  j.out = a.attn.out;
+  j.lse = a.attn.lse;
+  j.ldo = a.attn.ldo;
+  j.batch = (int32_t)a.attn.batch;
+  j.q_heads = a.attn.q_heads;
+  j.group = p.group;
+  j.head_dim = a.attn.cache.head_dim;
+  j.v_scale = a.attn.cache.v_scale;
+  switch (padded_of(a)) {
+    case 1: join_launch<64>(j, s); break;
+    case 2: join_launch<128>(j, s); break;
+    case 3: join_launch<192>(j, s); break;
+    default: join_launch<256>(j, s); break;
+  }
+  return hipGetLastError();
 }
 
 }  // namespace nvfp4

@@ -178,7 +178,7 @@ def test_workspaces(L):  # noqa: F811
     plain = need("attn_decode", attn(d))
     blank = dict(q=None, out=None, page_table=None, seq_lens=None, workspace=None, scale=0.0, ldq=0, ldo=0)
     s = need("attn_shared", shared(d, blank, prefix_table=None, prefix_len=None))
-    assert s > plain and need("attn_shared", shared(d, prefix_width=0)) == -(-plain // 256) * 256
+    assert s > plain and need("attn_shared", shared(d, prefix_width=0)) == plain
     w = need("attn_weigh", weigh(d, blank, weights=None, weights_out=None, decay=-1.0))
     assert w > plain + 4 * 4 * 40 * 16
     for name, a, n in (("attn_shared", shared(d, dict(workspace_bytes=s - 1)), s), ("attn_weigh", weigh(d, dict(workspace_bytes=w - 1)), w)):
