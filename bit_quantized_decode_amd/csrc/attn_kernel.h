@@ -201,30 +201,31 @@ __device__ __forceinline__ GroupBuffers group_buffers(const KvCache& c, int grou
 }
 
 constexpr int kStreamed = 2;  // cache policy nt
-template <int FMT, int DB>
+constexpr int kCached = 0;    // for what other workgroups read too
+template <int FMT, int DB, int POLICY = kStreamed>
 __device__ __forceinline__ void load_side(__amdgpu_buffer_rsrc_t r, int side, int lane, uint32_t* w) {
   using L = KvLayout<FMT, DB>;
 #pragma unroll
   for (int i = 0; i < L::kPlanes16; ++i) {
     const u32x4 x =
-        __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, lane * 16, side + i * 1024, kStreamed));
+        __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, lane * 16, side + i * 1024, POLICY));
 #pragma unroll
     for (int j = 0; j < 4; ++j) w[4 * i + j] = x[j];
   }
   if constexpr (L::kPlane8) {
     const u32x2 x = __builtin_bit_cast(
-        u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, lane * 8, side + L::kPlanes16 * 1024, kStreamed));
+        u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, lane * 8, side + L::kPlanes16 * 1024, POLICY));
     w[4 * L::kPlanes16] = x[0];
     w[4 * L::kPlanes16 + 1] = x[1];
   }
 }
 
-template <int FMT, int DB>
+template <int FMT, int DB, int POLICY = kStreamed>
 __device__ __forceinline__ void load_k(const GroupBuffers (&g)[2], int lane, Tile<FMT, DB>& t) {
   using L = KvLayout<FMT, DB>;
 #pragma unroll
   for (int a = 0; a < 2; ++a) {
-    load_side<FMT, DB>(g[a].codes, 0, lane, t.k[a]);
+    load_side<FMT, DB, POLICY>(g[a].codes, 0, lane, t.k[a]);
     if constexpr (FMT == kKvE4m3) t.ks[a] = g[a].scales[lane & 15];
     else if constexpr (FMT == kKvNvfp4) {
       if constexpr (L::kKScaleLane == 1) t.ks[a] = g[a].scales[lane];
@@ -234,12 +235,12 @@ __device__ __forceinline__ void load_k(const GroupBuffers (&g)[2], int lane, Til
   }
 }
 
-template <int FMT, int DB>
+template <int FMT, int DB, int POLICY = kStreamed>
 __device__ __forceinline__ void load_v(const GroupBuffers (&g)[2], int lane, Tile<FMT, DB>& t) {
   using L = KvLayout<FMT, DB>;
 #pragma unroll
   for (int a = 0; a < 2; ++a) {
-    load_side<FMT, DB>(g[a].codes, L::kSideBytes, lane, t.v[a]);
+    load_side<FMT, DB, POLICY>(g[a].codes, L::kSideBytes, lane, t.v[a]);
     if constexpr (FMT == kKvE4m3)
       t.vs[a][0] = *reinterpret_cast<const uint32_t*>(g[a].scales + L::kKScaleBytes + 4 * (lane >> 4));
     else if constexpr (FMT == kKvNvfp4) {

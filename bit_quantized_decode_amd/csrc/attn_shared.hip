@@ -8,33 +8,65 @@
 // joins them row by row.
 //
 // The tiles and operands are those of attn_kernel.h.  Here a wavefront holds RT tiles of sixteen rows: one
-// 32-token tile of the cache is read, and dequantised, once for 16 RT rows, and RT independent chains of
-// matrix instructions and exponentials fill each other's waits.  The four (or eight) wavefronts of a
+// 32-token tile of the cache is read, and dequantised, once for 16 RT rows.  The wavefronts of a
 // workgroup take the tiles of its share in turn and join through LDS at its end.
+//
+// (RT = 4 on one wavefront a SIMD: 32 users under 32,768 NVFP4 tokens 85 us against 66 with two of RT = 2, since then nothing
+// runs while a wavefront waits.  Eight wavefronts that bring a tile's operands into LDS for 128 rows: long prefixes
+// of 1000 bf16 rows run at 1.06 PFLOP/s of matrix instructions against 0.74, but the larger blocks' partial sums and the joins
+// cost 10 us more: 77 us against 79 for 8192 tokens, 67 against 51 for the 32 users.)
+#include <algorithm>
+
 #include "attn_kernel.h"
 
 namespace nvfp4 {
 namespace {
 
 // The shared prefix's partial sums.  Its units are (kv head, block of rows), a kv head's rows those of
-// all sequences, (sequence, query head of the group) in order.  The line of all units' tiles is
-// cut evenly over `grid` workgroups, fewer where there is little to do; the piece of unit u that workgroup w
-// leaves has the number u + w (along the line, each piece has one more workgroup or one more unit behind it).
+// all sequences, (sequence, query head of the group) in order.  Each unit's tiles are cut evenly over `each` workgroups
+// if that occupies nearly all CUs; else the line of all units' tiles is cut evenly over `grid` workgroups, of which some
+// then hold the end of one unit and the beginning of another.  Less is cut where there is little to do.
+// (Units of their own: 32 users of 40 heads under 32,768 NVFP4 tokens, 40 units, 58 us against 64.)
 struct Prefix {
   const int32_t* len;
   const int32_t* table;
   float* part;         // [piece][block_rows][DP + 4]: reference, sum, two unused, the padded head's sums
   int32_t most;        // tokens that the table holds
-  int32_t units, row_blocks, block_rows, grid;
+  int32_t units, row_blocks, block_rows, grid, each;
+  int32_t share;       // tiles of a workgroup's share, at least: one a wavefront
 };
-constexpr int kPrefixShare = 4;   // tiles of a workgroup's share, at least: one a wavefront
 __device__ __forceinline__ int prefix_len(const Prefix& p) {
   const int len = *p.len;
   return len < 0 ? 0 : len > p.most ? p.most : len;
 }
+// Workgroup w's share [begin, end) of the line, and the number of its first piece; that of the piece after
+// a unit's end is one more.
+struct Share {
+  int begin, end, piece;
+};
 __device__ __forceinline__ Cut prefix_cut(const Prefix& p, int tiles) {
+  if (p.each > 0) return cut_of(tiles, min(p.each, (tiles + p.share - 1) / p.share));
   const int line = p.units * tiles;
-  return cut_of(line, min(p.grid, (line + kPrefixShare - 1) / kPrefixShare));
+  return cut_of(line, min(p.grid, (line + p.share - 1) / p.share));
+}
+__device__ __forceinline__ int prefix_workgroups(const Prefix& p, const Cut& c) { return p.each > 0 ? p.units * c.n : c.n; }
+__device__ __forceinline__ Share prefix_share(const Prefix& p, const Cut& c, int tiles, int w) {
+  if (p.each > 0) {
+    const int unit = (int)((unsigned)w / (unsigned)c.n), i = w - unit * c.n;
+    return Share{unit * tiles + run_start(c, i), unit * tiles + run_start(c, i + 1), w};
+  }
+  // (Along the line each piece has one more workgroup or one more unit behind it.)
+  const int begin = run_start(c, w);
+  return Share{begin, run_start(c, w + 1), (int)((unsigned)begin / (unsigned)tiles) + w};
+}
+// A unit's pieces.
+struct Pieces {
+  int first, n;
+};
+__device__ __forceinline__ Pieces prefix_pieces(const Prefix& p, const Cut& c, int tiles, int unit) {
+  if (p.each > 0) return Pieces{unit * c.n, c.n};
+  const int w0 = run_of(c, unit * tiles);
+  return Pieces{unit + w0, run_of(c, unit * tiles + tiles - 1) + 1 - w0};
 }
 
 struct PrefixParams {
@@ -48,13 +80,36 @@ struct PrefixParams {
   int score_exp;
 };
 
-// Row tiles of a wavefront: as many as the rows fill, and registers hold.
-constexpr int max_row_tiles(int db) { return 2; }
+// Values d0 .. d0 + E - 1 of the queries of a kv head's row; rows and values that are not there: zeros, from
+// addresses inside.
+template <int E>
+__device__ __forceinline__ void load_queries(const PrefixParams& a, int head, int row, int d0, uint32_t (&qv)[E / 2]) {
+  const int d_here = a.cache.head_dim - d0;
+  const bool in = row < a.rows && d_here > 0;
+  const int b = in ? row / a.group : 0, qh = head * a.group + (in ? row - b * a.group : 0);
+  const uint16_t* qp = a.q + (int64_t)b * a.ldq + qh * a.cache.head_dim + (in ? d0 : 0);
+  const int last = in ? d_here - 8 : 0;
+#pragma unroll
+  for (int i = 0; i < E / 8; ++i) {
+    const u32x4 x = load16(qp + min(8 * i, last));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) qv[4 * i + j] = in && 8 * i <= last ? x[j] : 0u;
+  }
+}
+
 constexpr int prefix_waves(int fmt, int db, int rt) { return rt == 1 ? waves_per_simd(fmt, db) : db <= 2 ? 2 : 1; }
+
+// Neighbouring shares on one XCD, whose L2 then serves a kv head's other blocks of rows.
+__device__ __forceinline__ int xcd_order(int wg, int n) {
+  const int xcd = wg & 7;
+  return xcd * (n >> 3) + min(xcd, n & 7) + (wg >> 3);
+}
 
 template <int FMT, int DB, int RT>
 __global__ __launch_bounds__(256 * prefix_waves(FMT, DB, RT), (prefix_waves(FMT, DB, RT))) void prefix_kernel(const PrefixParams a) {
   using L = KvLayout<FMT, DB>;
+  // Two row tiles: other blocks of rows read the same.  (200 users under 8192 bf16 tokens 80 us against 91.)
+  constexpr int kPolicy = RT == 1 ? kStreamed : kCached;
   constexpr int kWaves = 4 * prefix_waves(FMT, DB, RT), kThreads = 64 * kWaves, kBlock = kRows * RT;
   constexpr int kDp = 64 * DB, kE = L::kE, kW = L::kW, kSteps = kE / 8, kQuads = kE / 4;
   struct Sums {
@@ -66,35 +121,22 @@ __global__ __launch_bounds__(256 * prefix_waves(FMT, DB, RT), (prefix_waves(FMT,
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int qn = lane & 15, h = lane >> 4, d0 = kE * h;
   const int len = prefix_len(a.prefix), tiles = (len + kTile - 1) / kTile;
+  if (tiles == 0) return;
   const Cut shares = prefix_cut(a.prefix, tiles);
-  if ((int)blockIdx.x >= shares.n) return;
-  // Neighbouring shares on one XCD, whose L2 then serves a kv head's other blocks of rows.
-  const int xcd = blockIdx.x & 7, each = shares.n >> 3, more = shares.n & 7;
-  const int w = xcd * each + min(xcd, more) + (int)(blockIdx.x >> 3);
-  const int s1 = run_start(shares, w + 1);
+  const int workgroups = prefix_workgroups(a.prefix, shares);
+  if ((int)blockIdx.x >= workgroups) return;
+  Share share = prefix_share(a.prefix, shares, tiles, xcd_order(blockIdx.x, workgroups));
 
-  for (int s = run_start(shares, w); s < s1;) {
-    const int unit = (int)((unsigned)s / (unsigned)tiles), t0 = s - unit * tiles, t1 = min(tiles, t0 + s1 - s);
+  for (int s = share.begin; s < share.end; ++share.piece) {
+    const int unit = (int)((unsigned)s / (unsigned)tiles), t0 = s - unit * tiles, t1 = min(tiles, t0 + share.end - s);
     const int head = unit / a.prefix.row_blocks, row0 = (unit - head * a.prefix.row_blocks) * kBlock;
     const int count = max((t1 - t0 - wave + kWaves - 1) / kWaves, 0);
 
-    // Queries: lane (q, h) holds values E h .. E h + E - 1 of its row of each tile; rows and values that are not
-    // there: zeros, from addresses inside.
     uint32_t qv[RT][kE / 2];
     float score_scale[RT];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-      const int row = row0 + kRows * rt + qn, d_here = a.cache.head_dim - d0;
-      const bool in = row < a.rows && d_here > 0;
-      const int b = in ? row / a.group : 0, qh = head * a.group + (in ? row - b * a.group : 0);
-      const uint16_t* qp = a.q + (int64_t)b * a.ldq + qh * a.cache.head_dim + (in ? d0 : 0);
-      const int last = in ? d_here - 8 : 0;
-#pragma unroll
-      for (int i = 0; i < kE / 8; ++i) {
-        const u32x4 x = load16(qp + min(8 * i, last));
-#pragma unroll
-        for (int j = 0; j < 4; ++j) qv[rt][4 * i + j] = in && 8 * i <= last ? x[j] : 0u;
-      }
+      load_queries<kE>(a, head, row0 + kRows * rt + qn, d0, qv[rt]);
       score_scale[rt] = query_scale<FMT>(qv[rt], a.score_factor, a.score_exp);
     }
 
@@ -133,9 +175,9 @@ __global__ __launch_bounds__(256 * prefix_waves(FMT, DB, RT), (prefix_waves(FMT,
     int group[2];
     look_up(0, group);
     to_load(group);
-    load_k<FMT, DB>(from, lane, t);
+    load_k<FMT, DB, kPolicy>(from, lane, t);
     __builtin_amdgcn_sched_barrier(0);
-    load_v<FMT, DB>(from, lane, t);
+    load_v<FMT, DB, kPolicy>(from, lane, t);
     __builtin_amdgcn_sched_barrier(0);
 
     for (int it = 0; it < count; ++it) {
@@ -173,7 +215,7 @@ __global__ __launch_bounds__(256 * prefix_waves(FMT, DB, RT), (prefix_waves(FMT,
 #pragma unroll
           for (int i = 0; i < 4; ++i) x[rt][4 * half + i] = rounded_product(acc[rt][i], score_scale[rt]);
       }
-      load_k<FMT, DB>(from, lane, t);
+      load_k<FMT, DB, kPolicy>(from, lane, t);
 
       if (!whole) {
 #pragma unroll
@@ -223,7 +265,7 @@ __global__ __launch_bounds__(256 * prefix_waves(FMT, DB, RT), (prefix_waves(FMT,
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           op[j][i] = __builtin_amdgcn_perm(vt[2 * i + 1][j / 2], vt[2 * i][j / 2], j % 2 ? 0x07060302u : 0x05040100u);
-      load_v<FMT, DB>(from, lane, t);
+      load_v<FMT, DB, kPolicy>(from, lane, t);
 #pragma unroll
       for (int j = 0; j < kW; ++j)
 #pragma unroll
@@ -251,7 +293,7 @@ __global__ __launch_bounds__(256 * prefix_waves(FMT, DB, RT), (prefix_waves(FMT,
       }
     }
     __syncthreads();
-    float* piece = a.prefix.part + (int64_t)(unit + w) * kBlock * (kDp + 4);
+    float* piece = a.prefix.part + (int64_t)share.piece * kBlock * (kDp + 4);
     const int rows = min(a.rows - row0, kBlock);
     for (int e = tid; e < rows * (kDp / 4); e += kThreads) {
       const int r = e / (kDp / 4), d = 4 * (e - r * (kDp / 4));
@@ -303,9 +345,10 @@ __global__ __launch_bounds__(256) void join_kernel(const JoinParams a) {
     const int head = qh / a.group, r = b * a.group + qh - head * a.group;
     const int block = r / a.prefix.block_rows, unit = head * a.prefix.row_blocks + block;
     const Cut c = prefix_cut(a.prefix, tiles);
-    const int w0 = run_of(c, unit * tiles), n = run_of(c, unit * tiles + tiles - 1) + 1 - w0;
+    const Pieces all = prefix_pieces(a.prefix, c, tiles, unit);
+    const int n = all.n;
     const int i1 = n * (run + 1) / kRuns;
-    const float* from = a.prefix.part + ((int64_t)(unit + w0) * a.prefix.block_rows + (r - block * a.prefix.block_rows)) * (DP + 4);
+    const float* from = a.prefix.part + ((int64_t)all.first * a.prefix.block_rows + (r - block * a.prefix.block_rows)) * (DP + 4);
     const int64_t stride = (int64_t)a.prefix.block_rows * (DP + 4);
     for (int i = n * run / kRuns; i < i1; i += kPieces) {
       f32x4 ml[kPieces], v[kPieces];
@@ -360,10 +403,9 @@ int head_rows_of(const AttnSharedLaunch& a) { return (int)(a.attn.batch * (a.att
 
 int padded_of(const AttnSharedLaunch& a) { return (a.attn.cache.head_dim + 63) / 64; }
 
-int block_tiles_of(const AttnSharedLaunch& a) {
-  const int tiles = (head_rows_of(a) + kRows - 1) / kRows, most = max_row_tiles(padded_of(a));
-  return tiles == 1 ? 1 : tiles == 2 || most == 2 ? 2 : 4;
-}
+
+// Row tiles of a workgroup: one if that takes all rows, else two.
+int block_tiles_of(const AttnSharedLaunch& a) { return head_rows_of(a) <= kRows ? 1 : 2; }
 
 int64_t prefix_units_of(const AttnSharedLaunch& a) {
   const int block = kRows * block_tiles_of(a);
@@ -372,9 +414,23 @@ int64_t prefix_units_of(const AttnSharedLaunch& a) {
 
 int64_t prefix_tiles_of(const AttnSharedLaunch& a) { return (a.prefix_width * a.attn.cache.page_size + kTile - 1) / kTile; }
 
+int prefix_share_of(const AttnSharedLaunch& a) {
+  return 4 * prefix_waves(a.attn.format, padded_of(a), block_tiles_of(a));
+}
+
+// Workgroups a unit (0: the line is cut), see Prefix.
+int prefix_each_of(const AttnSharedLaunch& a) {
+  const int64_t units = prefix_units_of(a), each = units <= kCus ? kCus / units : 0;
+  return 8 * each * units >= 7 * kCus ? (int)each : 0;
+}
+
+// Workgroups of the launch: as many as the longest prefix has work for.
 int prefix_grid_of(const AttnSharedLaunch& a) {
-  const int64_t shares = (prefix_units_of(a) * prefix_tiles_of(a) + kPrefixShare - 1) / kPrefixShare;
-  return (int)(shares < kCus ? shares : kCus);
+  const int64_t units = prefix_units_of(a), tiles = prefix_tiles_of(a), each = prefix_each_of(a);
+  const int64_t share = prefix_share_of(a);
+  const auto shares = [&](int64_t n) { return (n + share - 1) / share; };
+  const int64_t n = each > 0 ? units * std::min(each, shares(tiles)) : shares(units * tiles);
+  return (int)std::min<int64_t>(n, kCus);
 }
 
 size_t rounded(size_t bytes) { return (bytes + 255) & ~(size_t)255; }
@@ -388,13 +444,8 @@ size_t pieces_at(const AttnSharedLaunch& a) { return raw_at(a) + rounded((size_t
 template <int FMT, int DB>
 void prefix_launch(const AttnSharedLaunch& a, const PrefixParams& p, hipStream_t s) {
   const dim3 grid((unsigned)p.prefix.grid);
-  switch (p.prefix.block_rows / kRows) {
-    case 1: hipLaunchKernelGGL((prefix_kernel<FMT, DB, 1>), grid, dim3(256 * prefix_waves(FMT, DB, 1)), 0, s, p); break;
-    case 2: hipLaunchKernelGGL((prefix_kernel<FMT, DB, 2>), grid, dim3(256 * prefix_waves(FMT, DB, 2)), 0, s, p); break;
-    default:
-      if constexpr (max_row_tiles(DB) == 4)
-        hipLaunchKernelGGL((prefix_kernel<FMT, DB, 4>), grid, dim3(256 * prefix_waves(FMT, DB, 4)), 0, s, p);
-  }
+  if (p.prefix.block_rows == kRows) hipLaunchKernelGGL((prefix_kernel<FMT, DB, 1>), grid, dim3(256 * prefix_waves(FMT, DB, 1)), 0, s, p);
+  else hipLaunchKernelGGL((prefix_kernel<FMT, DB, 2>), grid, dim3(256 * prefix_waves(FMT, DB, 2)), 0, s, p);
 }
 
 template <int FMT>
@@ -436,6 +487,8 @@ hipError_t launch_attn_shared(const AttnSharedLaunch& a, hipStream_t s) {
   p.prefix.row_blocks = p.prefix.units / a.attn.cache.heads;
   p.prefix.block_rows = kRows * block_tiles_of(a);
   p.prefix.grid = prefix_grid_of(a);
+  p.prefix.each = prefix_each_of(a);
+  p.prefix.share = prefix_share_of(a);
   switch (a.attn.format) {
     case kKvBf16: prefix_launch_db<kKvBf16>(a, p, s); break;
     case kKvE4m3: prefix_launch_db<kKvE4m3>(a, p, s); break;
