@@ -11,11 +11,12 @@
 //
 // Selection.  A workgroup finds the K-th largest key eight bits at a time: a histogram of the next eight
 // bits of the keys that still agree with it, from the first bit in which any two differ; it stops as soon as the
-// keys that agree are all taken or all of one kind.
+// keys that agree are all taken or all of one kind.  Each thread holds a run of consecutive keys in registers; more
+// keys than that stay in memory and are read in each step.
 #include <algorithm>
+#include <type_traits>
 
-#include "attn_launchers.h"
-#include "device_common.h"
+#include "attn_kernel.h"
 
 namespace nvfp4 {
 namespace {
@@ -28,41 +29,55 @@ __device__ __forceinline__ u64 key_of(double v) {
   return u >> 63 ? ~u : u | 1ull << 63;
 }
 
-// Keys of one sequence (and kv head), in LDS where they fit, in memory beyond (written through to it and read from
-// it: other workgroups may have written them).
-constexpr int kKeysInLds = 4096;
-struct Keys {
-  u64* lds;            // nullptr: in memory
-  u64* memory;
-};
+// Keys in memory are written through to it and read from it: other workgroups may have written them.
 __device__ __forceinline__ u64 load_key(const u64* p) {
   return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 __device__ __forceinline__ void store_key(u64* p, u64 k) {
   __hip_atomic_store(p, k, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
-__device__ __forceinline__ u64 get_key(const Keys& k, int i) { return k.lds ? k.lds[i] : load_key(k.memory + i); }
+
+// A thread's share of n keys: those from `begin` to `end`, in registers if PER takes them (each(): (place, key) of
+// its keys in order).
+template <int THREADS, int PER>
+struct Keys {
+  u64 k[PER];
+  const u64* memory;   // where the keys are if they are not in registers
+  int begin, end;
+  __device__ __forceinline__ void share(int n) {
+    const int per = (n + THREADS - 1) / THREADS;
+    begin = min((int)threadIdx.x * per, n);
+    end = min(begin + per, n);
+  }
+  __device__ __forceinline__ bool held(int n) const { return n <= THREADS * PER; }
+  template <class F>
+  __device__ __forceinline__ void each(int n, F f) const {
+    if (held(n)) {
+#pragma unroll
+      for (int j = 0; j < PER; ++j)
+        if (begin + j < end) f(begin + j, k[j]);
+    } else {
+      for (int i = begin; i < end; ++i) f(i, load_key(memory + i));
+    }
+  }
+};
+
+constexpr int kDigit = 8, kBins = 1 << kDigit;
 
 template <int THREADS>
 struct SelectLds {
-  int hist[256];
+  int hist[2][kBins];
   int wave_sum[THREADS / 64];
-  u64 all_and[THREADS / 64], all_or[THREADS / 64];
+  uint32_t bits[THREADS / 64][4];
   int digit, above;
 };
 
 // Exclusive sum of v over the workgroup's threads, in order; total: that of all.
 template <int THREADS>
 __device__ __forceinline__ int block_scan(int v, int* wave_sum, int& total) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int upto = v;
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const int other = __shfl_up(upto, off);
-    upto += lane >= off ? other : 0;
-  }
+  const int wave = threadIdx.x >> 6, upto = lane_scan(v);
   __syncthreads();
-  if (lane == 63) wave_sum[wave] = upto;
+  if ((threadIdx.x & 63) == 63) wave_sum[wave] = upto;
   __syncthreads();
   int before = 0;
   total = 0;
@@ -75,6 +90,21 @@ __device__ __forceinline__ int block_scan(int v, int* wave_sum, int& total) {
   return before + upto - v;
 }
 
+template <bool AND, int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t join_bits(uint32_t v) {
+  const uint32_t other = (uint32_t)__builtin_amdgcn_update_dpp(AND ? -1 : 0, (int)v, CTRL, ROWS, 0xf, false);
+  return AND ? v & other : v | other;
+}
+template <bool AND>
+__device__ __forceinline__ uint32_t lanes_bits(uint32_t v) {  // of all lanes, in the last
+  v = join_bits<AND, 0x111, 0xf>(v);
+  v = join_bits<AND, 0x112, 0xf>(v);
+  v = join_bits<AND, 0x114, 0xf>(v);
+  v = join_bits<AND, 0x118, 0xf>(v);
+  v = join_bits<AND, 0x142, 0xa>(v);
+  return join_bits<AND, 0x143, 0xc>(v);
+}
+
 // Of n keys those to take, in the bits of `mask`: all above `over`, and the first `ties` of those equal to it.
 struct Chosen {
   u64 over, mask;
@@ -82,34 +112,30 @@ struct Chosen {
   bool all;            // those equal are no more than `ties`
 };
 
-// The `want` largest of n keys, 0 < want <= the number of keys that are not 0 (those that are 0 are never
-// among them).  Called by all threads, after the keys are visible to all.
-template <int THREADS>
-__device__ Chosen choose(const Keys& keys, int n, int want, SelectLds<THREADS>& s) {
+// The `want` largest of n keys, 0 < want < the number of keys that are not 0 (those that are 0 are never
+// among them).  Called by all threads.
+template <int THREADS, int PER>
+__device__ Chosen choose(const Keys<THREADS, PER>& keys, int n, int want, SelectLds<THREADS>& s) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   u64 both = ~0ull, any = 0;
-  for (int i = tid; i < n; i += THREADS) {
-    const u64 k = get_key(keys, i);
-    if (k != 0) {
-      both &= k;
-      any |= k;
-    }
-  }
+  keys.each(n, [&](int, u64 k) {
+    both &= k != 0 ? k : ~0ull;
+    any |= k;
+  });
+  const uint32_t bits[4] = {lanes_bits<true>((uint32_t)both), lanes_bits<true>((uint32_t)(both >> 32)),
+                            lanes_bits<false>((uint32_t)any), lanes_bits<false>((uint32_t)(any >> 32))};
+  __syncthreads();
+  if (lane == 63) {
 #pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) {
-    both &= __shfl_xor(both, off);
-    any |= __shfl_xor(any, off);
+    for (int i = 0; i < 4; ++i) s.bits[wave][i] = bits[i];
   }
+  for (int i = tid; i < kBins; i += THREADS) s.hist[0][i] = 0;
   __syncthreads();
-  if (lane == 0) {
-    s.all_and[wave] = both;
-    s.all_or[wave] = any;
-  }
-  __syncthreads();
+  both = ~0ull, any = 0;
 #pragma unroll
   for (int i = 0; i < THREADS / 64; ++i) {
-    both &= s.all_and[i];
-    any |= s.all_or[i];
+    both &= (u64)s.bits[i][1] << 32 | s.bits[i][0];
+    any |= (u64)s.bits[i][3] << 32 | s.bits[i][2];
   }
   // Bits above `top` are the same in all keys.
   int top = both == any ? 0 : 64 - __builtin_clzll(both ^ any);
@@ -118,42 +144,35 @@ __device__ Chosen choose(const Keys& keys, int n, int want, SelectLds<THREADS>& 
   c.over = any & c.mask;
   c.ties = want;
   c.all = false;
-  while (top > 0) {
-    const int bits = top < 8 ? top : 8, shift = top - bits;
-    __syncthreads();
-    for (int i = tid; i < 256; i += THREADS) s.hist[i] = 0;
-    __syncthreads();
-    for (int i = tid; i < n; i += THREADS) {
-      const u64 k = get_key(keys, i);
-      if (k != 0 && (k & c.mask) == c.over) atomicAdd(&s.hist[(int)(k >> shift) & ((1 << bits) - 1)], 1);
-    }
+  for (int step = 0; top > 0; step ^= 1) {
+    const int bits = top < kDigit ? top : kDigit, shift = top - bits;
+    int* hist = s.hist[step];
+    keys.each(n, [&](int, u64 k) {
+      if (k != 0 && (k & c.mask) == c.over) atomicAdd(&hist[(int)(k >> shift) & ((1 << bits) - 1)], 1);
+    });
     __syncthreads();
     // The digit that holds the ties-th largest: one wavefront, four digits a lane, from the largest down.
     if (wave == 0) {
-      int h[4], mine = 0;
+      constexpr int kMine = kBins / 64;
+      int h[kMine], mine = 0;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        h[j] = s.hist[255 - 4 * lane - j];
+      for (int j = 0; j < kMine; ++j) {
+        h[j] = hist[kBins - 1 - kMine * lane - j];
         mine += h[j];
       }
-      int upto = mine;
+      int above = lane_scan(mine) - mine;
 #pragma unroll
-      for (int off = 1; off < 64; off <<= 1) {
-        const int other = __shfl_up(upto, off);
-        upto += lane >= off ? other : 0;
-      }
-      int above = upto - mine;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < kMine; ++j) {
         if (above < c.ties && above + h[j] >= c.ties) {
-          s.digit = 255 - 4 * lane - j;
+          s.digit = kBins - 1 - kMine * lane - j;
           s.above = above;
         }
         above += h[j];
       }
     }
+    for (int i = tid; i < kBins; i += THREADS) s.hist[step ^ 1][i] = 0;
     __syncthreads();
-    const int digit = s.digit, left = s.hist[digit];
+    const int digit = s.digit, left = hist[digit];
     c.over |= (u64)digit << shift;
     c.mask |= ((1ull << bits) - 1) << shift;
     c.ties -= s.above;
@@ -161,30 +180,30 @@ __device__ Chosen choose(const Keys& keys, int n, int want, SelectLds<THREADS>& 
     c.all = left == c.ties;         // all that agree are taken
     if (c.all) break;
   }
-  __syncthreads();
   return c;
 }
 
-// Calls emit(i, place) for each i < n that `taken(i)` says, place counting them in order, over all threads; the count.
-template <int THREADS, class TAKEN, class EMIT>
-__device__ __forceinline__ int compact(int n, int* wave_sum, TAKEN taken, EMIT emit) {
-  const int per = (n + THREADS - 1) / THREADS, i0 = min((int)threadIdx.x * per, n), i1 = min(i0 + per, n);
-  int mine = 0;
-  for (int i = i0; i < i1; ++i) mine += taken(i) ? 1 : 0;
-  int total, place = block_scan<THREADS>(mine, wave_sum, total);
-  for (int i = i0; i < i1; ++i)
-    if (taken(i)) emit(i, place++);
+// Calls emit(place, rank) for each of the thread's keys that `taken(place, key)` says, rank counting them in order over all
+// threads; the count.
+template <int THREADS, int PER, class TAKEN, class EMIT>
+__device__ __forceinline__ int compact(const Keys<THREADS, PER>& keys, int n, int* wave_sum, TAKEN taken, EMIT emit) {
+  int mine = 0, total;
+  keys.each(n, [&](int i, u64 k) { mine += taken(i, k) ? 1 : 0; });
+  int rank = block_scan<THREADS>(mine, wave_sum, total);
+  keys.each(n, [&](int i, u64 k) {
+    if (taken(i, k)) emit(i, rank++);
+  });
   return total;
 }
 
 // Ties beyond those that are taken: the place where the first one left out lies (n: none is).
-template <int THREADS>
-__device__ __forceinline__ int ties_end(const Keys& keys, int n, const Chosen& c, int* wave_sum, int* out) {
+template <int THREADS, int PER>
+__device__ __forceinline__ int ties_end(const Keys<THREADS, PER>& keys, int n, const Chosen& c, int* wave_sum, int* out) {
   if (c.all) return n;
   if (threadIdx.x == 0) *out = n;
   __syncthreads();
-  compact<THREADS>(n, wave_sum, [&](int i) { const u64 k = get_key(keys, i); return k != 0 && (k & c.mask) == c.over; },
-                   [&](int i, int place) { if (place == c.ties) *out = i; });
+  compact(keys, n, wave_sum, [&](int, u64 k) { return k != 0 && (k & c.mask) == c.over; },
+          [&](int i, int rank) { if (rank == c.ties) *out = i; });
   __syncthreads();
   return *out;
 }
@@ -200,41 +219,66 @@ constexpr int kThreads = 256;
 constexpr int kStage = 16;             // query rows in LDS at a time
 constexpr int kCounters = 1024;        // (sequence, kv head)s whose scores may be cut over several workgroups
 
+constexpr int kSelectFew = 4, kSelectMany = 16;  // keys a thread holds: of tables of up to 1024 and 4096 pages
+
 struct SelectParams {
   KvSelectLaunch a;
   unsigned* counters;
   u64* keys;                           // [batch][heads][table_width]
   int chunk, shares;                   // pages of a workgroup's share; shares of a table
-  bool cut;                            // over several workgroups
 };
 
-template <int DB>
+// Sum over sixteen lanes, the same in each.
+template <int CTRL>
+__device__ __forceinline__ double add_partner(double v) {
+  const u64 u = (u64)__double_as_longlong(v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, 0xf, 0xf, true);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, 0xf, 0xf, true);
+  return v + __longlong_as_double((long long)((u64)hi << 32 | lo));
+}
+__device__ __forceinline__ double sum16(double v) {
+  v = add_partner<0xb1>(v);   // the neighbour, the other pair, the other four mirrored, the other eight mirrored
+  v = add_partner<0x4e>(v);
+  v = add_partner<0x141>(v);
+  return add_partner<0x140>(v);
+}
+
+// CUT: a table's pages are scored by several workgroups, the last of which to arrive selects.
+template <int DB, bool CUT, int PER>
 __global__ __launch_bounds__(kThreads) void select_kernel(const SelectParams p) {
   constexpr int kUnits = 2 * DB;       // pairs of channels that a lane holds of a page's bounds
+  constexpr int kAhead = DB <= 2 ? 4 : 2;  // pages of a sixteen of lanes whose bounds are read at once
   const KvSelectLaunch& a = p.a;
   __shared__ double s_q[kStage][kUnits][16][2];
-  __shared__ u64 s_keys[kKeysInLds];
+  __shared__ union {
+    u64 keys[CUT ? 1 : kThreads * PER];
+    int list[kThreads * PER];
+  } s;
+  u64* const s_keys = s.keys;
   __shared__ SelectLds<kThreads> s_sel;
   __shared__ int s_end;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, j = lane & 15;
-  const unsigned wg = blockIdx.x / (unsigned)p.shares;
-  const int b = (int)(wg / (unsigned)a.heads), head = (int)(wg - (unsigned)b * (unsigned)a.heads);
-  const int64_t pair = wg;
+  const int tid = threadIdx.x, j = tid & 15;
+  // (A table's shares apart in the launch, so that those of a long one are on CUs of their own: 32 ragged users 30 us against 33.)
+  const unsigned pairs = gridDim.x / (unsigned)p.shares, share = blockIdx.x / pairs, pair = blockIdx.x - share * pairs;
+  const int b = (int)(pair / (unsigned)a.heads), head = (int)(pair - (unsigned)b * (unsigned)a.heads);
 
   const int64_t most = a.table_width * a.page_size;
   const int64_t len = min((int64_t)max(a.lens[b], 0), most);
   const int n = (int)((len + a.page_size - 1) / a.page_size), budget = (int)a.budget;
-  const int first = (int)(blockIdx.x - wg * (unsigned)p.shares) * p.chunk;
-  const bool scored = n > budget;       // there is a choice
+  const int first = (int)share * p.chunk;
+  const bool scored = n > budget && budget > 1;  // there is a choice
   if (first > 0 && (!scored || first >= n - 1)) return;
   const int32_t* table = a.table + (int64_t)b * a.table_width;
-  const auto there = [&](int i) { const int page = table[i]; return page >= 0 && page < a.pages; };
-  Keys keys;
-  keys.lds = !p.cut && n <= kKeysInLds ? s_keys : nullptr;
-  keys.memory = p.keys + pair * a.table_width;
+  const auto there = [&](int page) { return page >= 0 && page < a.pages; };
+  Keys<kThreads, PER> keys;
+  keys.memory = p.keys + (int64_t)pair * a.table_width;
+  const int others = max(n - 1, 0);     // the last page is always taken
+  keys.share(others);
+  const bool in_lds = !CUT && keys.held(others);
 
   if (scored) {
-    const int end = min(first + p.chunk, n - 1);    // the last page is always taken
+    const int end = min(first + p.chunk, others);
+    u64* memory = p.keys + (int64_t)pair * a.table_width;
     for (int g0 = 0; g0 < a.group; g0 += kStage) {
       const int rows = min(a.group - g0, kStage);
       __syncthreads();
@@ -245,101 +289,148 @@ __global__ __launch_bounds__(kThreads) void select_kernel(const SelectParams p) 
         (&s_q[r][0][0][0])[x] = (double)bf16_lo(v);
       }
       __syncthreads();
-      for (int i0 = first + 4 * wave; i0 < end; i0 += 4 * (kThreads / 64)) {
-        const int i = i0 + (lane >> 4);
-        const bool live = i < end && there(min(i, end - 1));
-        const int page = live ? table[i] : 0;
-        const uint16_t* lo = a.bounds + ((int64_t)page * a.heads + head) * 2 * a.head_dim;
-        double low[2 * kUnits], high[2 * kUnits];
+      // Each sixteen lanes take a page: kAhead of them in flight.
+      constexpr int kAtOnce = kThreads / 16;
+      for (int i0 = first + (tid >> 4); i0 < end; i0 += kAhead * kAtOnce) {
+        int page[kAhead];
 #pragma unroll
-        for (int u = 0; u < DB; ++u) {
-          const int d = 4 * DB * j + 4 * u;
-          uint2 l = make_uint2(0, 0), h = l;
-          if (live && d < a.head_dim) {
-            l = *reinterpret_cast<const uint2*>(lo + d);
-            h = *reinterpret_cast<const uint2*>(lo + a.head_dim + d);
-          }
-          low[4 * u] = bf16_lo(l.x), low[4 * u + 1] = bf16_hi(l.x), low[4 * u + 2] = bf16_lo(l.y), low[4 * u + 3] = bf16_hi(l.y);
-          high[4 * u] = bf16_lo(h.x), high[4 * u + 1] = bf16_hi(h.x), high[4 * u + 2] = bf16_lo(h.y), high[4 * u + 3] = bf16_hi(h.y);
+        for (int k = 0; k < kAhead; ++k) {
+          const int i = i0 + k * kAtOnce;
+          page[k] = i < end ? table[i] : -1;
         }
-        u64 best = 0;
-        for (int r = 0; r < rows; ++r) {
-          double sum = 0.0;
+        uint2 l[kAhead][DB], h[kAhead][DB];
 #pragma unroll
-          for (int u = 0; u < kUnits; ++u) {
-            const double q0 = s_q[r][u][j][0], q1 = s_q[r][u][j][1];
-            sum += q0 * (q0 < 0.0 ? low[2 * u] : high[2 * u]);
-            sum += q1 * (q1 < 0.0 ? low[2 * u + 1] : high[2 * u + 1]);
+        for (int k = 0; k < kAhead; ++k) {
+          const uint16_t* lo = a.bounds + ((int64_t)(there(page[k]) ? page[k] : 0) * a.heads + head) * 2 * a.head_dim;
+#pragma unroll
+          for (int u = 0; u < DB; ++u) {
+            const int d = 4 * DB * j + 4 * u;
+            l[k][u] = h[k][u] = make_uint2(0, 0);
+            if (there(page[k]) && d < a.head_dim) {
+              l[k][u] = *reinterpret_cast<const uint2*>(lo + d);
+              h[k][u] = *reinterpret_cast<const uint2*>(lo + a.head_dim + d);
+            }
+          }
+        }
+        // Two pages at a time: their sums fill each other's waits.
+#pragma unroll
+        for (int k = 0; k < kAhead; k += 2) {
+          double low[2][2 * kUnits], high[2][2 * kUnits];
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int u = 0; u < DB; ++u) {
+              const uint2 lu = l[k + m][u], hu = h[k + m][u];
+              low[m][4 * u] = bf16_lo(lu.x), low[m][4 * u + 1] = bf16_hi(lu.x);
+              low[m][4 * u + 2] = bf16_lo(lu.y), low[m][4 * u + 3] = bf16_hi(lu.y);
+              high[m][4 * u] = bf16_lo(hu.x), high[m][4 * u + 1] = bf16_hi(hu.x);
+              high[m][4 * u + 2] = bf16_lo(hu.y), high[m][4 * u + 3] = bf16_hi(hu.y);
+            }
+          double best[2] = {-__builtin_inf(), -__builtin_inf()};
+          bool nan[2] = {false, false};
+          for (int r = 0; r < rows; ++r) {
+            double sum[2] = {0.0, 0.0};
+#pragma unroll
+            for (int u = 0; u < kUnits; ++u) {
+              const double q0 = s_q[r][u][j][0], q1 = s_q[r][u][j][1];
+#pragma unroll
+              for (int m = 0; m < 2; ++m) {
+                sum[m] += q0 * (q0 < 0.0 ? low[m][2 * u] : high[m][2 * u]);
+                sum[m] += q1 * (q1 < 0.0 ? low[m][2 * u + 1] : high[m][2 * u + 1]);
+              }
+            }
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+              const double score = sum16(sum[m]);
+              nan[m] |= score != score;
+              best[m] = fmax(best[m], score);
+            }
           }
 #pragma unroll
-          for (int off = 8; off >= 1; off >>= 1) sum += __shfl_xor(sum, off);
-          best = max(best, key_of(sum));
-        }
-        if (j == 0 && i < end) {
-          if (!live) best = 0;
-          u64* to = keys.lds ? keys.lds + i : keys.memory + i;
-          if (keys.lds) *to = g0 > 0 ? max(*to, best) : best;
-          else store_key(to, g0 > 0 ? max(load_key(to), best) : best);
+          for (int m = 0; m < 2; ++m) {
+            const int i = i0 + (k + m) * kAtOnce;
+            if (j == 0 && i < end) {
+              const u64 key = !there(page[k + m]) ? 0 : nan[m] ? ~0ull : key_of(best[m]);
+              if (in_lds) s_keys[i] = g0 > 0 ? max(s_keys[i], key) : key;
+              else store_key(memory + i, g0 > 0 ? max(load_key(memory + i), key) : key);
+            }
+          }
         }
       }
     }
-    if (p.cut) {
-      const unsigned shares = (unsigned)((n - 1 + p.chunk - 1) / p.chunk);
-      if (shares > 1 && !arrive_last(p.counters + pair, shares)) return;
-      if (n <= kKeysInLds) {            // this workgroup reads them several times
-        if (shares == 1) {
-          __builtin_amdgcn_s_waitcnt(0);
-          __syncthreads();
-        }
-        for (int i = tid; i < n - 1; i += kThreads) s_keys[i] = load_key(keys.memory + i);
-        keys.lds = s_keys;
+    const unsigned shares = (unsigned)((others + p.chunk - 1) / p.chunk);
+    if (CUT && shares > 1) {
+      if (!arrive_last(p.counters + pair, shares)) return;
+    } else {
+      __builtin_amdgcn_s_waitcnt(0);    // keys in memory have arrived there
+      __syncthreads();
+    }
+    if (keys.held(others)) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int at = keys.begin + i;
+        keys.k[i] = at >= keys.end ? 0 : in_lds ? s_keys[at] : load_key(memory + at);
       }
     }
-    __builtin_amdgcn_s_waitcnt(0);      // keys in memory have arrived there
-    __syncthreads();
   }
 
   // The best `budget - 1` of the pages before the last that are there, and the last.
-  int32_t* out = a.pages_out + pair * a.budget;
+  int32_t* out = a.pages_out + (int64_t)pair * a.budget;
   int taken = 0;
-  if (n > 1 && budget > 1) {
-    const auto emit = [&](int i, int place) { out[place] = table[i]; };
-    int total = 0;
+  if (others > 0 && budget > 1) {
+    // (Places first, then all their pages at once: a table's entry is a trip to memory.)
+    const bool listed = keys.held(others);
+    const auto emit = [&](int i, int place) {
+      if (listed) s.list[place] = i;
+      else out[place] = table[i];
+    };
+    int mine = 0, total = 0;
     if (scored) {
-      int mine = 0;
-      for (int i = tid; i < n - 1; i += kThreads) mine += get_key(keys, i) != 0 ? 1 : 0;
+      keys.each(others, [&](int, u64 k) { mine += k != 0 ? 1 : 0; });
       block_scan<kThreads>(mine, s_sel.wave_sum, total);
     }
-    if (scored && total > budget - 1) {
-      const Chosen c = choose<kThreads>(keys, n - 1, budget - 1, s_sel);
-      const int end = ties_end<kThreads>(keys, n - 1, c, s_sel.wave_sum, &s_end);
-      taken = compact<kThreads>(n - 1, s_sel.wave_sum, [&](int i) { return is_chosen(get_key(keys, i), i, c, end); }, emit);
-    } else {
-      taken = compact<kThreads>(n - 1, s_sel.wave_sum, there, emit);
+    if (total > budget - 1) {
+      const Chosen c = choose(keys, others, budget - 1, s_sel);
+      const int end = ties_end(keys, others, c, s_sel.wave_sum, &s_end);
+      taken = compact(keys, others, s_sel.wave_sum, [&](int i, u64 k) { return is_chosen(k, i, c, end); }, emit);
+    } else {                            // all that are there
+      for (int i = keys.begin; i < keys.end; ++i) taken += there(table[i]) ? 1 : 0;
+      int place = block_scan<kThreads>(taken, s_sel.wave_sum, taken);
+      for (int i = keys.begin; i < keys.end; ++i)
+        if (there(table[i])) emit(i, place++);
     }
+    __syncthreads();
+    if (listed)
+      for (int i = tid; i < taken; i += kThreads) out[i] = table[s.list[i]];
   }
-  if (tid == 0) {
-    if (n > 0) out[taken++] = there(n - 1) ? table[n - 1] : -1;
-    s_end = taken;
-    if (head == 0) a.lens_out[b] = n > 0 ? (int)((taken - 1) * (int64_t)a.page_size + (len - 1) % a.page_size + 1) : 0;
-  }
-  __syncthreads();
-  for (int i = s_end + tid; i < budget; i += kThreads) out[i] = -1;
+  if (tid == 0 && n > 0) out[taken] = there(table[n - 1]) ? table[n - 1] : -1;
+  if (n > 0) ++taken;
+  if (tid == 0 && head == 0)
+    a.lens_out[b] = n > 0 ? (int)((taken - 1) * (int64_t)a.page_size + (len - 1) % a.page_size + 1) : 0;
+  for (int i = taken + tid; i < budget; i += kThreads) out[i] = -1;
 }
 
 // ---- eviction -------------------------------------------------------------------
 
-constexpr int kEvictThreads = 1024;
-
 struct EvictParams {
   KvEvictLaunch a;
-  u64* keys;                           // [batch][table_width], if they do not fit LDS
+  u64* keys;                           // [batch][table_width], if registers do not hold them
 };
 
-__global__ __launch_bounds__(kEvictThreads) void evict_kernel(const EvictParams p) {
+constexpr int kEvictPer = 8;
+constexpr int kEvictFew = 256, kEvictMany = 1024;  // threads
+constexpr int kHeadsAtOnce = 8, kPagesAtOnce = 4;  // loads in flight of a thread
+
+// One workgroup a sequence.
+template <int THREADS>
+__global__ __launch_bounds__(THREADS) void evict_kernel(const EvictParams p) {
   const KvEvictLaunch& a = p.a;
-  __shared__ u64 s_keys[kKeysInLds];
-  __shared__ SelectLds<kEvictThreads> s_sel;
+  __shared__ union {
+    u64 keys[THREADS * kEvictPer];
+    int list[THREADS * kEvictPer];      // places of the pages that stay, in order, and behind them of those dropped
+  } s;
+  __shared__ int s_table[THREADS * kEvictPer];
+  __shared__ SelectLds<THREADS> s_sel;
   __shared__ int s_end;
   const int tid = threadIdx.x, b = blockIdx.x;
   const int64_t most = a.table_width * a.page_size;
@@ -347,77 +438,143 @@ __global__ __launch_bounds__(kEvictThreads) void evict_kernel(const EvictParams 
   const int n = (int)((len + a.page_size - 1) / a.page_size), budget = (int)a.budget;
   const int32_t* table = a.table + (int64_t)b * a.table_width;
   const float* weights = a.weights + (int64_t)b * a.heads * a.table_width;
-  const auto there = [&](int i) { return table[i] >= 0 || i == n - 1; };
-  Keys keys;
-  keys.lds = n <= kKeysInLds ? s_keys : nullptr;
-  keys.memory = p.keys ? p.keys + (int64_t)b * a.table_width : nullptr;
+  u64* memory = p.keys ? p.keys + (int64_t)b * a.table_width : nullptr;
+  Keys<THREADS, kEvictPer> keys;
+  keys.memory = memory;
+  keys.share(n);
+  const bool held = keys.held(n);
 
-  // Pages from `late` on are the newest ones, kept whatever they weigh: those that are there, as far as the budget goes.
-  int late = a.recent < n ? n - (int)a.recent : 0, newest = 0, mine = 0;
-  for (int i = late + tid; i < n; i += kEvictThreads) mine += there(i) ? 1 : 0;
-  block_scan<kEvictThreads>(mine, s_sel.wave_sum, newest);
-  int skip = max(newest - budget, 0);   // of them, the oldest that the budget leaves out
-  newest -= skip;
-  // The others by weight, the first `sink` places above all weights.
-  int others = 0;
-  mine = 0;
-  for (int i = tid; i < late; i += kEvictThreads) {
-    u64 k = 0;
-    if (table[i] >= 0) {
-      double sum = 0.0;
-      for (int h = 0; h < a.heads; ++h) sum += (double)weights[(int64_t)h * a.table_width + i];
-      k = i < a.sink ? ~0ull : key_of(sum);
-      ++mine;
+  // Pages from `late` on are the newest ones, kept whatever they weigh: key 1 if they are there.  The others' keys are
+  // their weights', the first `sink` places above all.  Key 0: not there.
+  const int late = a.recent < n ? n - (int)a.recent : 0;
+  const auto weigh = [&](int base, auto at_once) {
+    constexpr int kPages = decltype(at_once)::value;
+    int page[kPages];
+    double sum[kPages];
+#pragma unroll
+    for (int m = 0; m < kPages; ++m) {
+      const int i = base + m * THREADS + tid;
+      page[m] = i < n ? table[i] : -1;
+      sum[m] = 0.0;
     }
-    if (keys.lds) keys.lds[i] = k;
-    else store_key(keys.memory + i, k);
-  }
-  if (!keys.lds) __builtin_amdgcn_s_waitcnt(0);
-  block_scan<kEvictThreads>(mine, s_sel.wave_sum, others);
-  const int want = min(budget - newest, others);
-  Chosen c{~0ull, ~0ull, 0, true};
-  int end = 0;
-  if (want > 0 && want < others) {
-    c = choose<kEvictThreads>(keys, late, want, s_sel);
-    end = ties_end<kEvictThreads>(keys, late, c, s_sel.wave_sum, &s_end);
-  }
-  // How many of the newest are left out is a matter of their order: those before place `from`.
-  int from = late;
-  if (skip > 0) {
-    __syncthreads();
-    if (tid == 0) s_end = n;
-    __syncthreads();
-    const int late0 = late;
-    compact<kEvictThreads>(n - late0, s_sel.wave_sum, [&](int i) { return there(late0 + i); },
-                           [&](int i, int place) { if (place == skip) s_end = late0 + i; });
-    __syncthreads();
-    from = s_end;
-    __syncthreads();
-  }
-  const auto kept = [&](int i) {
-    if (i >= late) return i >= from && there(i);
-    if (want <= 0) return false;
-    return want >= others ? table[i] >= 0 : is_chosen(get_key(keys, i), i, c, end);
+    for (int h0 = 0; h0 < a.heads; h0 += kHeadsAtOnce) {
+      float w[kPages][kHeadsAtOnce];
+#pragma unroll
+      for (int m = 0; m < kPages; ++m) {
+        const int i = base + m * THREADS + tid;
+#pragma unroll
+        for (int h = 0; h < kHeadsAtOnce; ++h)
+          w[m][h] = h0 + h < a.heads && i < late ? weights[(int64_t)(h0 + h) * a.table_width + i] : 0.0f;
+      }
+#pragma unroll
+      for (int m = 0; m < kPages; ++m)
+#pragma unroll
+        for (int h = 0; h < kHeadsAtOnce; ++h) sum[m] += (double)w[m][h];
+    }
+#pragma unroll
+    for (int m = 0; m < kPages; ++m) {
+      const int i = base + m * THREADS + tid;
+      if (i >= n) continue;
+      u64 k = page[m] >= 0 || i == n - 1 ? 1 : 0;
+      if (i < late && k != 0) k = i < a.sink ? ~0ull : max(key_of(sum[m]), (u64)2);
+      if (held) {
+        s.keys[i] = k;
+        s_table[i] = page[m];
+      } else {
+        store_key(memory + i, k);
+      }
+    }
   };
-  int32_t* out = a.table_out + (int64_t)b * a.budget;
-  const int taken = compact<kEvictThreads>(n, s_sel.wave_sum, kept, [&](int i, int place) {
-    out[place] = table[i];
-    if (a.weights_out)
-      for (int h = 0; h < a.heads; ++h)
-        a.weights_out[((int64_t)b * a.heads + h) * a.budget + place] = weights[(int64_t)h * a.table_width + i];
+  int base = 0;
+  for (; n - base > THREADS; base += kPagesAtOnce * THREADS) weigh(base, std::integral_constant<int, kPagesAtOnce>());
+  if (base < n) weigh(base, std::integral_constant<int, 1>());
+  __builtin_amdgcn_s_waitcnt(0);        // keys in memory have arrived there
+  __syncthreads();
+  if (held) {
+#pragma unroll
+    for (int i = 0; i < kEvictPer; ++i) keys.k[i] = keys.begin + i < keys.end ? s.keys[keys.begin + i] : 0;
+  }
+  // How many there are of each kind.  Of the newest, the oldest that the budget has no room for are left out: those of
+  // rank below `skip`.
+  int mine = 0, newest, others;
+  keys.each(n, [&](int i, u64 k) { mine += k != 0 && i < late ? 1 : 0; });
+  block_scan<THREADS>(mine, s_sel.wave_sum, others);
+  mine = 0;
+  keys.each(n, [&](int i, u64 k) { mine += k != 0 && i >= late ? 1 : 0; });
+  const int rank0 = block_scan<THREADS>(mine, s_sel.wave_sum, newest);
+  const int skip = max(newest - budget, 0), want = min(budget - (newest - skip), others);
+  // The chosen ones of the others: their keys alone are looked at.
+  Chosen c{0, 0, 0, true};
+  int end = n;
+  if (want > 0 && want < others) {
+    Keys<THREADS, kEvictPer> old = keys;
+    old.share(n);
+    old.end = min(old.end, late);
+    c = choose(old, n, want, s_sel);
+    end = ties_end(old, n, c, s_sel.wave_sum, &s_end);
+  }
+  int late_rank = rank0;
+  const auto kept = [&](int i, u64 k, int rank) {
+    if (k == 0) return false;
+    if (i >= late) return rank >= skip;
+    return want > 0 && (want >= others || is_chosen(k, i, c, end));
+  };
+  // Kept pages, dropped ones and their places in one go over the keys.
+  int stay = 0, gone = 0, stay_all, gone_all;
+  keys.each(n, [&](int i, u64 k) {
+    const bool keep = kept(i, k, late_rank);
+    late_rank += k != 0 && i >= late ? 1 : 0;
+    stay += keep ? 1 : 0;
+    gone += !keep && k != 0 ? 1 : 0;
   });
-  if (tid == 0) a.lens_out[b] = n > 0 ? (int)((taken - 1) * (int64_t)a.page_size + (len - 1) % a.page_size + 1) : 0;
-  for (int i = taken + tid; i < budget; i += kEvictThreads) {
+  int stay_at = block_scan<THREADS>(stay, s_sel.wave_sum, stay_all);
+  int gone_at = block_scan<THREADS>(gone, s_sel.wave_sum, gone_all);
+  late_rank = rank0;
+  int32_t* out = a.table_out + (int64_t)b * a.budget;
+  int32_t* freed = a.freed ? a.freed + (int64_t)b * a.table_width : nullptr;
+  // (Places first, then all pages and weights at once: each is a trip to memory.  The scans above come after the last read
+  // of the keys in LDS.)
+  const auto move = [&](int i, int to) {
+    out[to] = held ? s_table[i] : table[i];
+    if (!a.weights_out) return;
+    float* dst = a.weights_out + (int64_t)b * a.heads * a.budget + to;
+    for (int h0 = 0; h0 < a.heads; h0 += kHeadsAtOnce) {
+      float w[kHeadsAtOnce];
+#pragma unroll
+      for (int h = 0; h < kHeadsAtOnce; ++h)
+        if (h0 + h < a.heads) w[h] = weights[(int64_t)(h0 + h) * a.table_width + i];
+#pragma unroll
+      for (int h = 0; h < kHeadsAtOnce; ++h)
+        if (h0 + h < a.heads) dst[(int64_t)(h0 + h) * a.budget] = w[h];
+    }
+  };
+  keys.each(n, [&](int i, u64 k) {
+    const bool keep = kept(i, k, late_rank);
+    late_rank += k != 0 && i >= late ? 1 : 0;
+    if (keep) {
+      if (held) s.list[stay_at] = i;
+      else move(i, stay_at);
+      ++stay_at;
+    } else if (k != 0) {
+      if (held) s.list[stay_all + gone_at] = i;
+      else if (freed) freed[gone_at] = table[i];
+      ++gone_at;
+    }
+  });
+  if (held) {
+    __syncthreads();
+    for (int r = tid; r < stay_all; r += THREADS) move(s.list[r], r);
+    if (freed)
+      for (int r = tid; r < gone_all; r += THREADS) freed[r] = s_table[s.list[stay_all + r]];
+  }
+  if (tid == 0) a.lens_out[b] = n > 0 ? (int)((stay_all - 1) * (int64_t)a.page_size + (len - 1) % a.page_size + 1) : 0;
+  for (int i = stay_all + tid; i < budget; i += THREADS) {
     out[i] = -1;
     if (a.weights_out)
       for (int h = 0; h < a.heads; ++h) a.weights_out[((int64_t)b * a.heads + h) * a.budget + i] = 0.0f;
   }
-  if (a.freed) {
-    int32_t* gone = a.freed + (int64_t)b * a.table_width;
-    const int dropped = compact<kEvictThreads>(n, s_sel.wave_sum, [&](int i) { return table[i] >= 0 && !kept(i); },
-                                               [&](int i, int place) { gone[place] = table[i]; });
-    for (int64_t i = dropped + tid; i < a.table_width; i += kEvictThreads) gone[i] = -1;
-  }
+  if (freed)
+    for (int64_t i = gone_all + tid; i < a.table_width; i += THREADS) freed[i] = -1;
 }
 
 // Pages of a workgroup's share: one workgroup a (sequence, kv head) where those fill the GPU or have no counter; else
@@ -430,11 +587,22 @@ int64_t chunk_of(const KvSelectLaunch& a) {
   return std::min(a.table_width, std::max<int64_t>(chunk, 64));
 }
 
+template <int DB, int PER>
+void select_launch_per(const SelectParams& p, bool cut, dim3 grid, hipStream_t s) {
+  if (cut) hipLaunchKernelGGL((select_kernel<DB, true, PER>), grid, dim3(kThreads), 0, s, p);
+  else hipLaunchKernelGGL((select_kernel<DB, false, PER>), grid, dim3(kThreads), 0, s, p);
+}
+template <int DB>
+void select_launch(const SelectParams& p, bool cut, dim3 grid, hipStream_t s) {
+  if (p.a.table_width <= kThreads * kSelectFew) select_launch_per<DB, kSelectFew>(p, cut, grid, s);
+  else select_launch_per<DB, kSelectMany>(p, cut, grid, s);
+}
+
 }  // namespace
 
 size_t kv_select_workspace_bytes(const KvSelectLaunch& a) {
   if (a.table_width <= a.budget) return 0;
-  if (chunk_of(a) >= a.table_width && a.table_width <= kKeysInLds) return 0;
+  if (chunk_of(a) >= a.table_width && a.table_width <= kThreads * kSelectMany) return 0;
   return kCounters * sizeof(unsigned) + (size_t)(a.batch * a.heads) * a.table_width * sizeof(u64);
 }
 
@@ -445,27 +613,30 @@ hipError_t launch_kv_select(const KvSelectLaunch& a, hipStream_t s) {
   p.keys = reinterpret_cast<u64*>(static_cast<uint8_t*>(a.ws) + kCounters * sizeof(unsigned));
   const int64_t chunk = std::max<int64_t>(a.table_width <= a.budget ? a.table_width : chunk_of(a), 1);
   p.chunk = (int)chunk;
-  p.cut = chunk < a.table_width;
+  const bool cut = chunk < a.table_width;
   p.shares = (int)std::max<int64_t>((a.table_width + chunk - 1) / chunk, 1);
   const dim3 grid((unsigned)(a.batch * a.heads * p.shares));
   switch ((a.head_dim + 63) / 64) {
-    case 1: hipLaunchKernelGGL((select_kernel<1>), grid, dim3(kThreads), 0, s, p); break;
-    case 2: hipLaunchKernelGGL((select_kernel<2>), grid, dim3(kThreads), 0, s, p); break;
-    case 3: hipLaunchKernelGGL((select_kernel<3>), grid, dim3(kThreads), 0, s, p); break;
-    default: hipLaunchKernelGGL((select_kernel<4>), grid, dim3(kThreads), 0, s, p); break;
+    case 1: select_launch<1>(p, cut, grid, s); break;
+    case 2: select_launch<2>(p, cut, grid, s); break;
+    case 3: select_launch<3>(p, cut, grid, s); break;
+    default: select_launch<4>(p, cut, grid, s); break;
   }
   return hipGetLastError();
 }
 
+// Threads of an eviction: few where they hold the table's keys, many beyond.
 size_t kv_evict_workspace_bytes(const KvEvictLaunch& a) {
-  return a.table_width <= kKeysInLds ? 0 : (size_t)a.batch * a.table_width * sizeof(u64);
+  return a.table_width <= kEvictMany * kEvictPer ? 0 : (size_t)a.batch * a.table_width * sizeof(u64);
 }
 
 hipError_t launch_kv_evict(const KvEvictLaunch& a, hipStream_t s) {
   EvictParams p;
   p.a = a;
   p.keys = static_cast<u64*>(a.ws);
-  hipLaunchKernelGGL(evict_kernel, dim3((unsigned)a.batch), dim3(kEvictThreads), 0, s, p);
+  const dim3 grid((unsigned)a.batch);
+  if (a.table_width <= kEvictFew * kEvictPer) hipLaunchKernelGGL((evict_kernel<kEvictFew>), grid, dim3(kEvictFew), 0, s, p);
+  else hipLaunchKernelGGL((evict_kernel<kEvictMany>), grid, dim3(kEvictMany), 0, s, p);
   return hipGetLastError();
 }
 
