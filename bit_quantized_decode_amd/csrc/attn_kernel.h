@@ -75,6 +75,9 @@ constexpr int kJoinBatch = 12;             // parts that a thread of a join read
 static_assert(kCus * 4 <= (int)kAttnCounterBytes, "one counter a workgroup");
 constexpr double kLog2e = 1.4426950408889634;
 constexpr float kLn2 = 0.6931471805599453f;
+// Of a grid made by grid_of().
+__device__ __forceinline__ int64_t workgroup() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
+
 constexpr float kNegInf = -__builtin_inff();
 constexpr float kFltMax = 3.40282347e38f;
 

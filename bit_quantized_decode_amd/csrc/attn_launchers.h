@@ -1,5 +1,5 @@
 // Host-side launchers of the attention side's kernels; called only by
-// attn_abi.cpp after it has validated every argument.
+// attn_abi.cpp and attn_long_abi.cpp after they have validated every argument.
 #pragma once
 
 #include <hip/hip_runtime_api.h>
@@ -86,6 +86,12 @@ hipError_t launch_attn_decode(const AttnLaunch& a, hipStream_t s);
 
 // Page tables of [batch][kv_heads][table_width].
 hipError_t launch_attn_heads(const AttnLaunch& a, hipStream_t s);
+
+// A grid of so many workgroups, or a few more: one dimension of a grid has fewer than 2^32 threads.
+inline dim3 grid_of(int64_t workgroups) {
+  const int64_t x = workgroups < 65536 ? workgroups : 65536;
+  return dim3((unsigned)x, (unsigned)((workgroups + x - 1) / x));
+}
 
 struct AttnSharedLaunch {
   AttnLaunch attn;         // of the sequences' own tokens, its workspace the call's

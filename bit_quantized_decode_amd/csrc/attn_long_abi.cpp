@@ -102,6 +102,8 @@ int check_select(const nvfp4_kv_select_args* a, bool need_buffers) {
                 (long long)a->cache->kv_heads, (long long)kMaxHeads);
   NVFP4_TRY(check_width(a->table_width, 0, a->cache->page_size, "table_width"));
   NVFP4_TRY(check_width(a->budget, 1, a->cache->page_size, "budget"));
+  if (a->batch * a->cache->kv_heads > (int64_t(1) << 23))
+    return fail(NVFP4_ERR_SHAPE, "batch * kv_heads must be at most 2^23");
   if (!need_buffers || a->batch == 0) return NVFP4_OK;
   NVFP4_TRY(check_ld(a->ldq, a->q_heads * a->cache->head_dim, "ldq"));
   if (!a->q || !a->bounds || !a->seq_lens || (a->table_width > 0 && !a->page_table) || !a->pages_out || !a->lens_out)
@@ -179,6 +181,7 @@ int nvfp4_kv_bounds(const nvfp4_kv_cache* c, const int32_t* pages, int64_t n, ui
   NVFP4_GUARD_BEGIN
   NVFP4_TRY(check_cache(c, n > 0));
   NVFP4_TRY(check_tokens(n));
+  if (n * c->kv_heads > (int64_t(1) << 32)) return fail(NVFP4_ERR_SHAPE, "n * kv_heads must be at most 2^32");
   if (n == 0) return ok();
   if (!pages || !bounds) return fail(NVFP4_ERR_NULL, "pages and bounds must be non-NULL");
   if (!aligned4(pages)) return fail(NVFP4_ERR_ALIGN, "pages must be 4-byte aligned");

@@ -7,6 +7,11 @@
 // all of them.  One launch leaves the prefix's partial sums, attn_kernel those of the own tokens, and a third
 // joins them row by row.
 //
+// Bound by the vector units, which dequantise and exponentiate: 32 users of 40 heads under 32,768 NVFP4 tokens
+// 57 us, of which 46 for the prefix (21.6 Gflop; 48 MB), 6 for 200 tokens of each user and 5 for the join; 200 under 8192
+// bf16 tokens 80 us, 65 for the prefix (33.8 Gflop).  Few rows are bound by the bytes: 7 users of 256-wide heads
+// under 50,001 E4M3 tokens 43 us, 25 for the prefix (105 MB, 4.2 TB/s).
+//
 // The tiles and operands are those of attn_kernel.h.  Here a wavefront holds RT tiles of sixteen rows: one
 // 32-token tile of the cache is read, and dequantised, once for 16 RT rows.  The wavefronts of a
 // workgroup take the tiles of its share in turn and join through LDS at its end.
@@ -26,7 +31,8 @@ namespace {
 // all sequences, (sequence, query head of the group) in order.  Each unit's tiles are cut evenly over `each` workgroups
 // if that occupies nearly all CUs; else the line of all units' tiles is cut evenly over `grid` workgroups, of which some
 // then hold the end of one unit and the beginning of another.  Less is cut where there is little to do.
-// (Units of their own: 32 users of 40 heads under 32,768 NVFP4 tokens, 40 units, 58 us against 64.)
+// (Units of their own: 32 users of 40 heads under 32,768 NVFP4 tokens, 40 units, 58 us against 64.  That leave
+// CUs idle: 70 users of 64 heads under 10,000, 144 units of one workgroup, 81 us against 65 along the line.)
 struct Prefix {
   const int32_t* len;
   const int32_t* table;
@@ -97,6 +103,7 @@ __device__ __forceinline__ void load_queries(const PrefixParams& a, int head, in
   }
 }
 
+// Wavefronts a SIMD.  (Two row tiles of heads beyond 128 have registers, and room for their sums in LDS, for one.)
 constexpr int prefix_waves(int fmt, int db, int rt) { return rt == 1 ? waves_per_simd(fmt, db) : db <= 2 ? 2 : 1; }
 
 // Neighbouring shares on one XCD, whose L2 then serves a kv head's other blocks of rows.
@@ -335,7 +342,7 @@ __global__ __launch_bounds__(256) void join_kernel(const JoinParams a) {
   __shared__ float s_ml[kRowsHere][kRuns][2];
   __shared__ f32x4 s_o[kRowsHere][kRuns][kQuads];
   const int t = threadIdx.x % THREADS, at = threadIdx.x / THREADS, run = t / kQuads, d = 4 * (t - run * kQuads);
-  const int64_t row = (int64_t)blockIdx.x * kRowsHere + at;
+  const int64_t row = workgroup() * kRowsHere + at;
   const bool live = row < (int64_t)a.batch * a.q_heads && run < kRuns;
   const int b = live ? (int)(row / a.q_heads) : 0, qh = live ? (int)(row - (int64_t)b * a.q_heads) : 0;
   const int tiles = (prefix_len(a.prefix) + kTile - 1) / kTile;
@@ -393,18 +400,19 @@ __global__ __launch_bounds__(256) void join_kernel(const JoinParams a) {
 
 template <int DP>
 void join_launch(const JoinParams& p, hipStream_t s) {
-  // A wavefront a row where its pieces are few, a workgroup where there are more than it reads at once.
+  // A wavefront a row where its pieces are few, a workgroup where there are more than it reads at once.  (200 users of 40 heads,
+  // a piece or two a row: 96 us against 102; 16 users of 8 heads, 64 pieces: 27 us against 35.)
   const int64_t rows = (int64_t)p.batch * p.q_heads, pieces = p.prefix.grid / p.prefix.units + 1;
-  if (pieces <= 8 * (256 / DP)) hipLaunchKernelGGL((join_kernel<DP, 64>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, s, p);
-  else hipLaunchKernelGGL((join_kernel<DP, 256>), dim3((unsigned)rows), dim3(256), 0, s, p);
+  if (pieces <= 8 * (256 / DP)) hipLaunchKernelGGL((join_kernel<DP, 64>), grid_of((rows + 3) / 4), dim3(256), 0, s, p);
+  else hipLaunchKernelGGL((join_kernel<DP, 256>), grid_of(rows), dim3(256), 0, s, p);
 }
 
 int head_rows_of(const AttnSharedLaunch& a) { return (int)(a.attn.batch * (a.attn.q_heads / a.attn.cache.heads)); }
 
 int padded_of(const AttnSharedLaunch& a) { return (a.attn.cache.head_dim + 63) / 64; }
 
-
-// Row tiles of a workgroup: one if that takes all rows, else two.
+// Row tiles of a workgroup: one if that takes all rows, else two.  (Eight rows under 32,768 NVFP4 tokens 22.1 us against 24.4 with
+// an empty second tile.)
 int block_tiles_of(const AttnSharedLaunch& a) { return head_rows_of(a) <= kRows ? 1 : 2; }
 
 int64_t prefix_units_of(const AttnSharedLaunch& a) {

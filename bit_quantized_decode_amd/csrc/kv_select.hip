@@ -3,16 +3,21 @@
 //
 // Scores.  For a query q and a page whose keys lie between lo and hi channel by channel,
 //   sum_d max(q_d lo_d, q_d hi_d)  =  sum_d q_d (q_d < 0 ? lo_d : hi_d)
-// is at least q.k of every key in it.  The products of bf16 numbers are exact in fp64, and their sum is
-// rounded to 2^-53, so that the order of two pages does not depend on how the sum is cut; ties are ties.
+// is at least q.k of every key in it.  The products of bf16 numbers are exact in fp64 and their sum is
+// formed in one order for all pages, whatever the launch: pages of equal bounds tie.
 //
 // Keys.  An fp64 number's bits, all flipped if it is negative and the sign bit alone if not, order as an
 // unsigned integer; a NaN is taken above everything, and key 0 stands for a page that is not there.
 //
-// Selection.  A workgroup finds the K-th largest key eight bits at a time: a histogram of the next eight
+// Choosing.  A workgroup finds the K-th largest key eight bits at a time: a histogram of the next eight
 // bits of the keys that still agree with it, from the first bit in which any two differ; it stops as soon as the
 // keys that agree are all taken or all of one kind.  Each thread holds a run of consecutive keys in registers; more
 // keys than that stay in memory and are read in each step.
+//
+// What bounds them is latency where little is to be done: one user's choice of 128 pages out of 2048 for each of 8 kv
+// heads (8.4 MB of bounds) takes 16 us, of which the launch 3, the scores 5, the way to the last workgroup of a pair 4 and
+// choosing 4; 256 pages of 32 users are evicted in 8 us, 8192 of one in 35 (keys 9, choosing 11, places and outputs 11).
+// Many scores are bound by fp64 arithmetic: 32 users of up to 512 pages and 8 kv heads of five rows 27 us, each row 3 us of it.
 #include <algorithm>
 #include <type_traits>
 
@@ -417,19 +422,19 @@ struct EvictParams {
   u64* keys;                           // [batch][table_width], if registers do not hold them
 };
 
-constexpr int kEvictPer = 8;
 constexpr int kEvictFew = 256, kEvictMany = 1024;  // threads
+constexpr int kPerFew = 4, kPerMany = 8;           // keys that each holds
 constexpr int kHeadsAtOnce = 8, kPagesAtOnce = 4;  // loads in flight of a thread
 
 // One workgroup a sequence.
-template <int THREADS>
+template <int THREADS, int PER>
 __global__ __launch_bounds__(THREADS) void evict_kernel(const EvictParams p) {
   const KvEvictLaunch& a = p.a;
   __shared__ union {
-    u64 keys[THREADS * kEvictPer];
-    int list[THREADS * kEvictPer];      // places of the pages that stay, in order, and behind them of those dropped
+    u64 keys[THREADS * PER];
+    int list[THREADS * PER];      // places of the pages that stay, in order, and behind them of those dropped
   } s;
-  __shared__ int s_table[THREADS * kEvictPer];
+  __shared__ int s_table[THREADS * PER];
   __shared__ SelectLds<THREADS> s_sel;
   __shared__ int s_end;
   const int tid = threadIdx.x, b = blockIdx.x;
@@ -439,7 +444,7 @@ __global__ __launch_bounds__(THREADS) void evict_kernel(const EvictParams p) {
   const int32_t* table = a.table + (int64_t)b * a.table_width;
   const float* weights = a.weights + (int64_t)b * a.heads * a.table_width;
   u64* memory = p.keys ? p.keys + (int64_t)b * a.table_width : nullptr;
-  Keys<THREADS, kEvictPer> keys;
+  Keys<THREADS, PER> keys;
   keys.memory = memory;
   keys.share(n);
   const bool held = keys.held(n);
@@ -492,7 +497,7 @@ __global__ __launch_bounds__(THREADS) void evict_kernel(const EvictParams p) {
   __syncthreads();
   if (held) {
 #pragma unroll
-    for (int i = 0; i < kEvictPer; ++i) keys.k[i] = keys.begin + i < keys.end ? s.keys[keys.begin + i] : 0;
+    for (int i = 0; i < PER; ++i) keys.k[i] = keys.begin + i < keys.end ? s.keys[keys.begin + i] : 0;
   }
   // How many there are of each kind.  Of the newest, the oldest that the budget has no room for are left out: those of
   // rank below `skip`.
@@ -507,7 +512,7 @@ __global__ __launch_bounds__(THREADS) void evict_kernel(const EvictParams p) {
   Chosen c{0, 0, 0, true};
   int end = n;
   if (want > 0 && want < others) {
-    Keys<THREADS, kEvictPer> old = keys;
+    Keys<THREADS, PER> old = keys;
     old.share(n);
     old.end = min(old.end, late);
     c = choose(old, n, want, s_sel);
@@ -578,7 +583,8 @@ __global__ __launch_bounds__(THREADS) void evict_kernel(const EvictParams p) {
 }
 
 // Pages of a workgroup's share: one workgroup a (sequence, kv head) where those fill the GPU or have no counter; else
-// so that there are four a CU, but 64 pages at least.
+// so that there are four a CU, but 64 pages at least.  (32 users of 8 kv heads: two a CU 53 us for 1000 pages against 46, 31 for 500
+// against 28.  One user: shares of 32 pages and more 18 us for 2048 pages against 15.5, of 128 17.8.)
 int64_t chunk_of(const KvSelectLaunch& a) {
   const int64_t pairs = a.batch * a.heads;
   if (pairs >= kCounters) return a.table_width;
@@ -594,6 +600,7 @@ void select_launch_per(const SelectParams& p, bool cut, dim3 grid, hipStream_t s
 }
 template <int DB>
 void select_launch(const SelectParams& p, bool cut, dim3 grid, hipStream_t s) {
+  // (One user of 1000 pages 14.6 us against 18.9, 150 users 180 against 192.)
   if (p.a.table_width <= kThreads * kSelectFew) select_launch_per<DB, kSelectFew>(p, cut, grid, s);
   else select_launch_per<DB, kSelectMany>(p, cut, grid, s);
 }
@@ -610,7 +617,7 @@ hipError_t launch_kv_select(const KvSelectLaunch& a, hipStream_t s) {
   SelectParams p;
   p.a = a;
   p.counters = static_cast<unsigned*>(a.ws);
-  p.keys = reinterpret_cast<u64*>(static_cast<uint8_t*>(a.ws) + kCounters * sizeof(unsigned));
+  p.keys = a.ws ? reinterpret_cast<u64*>(p.counters + kCounters) : nullptr;
   const int64_t chunk = std::max<int64_t>(a.table_width <= a.budget ? a.table_width : chunk_of(a), 1);
   p.chunk = (int)chunk;
   const bool cut = chunk < a.table_width;
@@ -625,9 +632,8 @@ hipError_t launch_kv_select(const KvSelectLaunch& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Threads of an eviction: few where they hold the table's keys, many beyond.
 size_t kv_evict_workspace_bytes(const KvEvictLaunch& a) {
-  return a.table_width <= kEvictMany * kEvictPer ? 0 : (size_t)a.batch * a.table_width * sizeof(u64);
+  return a.table_width <= kEvictMany * kPerMany ? 0 : (size_t)a.batch * a.table_width * sizeof(u64);
 }
 
 hipError_t launch_kv_evict(const KvEvictLaunch& a, hipStream_t s) {
@@ -635,8 +641,10 @@ hipError_t launch_kv_evict(const KvEvictLaunch& a, hipStream_t s) {
   p.a = a;
   p.keys = static_cast<u64*>(a.ws);
   const dim3 grid((unsigned)a.batch);
-  if (a.table_width <= kEvictFew * kEvictPer) hipLaunchKernelGGL((evict_kernel<kEvictFew>), grid, dim3(kEvictFew), 0, s, p);
-  else hipLaunchKernelGGL((evict_kernel<kEvictMany>), grid, dim3(kEvictMany), 0, s, p);
+  // Few threads where they hold the table's keys.  (32 users of 256 pages 8.4 us against 12.5, of 1000 15.0 against 15.7, of 2000 on
+  // eight keys a thread 24.8 against 20.0; 300 users of 1000 18.0 against 30.1.)
+  if (a.table_width <= kEvictFew * kPerFew) hipLaunchKernelGGL((evict_kernel<kEvictFew, kPerFew>), grid, dim3(kEvictFew), 0, s, p);
+  else hipLaunchKernelGGL((evict_kernel<kEvictMany, kPerMany>), grid, dim3(kEvictMany), 0, s, p);
   return hipGetLastError();
 }
 

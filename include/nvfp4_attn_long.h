@@ -27,7 +27,7 @@ extern "C" {
  * [0, pages) hold nothing.  The prefix's pages may be anyone's, a sequence's own among them.
  *
  * In one call batch * q_heads is at most 2^30, and the prefix's tiles of 32 tokens, counted for every kv head
- * and 16, 32 or 64 rows of batch * q_heads / kv_heads, fewer than 2^31 at the longest prefix that its table allows.
+ * and 16 or 32 rows of batch * q_heads / kv_heads, fewer than 2^31 at the longest prefix that its table allows.
  */
 typedef struct nvfp4_attn_shared_args {
   nvfp4_attn_args attn;
@@ -47,7 +47,7 @@ int nvfp4_attn_shared(const nvfp4_attn_shared_args* args /* host */, void* strea
  * in both.  A page's bounds mean something once all its places are written; kv_select() needs
  * them of every page of a sequence but its last, so that they are formed when a page is full.
  */
-int nvfp4_kv_bounds(const nvfp4_kv_cache* cache /* host */, const int32_t* pages, int64_t n /* 0..2^24 */,
+int nvfp4_kv_bounds(const nvfp4_kv_cache* cache /* host */, const int32_t* pages, int64_t n /* 0..2^24; n * kv_heads at most 2^32 */,
                     uint16_t* bounds /* bf16 [cache->pages][kv_heads][2][head_dim], 16-byte aligned */, void* stream);
 
 /* nvfp4_kv_select(): of the N = ceil(n_b / page_size) pages of sequence b (n_b = seq_lens[b], clamped to
@@ -61,7 +61,7 @@ int nvfp4_kv_bounds(const nvfp4_kv_cache* cache /* host */, const int32_t* pages
  * nvfp4_attn_decode_heads() over pages_out and lens_out is attention over the selected pages. */
 typedef struct nvfp4_kv_select_args {
   const nvfp4_kv_cache* cache;  /* host; its pool is not looked at */
-  int64_t batch;            /* 0..65536 */
+  int64_t batch;            /* 0..65536; batch * kv_heads at most 2^23 */
   int64_t q_heads;          /* multiple of kv_heads */
   const uint16_t* q;        /* bf16 [batch][ldq], 16-byte aligned */
   int64_t ldq;
@@ -90,9 +90,9 @@ int nvfp4_attn_decode_heads(const nvfp4_attn_args* args /* host */, void* stream
  *   weights_out[b][h][i] = decay * weights[b][h][i] + sum exp(s_j - lse)
  * over the query heads of kv head h and the tokens j of page i that they attend to, for all i < table_width: a page's
  * share of what its readers looked at, each query head adding up to 1.  Terms and sums are fp32, as
- * the attention's are; a query head whose lse is -inf adds nothing, one whose lse is NaN makes its kv head's
- * attended pages NaN.  decay 0: weights is not read and may be NULL.  weights_out may be weights.  q_heads,
- * batch and table as in nvfp4_attn_decode(), and batch * kv_heads * table_width at most 2^31. */
+ * the attention's are; a query head whose lse is -inf adds nothing, one whose lse is NaN makes the pages NaN that it
+ * attends to, but for those whose terms are all 0.  decay 0: weights is not read and may be NULL.  weights_out may
+ * be weights.  q_heads, batch and table as in nvfp4_attn_decode(), and batch * kv_heads * table_width at most 2^31. */
 typedef struct nvfp4_attn_weigh_args {
   nvfp4_attn_args attn;
   const float* weights;     /* [batch][kv_heads][table_width] */

@@ -149,6 +149,7 @@ def test_bounds_refusals(L):  # noqa: F811
     d = desc()
     call = lambda c=d, pages=A, n=4, bounds=A: L.nvfp4_kv_bounds(ctypes.byref(c), pages, n, bounds, None)  # noqa: E731
     assert call(n=-1) == call(n=(1 << 24) + 1) == B.NVFP4_ERR_SHAPE
+    assert call(c=desc(pages=1, kv_heads=1024), n=(1 << 22) + 1) == B.NVFP4_ERR_SHAPE
     assert call(pages=None) == call(bounds=None) == call(c=desc(pool=None)) == B.NVFP4_ERR_NULL
     assert call(pages=ODD) == call(bounds=A + 8) == call(c=desc(pool=A + 8)) == B.NVFP4_ERR_ALIGN
     assert call(n=0, pages=None, bounds=None) == call(n=0, c=desc(pool=None)) == B.NVFP4_OK
