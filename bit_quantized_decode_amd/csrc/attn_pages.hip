@@ -45,10 +45,22 @@ __global__ __launch_bounds__(256) void weigh_kernel(const WeighParams w) {
       const float* mass = w.mass + ((unit * a.row_tiles + rt) * w.groups + first) * a.part_rows;
       const int rows = min(a.group - rt * kRows, kRows);
       const float* lse = a.lse + (int64_t)b * a.q_heads + head * a.group + rt * kRows;
-      for (int e = lane; e < n * a.part_rows; e += LANES) {
-        const int r = e % a.part_rows;
-        const float m = r < rows ? mass[e] : kNegInf;
-        if (m != kNegInf) sum += __builtin_amdgcn_exp2f(m - lse[r] * (float)kLog2e);   // (-inf: no term, or a row of none)
+      // Both loads at once, four of each a trip.  A sum of -inf is one of no terms, or of a row that has none; none is more than
+      // its row's, whatever the rounding of far scores says.
+      for (int e0 = lane; e0 < n * a.part_rows; e0 += 4 * LANES) {
+        float m[4], l[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int e = e0 + i * LANES, r = e % a.part_rows;
+          const bool in = e < n * a.part_rows && r < rows;
+          m[i] = in ? mass[e] : kNegInf;
+          l[i] = lse[in ? r : 0];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float x = m[i] - l[i] * (float)kLog2e;
+          sum += m[i] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(x > 0.0f ? 0.0f : x);   // NaN stays NaN
+        }
       }
     }
   }

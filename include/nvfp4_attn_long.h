@@ -90,7 +90,7 @@ int nvfp4_attn_decode_heads(const nvfp4_attn_args* args /* host */, void* stream
  *   weights_out[b][h][i] = decay * weights[b][h][i] + sum exp(s_j - lse)
  * over the query heads of kv head h and the tokens j of page i that they attend to, for all i < table_width: a page's
  * share of what its readers looked at, each query head adding up to 1.  Terms and sums are fp32, as
- * the attention's are; a query head whose lse is -inf adds nothing, one whose lse is NaN makes the pages NaN that it
+ * the attention's are, and s_j - lse is off by up to 2^-21 (|s_j| + |lse| + 1), never above 0; a query head whose lse is -inf adds nothing, one whose lse is NaN makes the pages NaN that it
  * attends to, but for those whose terms are all 0.  decay 0: weights is not read and may be NULL.  weights_out may
  * be weights.  q_heads, batch and table as in nvfp4_attn_decode(), and batch * kv_heads * table_width at most 2^31. */
 typedef struct nvfp4_attn_weigh_args {

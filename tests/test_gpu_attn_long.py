@@ -16,7 +16,7 @@ WAIT = 2_000_000      # clock ticks, about a millisecond: what follows on that s
 
 
 def to(dev, a, dtype=torch.int32):
-    return torch.as_tensor(np.asarray(a), dtype=dtype, device=dev)
+    return torch.as_tensor(np.array(a, order="C"), dtype=dtype, device=dev)
 
 
 def rows(n, heads, d, seed):
@@ -233,6 +233,26 @@ def test_scores_far_beyond_the_exponentials_range(shift):
                 bound = 2.0 ** -8 * np.abs(best.mean(0)) + (len(best) + 8) * 2.0 ** -24 * np.abs(best).mean(0) + 1e-30
                 assert (np.abs(out[b, h] - best.mean(0)) <= bound).all(), (name, b, h)
                 assert abs(lse[b, h] - s.max() * 2.0 ** shift) <= 2.0 ** -20 * abs(s.max() * 2.0 ** shift)
+
+
+@pytest.mark.parametrize("shift", [20, 24, 32, 90])
+def test_weights_of_far_scores(shift):
+    """Scores of +-2^shift times small integers: pages without a largest term weigh nothing, the others no more than their sixteens."""
+    dev, page, n = device(), 32, 300
+    x = Weighed(B.NVFP4_KV_E4M3, [n], 4, 2, 64, page, seed=12)
+    k = torch.zeros(n, 2, 64)
+    best = np.arange(n) // page % 3 == 1                   # pages 1, 4 and 7 hold the largest scores
+    k[:, :, 0] = torch.from_numpy(np.where(best & (np.arange(n) % 5 == 0), 6.0, 4.0))[:, None]
+    x.pool.write(x.pool.slots(x.table[0], n)[0], k.to(torch.bfloat16), rows(n, 2, 64, 13))
+    x.q.zero_()
+    x.q[:, :, 0] = 1.0
+    w = torch.full((1, 2, x.table.shape[1]), 0.25, device=dev)
+    out, lse, w = B.attn_weigh(*x.args(), w, 1.0, scale=2.0 ** shift, lse=True)
+    w = w.cpu().numpy() - 0.25
+    assert np.isfinite(w).all() and (w[:, :, 0::3] == 0).all() and (w[:, :, 2::3] == 0).all()
+    assert (w[:, :, 1::3] >= 0).all() and (w <= 2 * page // 16).all()
+    if shift == 20:                                        # half a step of a score is 2^-2: a factor of 2 at most for each rounding
+        assert (w[:, :, 1::3] > 0).all()
 
 
 # ---- the largest -------------------------------------------------------------------------------------
