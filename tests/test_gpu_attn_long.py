@@ -195,6 +195,75 @@ def test_nan_in_a_cache_row_stays_in_its_head(fmt, at):
                 assert lse[b, 2:].isnan().all() == (hit and side == 0) and (hit or not lse[b].isnan().any()), (name, b)
 
 
+class Part:
+    """Some heads and channels of a pool."""
+
+    def __init__(self, pool, heads, channels=slice(None)):
+        self.fmt, self.k, self.v = pool.fmt, pool.k[:, heads], pool.v[:, heads][..., channels]
+        self.hk, self.d = self.k.shape[1:]
+
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("at", [3, 70])
+def test_infinite_keys(at, sign):
+    """bf16: a score of -inf weighs nothing, one of +inf makes its query head's row and lse NaN."""
+    inf = float("inf")
+    x, calls = kinds(B.NVFP4_KV_BF16, [200, 50], seed=at + 1)
+    x.q[:, :2, 5], x.q[:, 2:, 5] = sign, -sign                 # head 0: +inf, head 1: -inf
+    slot = np.array([x.table[0, at // 32] * 32 + at % 32])
+    key = rows(1, 2, 64, 5)
+    key[..., 5] = sign * inf
+    x.pool.write(slot, key, rows(1, 2, 64, 6))
+    for name, call, lists in calls:
+        out, lse = call()
+        for b in range(2):
+            hit = slot[0] in lists[b]
+            assert out[b, :2].isnan().all() == hit and lse[b, :2].isnan().all() == hit, (name, b)
+        rest = [np.setdiff1d(at_b, slot) for at_b in lists]
+        G.check_rows(Part(x.pool, slice(1, 2)), x.q[:, 2:], rest, out[:, 2:], lse[:, 2:], what=name)
+
+
+@pytest.mark.parametrize("fmt", G.FORMATS, ids=G.IDS)
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+def test_queries_that_are_not_finite(fmt, bad):
+    """Their own rows alone: NaN where some score is, nothing where all scores are -inf."""
+    x, calls = kinds(fmt, [200, 50], seed=14)
+    n = x.pool.pages * 32
+    k = rows(n, 2, 64, 7)
+    k[:, 1, 5] = -4.0
+    x.pool.write(np.arange(n), k, rows(n, 2, 64, 8))
+    x.q[0, 2, 5] = bad
+    for name, call, lists in calls:
+        out, lse = call()
+        if bad == bad:
+            assert (out[0, 2] == 0).all() and lse[0, 2] == -float("inf"), name
+        else:
+            assert out[0, 2].isnan().all() and lse[0, 2].isnan(), name
+        head = [0, 1, 3]
+        for h in head:
+            G.check_rows(Part(x.pool, slice(h // 2, h // 2 + 1)), x.q[:, h:h + 1], lists, out[:, h:h + 1], lse[:, h:h + 1], what=(name, h))
+
+
+@pytest.mark.parametrize("fmt", G.FORMATS, ids=G.IDS)
+@pytest.mark.parametrize("at", [3, 70])
+def test_infinite_values(fmt, at):
+    """They reach the outputs that hold them (their element, in E4M3 their row, in NVFP4 their block of 16), and lse not."""
+    x, calls = kinds(fmt, [200, 50], seed=15)
+    slot = np.array([x.table[0, at // 32] * 32 + at % 32])
+    value = rows(1, 2, 64, 9)
+    value[0, 1, 5] = float("inf")
+    x.pool.write(slot, rows(1, 2, 64, 10), value)
+    reach = {0: slice(5, 6), 1: slice(0, 64), 2: slice(0, 16)}[fmt]
+    for name, call, lists in calls:
+        out, lse = call()
+        assert lse.isfinite().all()
+        G.check_rows(Part(x.pool, slice(0, 1)), x.q[:, :2], lists, out[:, :2], lse[:, :2], what=name)
+        for b in range(2):
+            assert out[b, 2:, reach].isfinite().logical_not().all() == (slot[0] in lists[b]), (name, b)
+            if fmt != B.NVFP4_KV_E4M3:
+                assert out[b, 2:, 16:].isfinite().all()
+
+
 @pytest.mark.parametrize("fmt", G.FORMATS, ids=G.IDS)
 def test_garbage_behind_the_last_token_is_not_read(fmt):
     """The places of attended pages that no sequence has reached hold NaN codes and scales (Pool leaves them so)."""
