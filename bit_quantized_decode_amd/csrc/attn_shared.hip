@@ -225,6 +225,7 @@ __global__ __launch_bounds__(256 * prefix_waves(FMT, DB, RT), (prefix_waves(FMT,
       load_k<FMT, DB, kPolicy>(from, lane, t);
 
       if (!whole) {
+        asm volatile("" : "+v"(okbits));   // (here, or the compiler tests the bits of whole tiles too)
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
