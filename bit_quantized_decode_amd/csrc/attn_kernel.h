@@ -121,7 +121,8 @@ enum Mode {
   kPlain,
   kHeads,    // the page table is [batch][kv_heads][table_width]
   kWeigh,    // the terms of every sixteen tokens are summed and kept, for the weights of pages
-  kRaw       // rows are left as reference, sum and sums, for a later join
+  kRaw,      // rows are left as reference, sum and sums, for a later join
+  kBehind    // each sequence's tokens come behind a prefix with a page table of its own
 };
 template <int MODE>
 struct ModeParams : AttnParams {};
@@ -138,6 +139,15 @@ struct ModeParams<kWeigh> : AttnParams {
 template <>
 struct ModeParams<kRaw> : AttnParams {
   float* raw;
+};
+
+// kBehind: a row's sixteens are the prefix's, then its own; table_width is the sum of both tables'.
+template <>
+struct ModeParams<kBehind> : AttnParams {
+  const int32_t* prefix_table;
+  const int32_t* prefix_len;
+  int32_t prefix_most, own_most;     // tokens that the tables hold
+  int64_t own_width;
 };
 
 // The tokens that a row attends to.
@@ -584,8 +594,20 @@ __global__ __launch_bounds__(256 * waves_per_simd(FMT, DB), (waves_per_simd(FMT,
   const int qn = lane & 15, h = lane >> 4, d0 = kE * h;
   const int units_per_row = a.cache.heads * a.row_tiles;
 
+  // kBehind: places [hole, own) behind the prefix's last token hold none.
+  int hole = 0, own = 0;
+  if constexpr (MODE == kBehind) {
+    hole = min(max(*a.prefix_len, 0), a.prefix_most);
+    own = (hole + kKvGroup - 1) & ~(kKvGroup - 1);
+  }
   // The line's length, and each lane's stretch of it: `per` rows of the batch.
-  const auto len_of = [&](int row) { return row < a.batch ? a.lens[row] : 0; };
+  const auto len_of = [&](int row) {
+    if constexpr (MODE == kBehind) {
+      const int len = row < a.batch ? a.lens[row] : -1;
+      return len < 0 ? 0 : own + min(len, a.own_most);
+    }
+    return row < a.batch ? a.lens[row] : 0;
+  };
   const auto places_in = [&](int row, int len) {
     return row < a.batch ? span_of(a, len).tiles + kLead : 0;  // of a unit
   };
@@ -722,9 +744,17 @@ __global__ __launch_bounds__(256 * waves_per_simd(FMT, DB), (waves_per_simd(FMT,
         looked_up = -1;
         if (it + (lane >> 1) < count && tok < sp.end) {
           const int tg = tok / kKvGroup, pg = tg / a.cache.gpp;
-          const int page = a.table[(MODE == kHeads ? (int64_t)b * a.cache.heads + head : (int64_t)b) * a.table_width + pg];
-          if (page >= 0 && page < a.cache.pages)
-            looked_up = (page * a.cache.heads + head) * a.cache.gpp + (tg - pg * a.cache.gpp);
+          if constexpr (MODE == kBehind) {
+            const bool behind = tok >= own;
+            const int og = behind ? tg - own / kKvGroup : tg, op = og / a.cache.gpp;
+            const int page = *(behind ? a.table + (int64_t)b * a.own_width + op : a.prefix_table + op);
+            if (page >= 0 && page < a.cache.pages)
+              looked_up = (page * a.cache.heads + head) * a.cache.gpp + (og - op * a.cache.gpp);
+          } else {
+            const int page = a.table[(MODE == kHeads ? (int64_t)b * a.cache.heads + head : (int64_t)b) * a.table_width + pg];
+            if (page >= 0 && page < a.cache.pages)
+              looked_up = (page * a.cache.heads + head) * a.cache.gpp + (tg - pg * a.cache.gpp);
+          }
         }
       }
       group[0] = __builtin_amdgcn_readlane(looked_up, 2 * (it & 31));
@@ -761,7 +791,8 @@ __global__ __launch_bounds__(256 * waves_per_simd(FMT, DB), (waves_per_simd(FMT,
     for (int it = 0; it < count; ++it) {
       const int tok0 = sp.base + (first + it) * kTile;
       const bool has0 = group[0] >= 0, has1 = group[1] >= 0;
-      const bool whole = has0 && has1 && tok0 >= sp.begin && tok0 + kTile <= sp.end;
+      const bool whole = has0 && has1 && tok0 >= sp.begin && tok0 + kTile <= sp.end &&
+                         (MODE != kBehind || tok0 >= own || tok0 + kTile <= hole);
       if (it + 1 < count) look_up(it + 1, group);
       else group[0] = group[1] = -1;
       to_load(group);
@@ -771,7 +802,8 @@ __global__ __launch_bounds__(256 * waves_per_simd(FMT, DB), (waves_per_simd(FMT,
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int tok = tok0 + (i / 4) * kKvGroup + 4 * h + i % 4;
-          okbits |= ((i / 4 ? has1 : has0) && tok >= sp.begin && tok < sp.end) ? 1u << i : 0u;
+          okbits |= ((i / 4 ? has1 : has0) && tok >= sp.begin && tok < sp.end && (MODE != kBehind || tok < hole || tok >= own))
+                        ? 1u << i : 0u;
         }
       }
 

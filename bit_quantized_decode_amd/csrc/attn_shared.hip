@@ -4,7 +4,7 @@
 // with references r, r' and sums l, l' of terms 2^(s - r), the joined sums are those of the larger
 // reference, the other's times 2^(r' - r).  So the prefix is one problem of its own: for each kv head, the
 // queries of all sequences and of its group are the rows of a matrix, and its keys and values are read once for
-// all of them.  One launch leaves the prefix's partial sums, attn_kernel those of the own tokens, and a third
+// all of them (where that saves more than two launches cost, see apart()).  One launch leaves the prefix's partial sums, attn_kernel those of the own tokens, and a third
 // joins them row by row.
 //
 // Bound by the vector units, which dequantise and exponentiate: 32 users of 40 heads under 32,768 NVFP4 tokens
@@ -442,6 +442,25 @@ int prefix_grid_of(const AttnSharedLaunch& a) {
   return (int)std::min<int64_t>(n, kCus);
 }
 
+AttnLaunch behind_of(const AttnSharedLaunch& a) {
+  AttnLaunch l = a.attn;
+  l.table_width += a.prefix_width;
+  return l;
+}
+// Whether each sequence reads the prefix by itself (kBehind), in one launch instead of three: where a prefix that fills its table
+// is so few bytes, most of which come from caches, or nothing would be shared.  (32 users of 40 heads, NVFP4: under 500 tokens 11.2 us
+// against 20.6, 2000 (66 MB) 18.4 against 23.2, 4000 (131 MB) 26.6 against 24.9; 16 users, bf16: 1000 13.0 against 19.3, 2000
+// (131 MB) 18.8 against 20.9, 4000 22.8 against 22.9; one user of 16 heads under 30,000 E4M3 tokens 17.4 against 22.0.)
+constexpr int64_t kApartBytes = int64_t(96) << 20;
+bool apart(const AttnSharedLaunch& a) {
+  const int64_t row_tiles = row_tiles_of(a.attn), block = kRows * block_tiles_of(a);
+  const int64_t bytes = a.attn.batch * row_tiles * a.prefix_width * a.attn.cache.gpp * a.attn.cache.heads *
+                        (int64_t)kv_code_bytes(a.attn.format, padded_of(a));
+  const bool alone = a.attn.batch * row_tiles <= (head_rows_of(a) + block - 1) / block;
+  return (alone || bytes <= kApartBytes) && attn_fits(behind_of(a)) &&
+         behind_of(a).table_width * a.attn.cache.page_size <= int64_t(1) << 30;
+}
+
 size_t rounded(size_t bytes) { return (bytes + 255) & ~(size_t)255; }
 
 size_t row_bytes(const AttnSharedLaunch& a) { return (64 * padded_of(a) + 4) * sizeof(float); }
@@ -475,12 +494,22 @@ bool attn_shared_fits(const AttnSharedLaunch& a) {
 }
 
 size_t attn_shared_workspace_bytes(const AttnSharedLaunch& a) {
-  if (prefix_grid_of(a) == 0) return attn_workspace_bytes(a.attn);
+  if (apart(a)) return attn_workspace_bytes(behind_of(a));
   return pieces_at(a) + (size_t)(prefix_units_of(a) + prefix_grid_of(a)) * (kRows * block_tiles_of(a)) * row_bytes(a);
 }
 
 hipError_t launch_attn_shared(const AttnSharedLaunch& a, hipStream_t s) {
-  if (prefix_grid_of(a) == 0) return launch_attn_decode(a.attn, s);   // no prefix
+  if (apart(a)) {
+    ModeParams<kBehind> p;
+    const AttnLaunch l = behind_of(a);
+    fill_params(l, p);
+    p.prefix_table = a.prefix_table;
+    p.prefix_len = a.prefix_len;
+    p.prefix_most = (int32_t)(a.prefix_width * a.attn.cache.page_size);
+    p.own_most = (int32_t)(a.attn.table_width * a.attn.cache.page_size);
+    p.own_width = a.attn.table_width;
+    return attn_launch(l, p, s);
+  }
   PrefixParams p;
   p.cache = a.attn.cache;
   p.q = a.attn.q;

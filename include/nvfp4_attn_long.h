@@ -21,7 +21,8 @@ extern "C" {
  *   s_j = scale * q . k_j   over the first n = *prefix_len tokens of prefix_table (clamped to
  *                           [0, prefix_width * page_size]) and the first seq_lens[b] of its own table,
  * with o and lse as nvfp4_attn_decode() defines them over both.  attn.page_table and attn.seq_lens count
- * the own tokens alone: the first of them starts a page.  The prefix is read once for all sequences.
+ * the own tokens alone: the first of them starts a page.  The prefix is read once for all sequences
+ * (by each, in one launch, where its table holds little).
  * A sequence whose length is below 0 is a free place of the batch: it attends to nothing, not to the
  * prefix either, and its row is zeros with lse = -inf.  attn.window must be 0.  Prefix pages outside
  * [0, pages) hold nothing.  The prefix's pages may be anyone's, a sequence's own among them.

@@ -46,6 +46,14 @@ class Pool:
         return np.stack((k.min(1), k.max(1)), 2)
 
 
+def with_room(prefix_pages, fmt, batch, hq, hk, d, page):
+    """A prefix's table with places for so many more pages (ids that hold nothing) that its tokens are read for all sequences at
+    once, not by each: beyond 96 MB of codes."""
+    group = 16 * 2 * 64 * -(-d // 64) * {0: 4, 1: 2, 2: 1}[fmt] // 2
+    each = batch * -(-hq // hk // 16) * hk * (page // 16) * group
+    return np.concatenate((prefix_pages, np.full((97 << 20) // each + 1, 2 ** 31 - 1))).astype(np.int32)
+
+
 def queries(b, hq, d, seed=1, spread=1.0):
     rng = np.random.default_rng(seed)
     return torch.from_numpy((rng.standard_normal((b, hq, d)) * spread).astype(np.float32)).to(torch.bfloat16)

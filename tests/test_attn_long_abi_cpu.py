@@ -178,11 +178,15 @@ def test_workspaces(L):  # noqa: F811
     d = desc()
     plain = need("attn_decode", attn(d))
     blank = dict(q=None, out=None, page_table=None, seq_lens=None, workspace=None, scale=0.0, ldq=0, ldo=0)
-    s = need("attn_shared", shared(d, blank, prefix_table=None, prefix_len=None))
+    s = need("attn_shared", shared(d, blank, prefix_table=None, prefix_len=None, prefix_width=1 << 16))
     assert s > plain and need("attn_shared", shared(d, prefix_width=0)) == plain
+    # A prefix that each sequence reads by itself is so much more of its table; to the largest tables it is not.
+    assert need("attn_shared", shared(d)) == need("attn_decode", attn(d, table_width=attn(d).table_width + 100))
+    most = (1 << 30) // d.page_size
+    assert need("attn_shared", shared(d, dict(batch=1, q_heads=8, table_width=most), prefix_width=most)) > plain
     w = need("attn_weigh", weigh(d, blank, weights=None, weights_out=None, decay=-1.0))
     assert w > plain + 4 * 4 * 40 * 16
-    for name, a, n in (("attn_shared", shared(d, dict(workspace_bytes=s - 1)), s), ("attn_weigh", weigh(d, dict(workspace_bytes=w - 1)), w)):
+    for name, a, n in (("attn_shared", shared(d, dict(workspace_bytes=s - 1), prefix_width=1 << 16), s), ("attn_weigh", weigh(d, dict(workspace_bytes=w - 1)), w)):
         assert getattr(L, f"nvfp4_{name}")(ctypes.byref(a), None) == B.NVFP4_ERR_WORKSPACE
         assert str(n).encode() in L.nvfp4_last_error()
     for name, a in (("attn_shared", shared(d, dict(batch=0))), ("attn_weigh", weigh(d, dict(batch=0))), ("kv_select", select(d, batch=0)),

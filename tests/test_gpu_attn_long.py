@@ -122,9 +122,11 @@ def test_generation_with_eviction(fmt):
     assert evictions >= 1 and len(free) == pages - sum(-(-n // page) for n in lens)
 
 
+@pytest.mark.parametrize("at_once", [False, True], ids=["each", "at_once"])
 @pytest.mark.parametrize("fmt", G.FORMATS, ids=G.IDS)
-def test_generation_under_a_shared_prefix(fmt):
+def test_generation_under_a_shared_prefix(fmt, at_once, monkeypatch):
     """Places of the batch that are free at first, join and leave again; each step appends for those that are there."""
+    monkeypatch.setattr(Shared, "at_once", at_once)
     x = Shared(fmt, 100, [-1, 3, -1, 0, 20], 6, 2, 64, 16, seed=21, extra=3)
     dev, page = x.pool.dev, 16
     spare = [p for p in range(x.pool.pages) if p not in set(x.prefix_pages) and p not in set(x.table.reshape(-1))]
@@ -167,12 +169,14 @@ def kinds(fmt, lens, seed, qspread=1.0):
     # The first sequence's first two pages as a prefix that all have, those of the others gone.
     own = [max(n - 2 * page, 0) for n in lens]
     rest = to(dev, np.concatenate((x.table[:, 2:], np.full((b, 2), -1)), 1))
-    prefix = to(dev, x.table[0, :2])
-    out.append(("shared", lambda **kw: B.attn_shared(*args(), prefix, to(dev, [min(lens[0], 2 * page)]), rest, to(dev, own), lse=True, **kw)))
+    shared = lambda prefix, **kw: B.attn_shared(*args(), to(dev, prefix), to(dev, [min(lens[0], 2 * page)]), rest,  # noqa: E731
+                                                to(dev, own), lse=True, **kw)
+    out.append(("shared", lambda **kw: shared(x.table[0, :2], **kw)))
+    out.append(("shared at once", lambda **kw: shared(G.with_room(x.table[0, :2], fmt, b, 4, 2, 64, page), **kw)))
     whole = [x.pool.slots(x.table[i], n)[0] for i, n in enumerate(lens)]
     first = x.pool.slots(x.table[0, :2], lens[0])[0]
     split = [np.concatenate((first, x.pool.slots(x.table[i, 2:], own[i])[0])) for i in range(b)]
-    return x, [(name, call, split if name == "shared" else whole) for name, call in out]
+    return x, [(name, call, split if name.startswith("shared") else whole) for name, call in out]
 
 
 @pytest.mark.parametrize("fmt", G.FORMATS, ids=G.IDS)
@@ -349,8 +353,10 @@ def test_offsets_past_32_bits(fmt):
     pool.k, pool.v = R.stored(k.float().numpy(), fmt), R.stored(v.float().numpy(), fmt)
     q = rows(1, 2 * hk, d, 3)
     args = (q.to(dev), cache)
-    out, lse = B.attn_shared(*args, to(dev, ids[:2]), to(dev, [2 * page]), to(dev, ids[None, 2:]), to(dev, [n - 2 * page]), lse=True)
-    G.check_rows(pool, q, [j], out, lse, what="shared")
+    for front in (ids[:2], G.with_room(ids[:2], fmt, 2, 2 * hk, hk, d, page)):
+        out, lse = B.attn_shared(q.expand(2, -1, -1).contiguous().to(dev), cache, to(dev, front), to(dev, [2 * page]),
+                                 to(dev, np.stack((ids[2:], ids[2:]))), to(dev, [n - 2 * page] * 2), lse=True)
+        G.check_rows(pool, q.expand(2, -1, -1), [j, j], out, lse, what="shared")
     out, lse = B.attn_decode(*args, to(dev, np.broadcast_to(ids, (1, hk, 4))), to(dev, [n]), lse=True)
     G.check_rows(pool, q, [j], out, lse, what="heads")
     out, lse, w = B.attn_weigh(*args, to(dev, ids[None]), to(dev, [n]), None, 0.0, torch.empty(1, hk, 4, device=dev), lse=True)
@@ -459,9 +465,10 @@ def test_most_heads(hq, hk):
     assert np.array_equal(chosen.cpu().numpy(), want)
     G.check_rows(x.pool, x.q, [[x.pool.slots(want[0, h], tokens.item())[0] for h in range(hk)]],
                  *B.attn_decode(x.q.to(x.dev), x.pool.cache, chosen, tokens, lse=True), what="heads")
-    out, lse = B.attn_shared(x.q.to(x.dev), x.pool.cache, to(x.dev, x.table[0, :2]), to(x.dev, [32]), to(x.dev, x.table[:, 2:]),
-                             to(x.dev, [18]), lse=True)
-    G.check_rows(x.pool, x.q, [x.pool.slots(x.table[0], 50)[0]], out, lse, what="shared")
+    for front in (x.table[0, :2], G.with_room(x.table[0, :2], x.pool.fmt, 1, hq, hk, 16, 16)):
+        out, lse = B.attn_shared(x.q.to(x.dev), x.pool.cache, to(x.dev, front), to(x.dev, [32]), to(x.dev, x.table[:, 2:]),
+                                 to(x.dev, [18]), lse=True)
+        G.check_rows(x.pool, x.q, [x.pool.slots(x.table[0], 50)[0]], out, lse, what="shared")
 
 
 # ---- streams, graphs, workspaces ----------------------------------------------------------------------
@@ -473,17 +480,18 @@ def chain_of(seed=31):
     bounds = torch.zeros(x.pool.pages, 2, 2, 128, dtype=torch.bfloat16, device=dev)
     listed = list(x.table.reshape(-1)) + [p for p in range(x.pool.pages) if p not in x.table]
     inputs = [x.pool.cache.pool, x.q.to(dev), to(dev, x.table), to(dev, x.lens), torch.from_numpy(x.w).to(dev), bounds,
-              to(dev, [65]), to(dev, listed), torch.empty(3, 2, x.table.shape[1], device=dev)]
+              to(dev, [65]), to(dev, G.with_room(x.table[0, :2], x.pool.fmt, 3, 10, 2, 128, 64)), to(dev, listed), torch.empty(3, 2, x.table.shape[1], device=dev)]
 
-    def chain(stream, pool, q, table, seq, w, bounds, one, ids, w2):
+    def chain(stream, pool, q, table, seq, w, bounds, one, front, ids, w2):
         cache = B.KvCache(x.pool.pages, 64, 2, 128, x.pool.fmt, device=dev, pool=pool)
         kw = dict(stream=stream)
         B.kv_bounds(cache, ids, bounds, **kw)
         chosen, tokens = B.kv_select(q, cache, bounds, table, seq, 7, **kw)
         first = B.attn_decode(q, cache, chosen, tokens, lse=True, **kw)
         o, lse, w2 = B.attn_weigh(q, cache, table, seq, w, 0.5, w2, lse=True, **kw)
-        shared = B.attn_shared(q, cache, ids[:2], one, table, seq, lse=True, **kw)
-        return (bounds, chosen, tokens, *first, o, lse, w2, *shared, *B.kv_evict(w2, table, seq, 64, 9, 1, 2, **kw))
+        shared = B.attn_shared(q, cache, front, one, table, seq, lse=True, **kw)
+        by_each = B.attn_shared(q, cache, ids[:2], one, table, seq, lse=True, **kw)
+        return (bounds, chosen, tokens, *first, o, lse, w2, *shared, *by_each, *B.kv_evict(w2, table, seq, 64, 9, 1, 2, **kw))
 
     return chain, inputs
 
@@ -564,7 +572,9 @@ def test_prepared_under_capture():
     bounds = B.kv_bounds(cache, to(dev, x.table.reshape(-1)))
     many = to(dev, np.tile(x.table[:1, :40], (1, 8)))
     w, w2 = torch.from_numpy(x.w).to(dev), torch.empty(3, 2, x.table.shape[1], device=dev)
+    front = to(dev, G.with_room(x.table[0, :9], x.pool.fmt, 3, 10, 2, 128, 64))
     make = [lambda: B.attn_shared_prepared(q, cache, table[0, :9], to_one, table, seq, lse=True),
+            lambda: B.attn_shared_prepared(q, cache, front, to_one, table, seq, lse=True),
             lambda: B.kv_select_prepared(q[:1], cache, bounds, many, long, 9),
             lambda: B.attn_weigh_prepared(q, cache, table, seq, w, 0.5, w2, lse=True)]
     to_one, long = to(dev, [500]), to(dev, [320 * 64 - 3])

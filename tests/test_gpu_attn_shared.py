@@ -11,6 +11,8 @@ pytestmark = pytest.mark.gpu
 
 
 class Shared:
+    at_once = False       # whether the prefix's table has room for a prefix that is read for all sequences at once
+
     def __init__(self, fmt, prefix, lens, hq, hk, d, page, seed=0, scales=(1.0, 1.0), qspread=1.0, extra=0):
         dev = device()
         rng = np.random.default_rng(seed)
@@ -30,6 +32,8 @@ class Shared:
             slots.append(self.table[i, np.arange(max(n, 0)) // page].astype(np.int64) * page + np.arange(max(n, 0)) % page)
         self.pool = G.Pool(dev, fmt, pages, page, hk, d, seed, scales, slots=np.concatenate(slots))
         self.q = G.queries(b, hq, d, seed + 1, qspread)
+        if self.at_once:
+            self.prefix_pages = G.with_room(self.prefix_pages, fmt, b, hq, hk, d, page)
         self.args = [self.q.to(dev), self.pool.cache, torch.from_numpy(self.prefix_pages).to(dev),
                      torch.tensor([prefix], dtype=torch.int32, device=dev), torch.from_numpy(self.table).to(dev),
                      torch.tensor(self.lens, dtype=torch.int32, device=dev)]
@@ -43,6 +47,11 @@ class Shared:
         out, lse = B.attn_shared(*self.args, lse=True, **kw)
         G.check_rows(self.pool, self.q, self.lists(), out, lse, kw.get("scale"), what)
         return out, lse
+
+
+@pytest.fixture(autouse=True, params=[False, True], ids=["each", "at_once"])
+def at_once(request, monkeypatch):
+    monkeypatch.setattr(Shared, "at_once", request.param)
 
 
 @pytest.mark.parametrize("fmt", G.FORMATS, ids=G.IDS)
@@ -117,7 +126,7 @@ def test_evicted_pages(fmt):
 def test_the_prefix_may_be_a_sequences_own_too(fmt):
     """Pages listed twice: the prefix read twice by one sequence, its tokens counting twice."""
     x = Shared(fmt, 64, [64, 10], 4, 2, 64, 32, seed=6)
-    x.table[0, :2] = x.prefix_pages
+    x.table[0, :2] = x.prefix_pages[:2]
     x.args[4] = torch.from_numpy(x.table).to(x.pool.dev)
     x.check()
 
@@ -136,6 +145,7 @@ def test_long_prefix_of_many_rows(fmt):
     Shared(fmt, 20011, [3, 0, 129], 8, 2, 64, 64, seed=8).check()
     Shared(fmt, 40, [i % 3 for i in range(300)], 12, 3, 64, 16, seed=9).check()
     Shared(fmt, 1500, [i % 3 for i in range(64)], 15, 3, 128, 16, seed=10).check()
+    Shared(fmt, 700, [i % 40 for i in range(9)], 160, 4, 64, 32, seed=10).check()
 
 
 @pytest.mark.parametrize("fmt", G.FORMATS, ids=G.IDS)
