@@ -9,8 +9,8 @@
 // Sums of sixteen tokens are 4 bytes a row, for 16 * 2 * head_dim values of the cache; the second launch finds them in the L2
 // and the last-level cache.
 //
-// Bound as attn_kernel is; what weighing adds is its 5 us: 32 users of 8192 NVFP4 tokens 40 us, 35 of them attention's
-// (151 MB, 4.3 TB/s); one of 131,072 34 us, 29 of them attention's.
+// Bound as attn_kernel is; what weighing adds is its 5 us and up to 3 us of the pass: 32 users of up to 8192 NVFP4 tokens 38 us
+// (152 MB, 4.0 TB/s), the attention alone 35; one of 65,536 E4M3 tokens 34 us (135 MB, 4.0 TB/s), the attention alone 29.
 #include "attn_kernel.h"
 
 namespace nvfp4 {

@@ -8,9 +8,10 @@
 // joins them row by row.
 //
 // Bound by the vector units, which dequantise and exponentiate: 32 users of 40 heads under 32,768 NVFP4 tokens
-// 57 us, of which 46 for the prefix (21.6 Gflop; 48 MB), 6 for 200 tokens of each user and 5 for the join; 200 under 8192
-// bf16 tokens 80 us, 65 for the prefix (33.8 Gflop).  Few rows are bound by the bytes: 7 users of 256-wide heads
-// under 50,001 E4M3 tokens 43 us, 25 for the prefix (105 MB, 4.2 TB/s).
+// 55 us, of which 45 for the prefix (21.6 Gflop; 48 MB), 9 for up to 512 tokens of each user and 5 for the join; 200 under 8192
+// bf16 tokens 79 us, 64 for the prefix (33.8 Gflop), 17 and 7.  Few rows are bound by the bytes: 7 users of 256-wide heads
+// under 50,001 E4M3 tokens 41 us, 24 for the prefix (105 MB, 4.4 TB/s).
+// (Two tiles in flight a wavefront instead of one gained nothing: 54.4 us against 55.1, 64-wide E4M3 heads 42.5 against 40.8.)
 //
 // The tiles and operands are those of attn_kernel.h.  Here a wavefront holds RT tiles of sixteen rows: one
 // 32-token tile of the cache is read, and dequantised, once for 16 RT rows.  The wavefronts of a
@@ -336,10 +337,11 @@ struct JoinParams {
 };
 
 // Each row by THREADS threads: its quads of values times as many runs of its pieces.  A run's pieces are read kPieces at a
-// time and added in order, the runs after one another.
+// time and added in order, the runs after one another.  (A workgroup reads 64 pieces or so at once: 7 users of 256-wide heads under
+// 50,001 E4M3 tokens 40.4 us against 42.6 with sixteen of them, 41.2 with 32.)
 template <int DP, int THREADS>
 __global__ __launch_bounds__(256) void join_kernel(const JoinParams a) {
-  constexpr int kQuads = DP / 4, kRuns = THREADS / kQuads, kPieces = 4, kRowsHere = 256 / THREADS;
+  constexpr int kQuads = DP / 4, kRuns = THREADS / kQuads, kPieces = THREADS == 256 ? DP / 16 : 4, kRowsHere = 256 / THREADS;
   __shared__ float s_ml[kRowsHere][kRuns][2];
   __shared__ f32x4 s_o[kRowsHere][kRuns][kQuads];
   const int t = threadIdx.x % THREADS, at = threadIdx.x / THREADS, run = t / kQuads, d = 4 * (t - run * kQuads);

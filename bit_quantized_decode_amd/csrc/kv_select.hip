@@ -14,7 +14,7 @@
 // keys that agree are all taken or all of one kind.  Each thread holds a run of consecutive keys in registers; more
 // keys than that stay in memory and are read in each step.
 //
-// What bounds them is latency where little is to be done: one user's choice of 128 pages out of 2048 for each of 8 kv
+// What bounds them is latency where little is to be done: one user's choice of 64 pages out of 2048 for each of 8 kv
 // heads (8.4 MB of bounds) takes 16 us, of which the launch 3, the scores 5, the way to the last workgroup of a pair 4 and
 // choosing 4; 256 pages of 32 users are evicted in 8 us, 8192 of one in 35 (keys 9, choosing 11, places and outputs 11).
 // Many scores are bound by fp64 arithmetic: 32 users of up to 512 pages and 8 kv heads of five rows 27 us, each row 3 us of it.
