@@ -15,9 +15,9 @@
 // keys than that stay in memory and are read in each step.
 //
 // What bounds them is latency where little is to be done: one user's choice of 64 pages out of 2048 for each of 8 kv
-// heads (8.4 MB of bounds) takes 16 us, of which the launch 3, the scores 5, the way to the last workgroup of a pair 4 and
+// heads (8.4 MB of bounds) takes 15 us, of which the launch 3, the scores 4, the way to the last workgroup of a pair 4 and
 // choosing 4; 256 pages of 32 users are evicted in 8 us, 8192 of one in 35 (keys 9, choosing 11, places and outputs 11).
-// Many scores are bound by fp64 arithmetic: 32 users of up to 512 pages and 8 kv heads of five rows 27 us, each row 3 us of it.
+// Many scores are bound by fp64 arithmetic: 32 users of up to 512 pages and 8 kv heads of five rows 22 us, 150 of 500 pages 77 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -221,7 +221,6 @@ __device__ __forceinline__ bool is_chosen(u64 k, int i, const Chosen& c, int end
 // ---- selection for attention --------------------------------------------------
 
 constexpr int kThreads = 256;
-constexpr int kStage = 16;             // query rows in LDS at a time
 constexpr int kCounters = 1024;        // (sequence, kv head)s whose scores may be cut over several workgroups
 
 constexpr int kSelectFew = 4, kSelectMany = 16;  // keys a thread holds: of tables of up to 1024 and 4096 pages
@@ -233,19 +232,32 @@ struct SelectParams {
   int chunk, shares;                   // pages of a workgroup's share; shares of a table
 };
 
-// Sum over sixteen lanes, the same in each.
+// v of another lane of the sixteen.
 template <int CTRL>
-__device__ __forceinline__ double add_partner(double v) {
+__device__ __forceinline__ double partner(double v) {
   const u64 u = (u64)__double_as_longlong(v);
   const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, 0xf, 0xf, true);
   const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, 0xf, 0xf, true);
-  return v + __longlong_as_double((long long)((u64)hi << 32 | lo));
+  return __longlong_as_double((long long)((u64)hi << 32 | lo));
 }
-__device__ __forceinline__ double sum16(double v) {
-  v = add_partner<0xb1>(v);   // the neighbour, the other pair, the other four mirrored, the other eight mirrored
-  v = add_partner<0x4e>(v);
-  v = add_partner<0x141>(v);
-  return add_partner<0x140>(v);
+// Sums over sixteen lanes of N values: lane j is left with value j % N's.  Each exchange halves what a lane keeps, the last
+// ones (eight and four lanes round) add what is left.
+template <int N>
+__device__ __forceinline__ double sums16(const double (&v)[N], int j) {
+  static_assert(N == 2 || N == 4, "pages at once");
+  double a;
+  if constexpr (N == 4) {
+    const bool two = j & 2, one = j & 1;
+    const double x = (two ? v[2] : v[0]) + partner<0x4e>(two ? v[0] : v[2]);
+    const double y = (two ? v[3] : v[1]) + partner<0x4e>(two ? v[1] : v[3]);
+    a = (one ? y : x) + partner<0xb1>(one ? x : y);
+  } else {
+    const bool one = j & 1;
+    a = (one ? v[1] : v[0]) + partner<0xb1>(one ? v[0] : v[1]);
+    a += partner<0x4e>(a);
+  }
+  a += partner<0x128>(a);
+  return a + partner<0x124>(a);
 }
 
 // CUT: a table's pages are scored by several workgroups, the last of which to arrive selects.
@@ -253,8 +265,11 @@ template <int DB, bool CUT, int PER>
 __global__ __launch_bounds__(kThreads) void select_kernel(const SelectParams p) {
   constexpr int kUnits = 2 * DB;       // pairs of channels that a lane holds of a page's bounds
   constexpr int kAhead = DB <= 2 ? 4 : 2;  // pages of a sixteen of lanes whose bounds are read at once
+  // Heads of up to 128: a query's values in LDS twice, see below.
+  constexpr bool kSplit = DB <= 2;
+  constexpr int kParts = kSplit ? 2 : 1, kStage = 16 / kParts;  // (query rows in LDS at a time)
   const KvSelectLaunch& a = p.a;
-  __shared__ double s_q[kStage][kUnits][16][2];
+  __shared__ double s_q[kStage][kUnits][16][2 * kParts];
   __shared__ union {
     u64 keys[CUT ? 1 : kThreads * PER];
     int list[kThreads * PER];
@@ -288,10 +303,17 @@ __global__ __launch_bounds__(kThreads) void select_kernel(const SelectParams p) 
       const int rows = min(a.group - g0, kStage);
       __syncthreads();
       for (int e = tid; e < rows * kUnits * 32; e += kThreads) {
-        const int r = e / (kUnits * 32), x = e - r * (kUnits * 32);   // of a row: [unit][lane][2]
+        const int r = e / (kUnits * 32), x = e - r * (kUnits * 32);   // of a row: [unit][lane][channel]
         const int d = (x >> 1 & 15) * (4 * DB) + 2 * (x >> 5) + (x & 1);
         const uint16_t v = d < a.head_dim ? a.q[(int64_t)b * a.ldq + (int64_t)(head * a.group + g0 + r) * a.head_dim + d] : 0;
-        (&s_q[r][0][0][0])[x] = (double)bf16_lo(v);
+        const double q = (double)bf16_lo(v);
+        double* to = &s_q[r][0][0][0] + kParts * x;
+        if constexpr (kSplit) {
+          to[0] = q < 0.0 ? 0.0 : q;
+          to[1] = q < 0.0 ? q : 0.0;
+        } else {
+          to[0] = q;
+        }
       }
       __syncthreads();
       // Each sixteen lanes take a page: kAhead of them in flight.
@@ -317,49 +339,64 @@ __global__ __launch_bounds__(kThreads) void select_kernel(const SelectParams p) 
             }
           }
         }
-        // Two pages at a time: their sums fill each other's waits.
+        double low[kAhead][2 * kUnits], high[kAhead][2 * kUnits];
+        u16x2 largest{0, 0};            // magnitudes: finite below 0x7f80
 #pragma unroll
-        for (int k = 0; k < kAhead; k += 2) {
-          double low[2][2 * kUnits], high[2][2 * kUnits];
+        for (int k = 0; k < kAhead; ++k)
 #pragma unroll
-          for (int m = 0; m < 2; ++m)
+          for (int u = 0; u < DB; ++u) {
+            const uint32_t w[4] = {l[k][u].x, l[k][u].y, h[k][u].x, h[k][u].y};
 #pragma unroll
-            for (int u = 0; u < DB; ++u) {
-              const uint2 lu = l[k + m][u], hu = h[k + m][u];
-              low[m][4 * u] = bf16_lo(lu.x), low[m][4 * u + 1] = bf16_hi(lu.x);
-              low[m][4 * u + 2] = bf16_lo(lu.y), low[m][4 * u + 3] = bf16_hi(lu.y);
-              high[m][4 * u] = bf16_lo(hu.x), high[m][4 * u + 1] = bf16_hi(hu.x);
-              high[m][4 * u + 2] = bf16_lo(hu.y), high[m][4 * u + 3] = bf16_hi(hu.y);
+            for (int i = 0; i < 4; ++i) {
+              double* to = i < 2 ? &low[k][4 * u + 2 * i] : &high[k][4 * u + 2 * i - 4];
+              to[0] = bf16_lo(w[i]);
+              to[1] = bf16_hi(w[i]);
+              if constexpr (kSplit) largest = __builtin_elementwise_max(largest, __builtin_bit_cast(u16x2, w[i] & 0x7fff7fffu));
             }
-          double best[2] = {-__builtin_inf(), -__builtin_inf()};
-          bool nan[2] = {false, false};
+          }
+        // For finite bounds both products are formed, of q's part below 0 with lo and of the rest with hi, one of which is 0: a
+        // select costs two instructions, a product one.  (32 users of 1000 pages of five rows 40 us against 46, of 500 pages
+        // of eight rows 31 against 36; one row, for which four pages' registers at once are too many, 19 against 17.  256-wide
+        // heads, whose parts LDS takes longer to read than selects take: 40 against 35.)
+        double best = -__builtin_inf();
+        bool nan = false;
+        const auto score = [&](auto both) {
           for (int r = 0; r < rows; ++r) {
-            double sum[2] = {0.0, 0.0};
+            double sum[kAhead];
 #pragma unroll
-            for (int u = 0; u < kUnits; ++u) {
-              const double q0 = s_q[r][u][j][0], q1 = s_q[r][u][j][1];
+            for (int k = 0; k < kAhead; ++k) sum[k] = 0.0;
 #pragma unroll
-              for (int m = 0; m < 2; ++m) {
-                sum[m] += q0 * (q0 < 0.0 ? low[m][2 * u] : high[m][2 * u]);
-                sum[m] += q1 * (q1 < 0.0 ? low[m][2 * u + 1] : high[m][2 * u + 1]);
+            for (int u = 0; u < kUnits; ++u)
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                const double up = s_q[r][u][j][kParts * c], down = s_q[r][u][j][kParts * c + kParts - 1];
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                  const double lo = low[k][2 * u + c], hi = high[k][2 * u + c];
+                  if constexpr (decltype(both)::value) {
+                    sum[k] = __builtin_fma(up, hi, sum[k]);
+                    sum[k] = __builtin_fma(down, lo, sum[k]);
+                  } else {
+                    sum[k] = down < 0.0 ? __builtin_fma(down, lo, sum[k]) : __builtin_fma(up, hi, sum[k]);
+                  }
+                }
               }
-            }
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {
-              const double score = sum16(sum[m]);
-              nan[m] |= score != score;
-              best[m] = fmax(best[m], score);
-            }
+            const double all = sums16(sum, j);
+            nan |= all != all;
+            best = fmax(best, all);
           }
+        };
+        const bool finite = !__any(largest[0] >= 0x7f80 || largest[1] >= 0x7f80);
+        if (kSplit && finite) score(std::bool_constant<kSplit>());
+        else score(std::false_type());
+        const int k = j % kAhead, i = i0 + k * kAtOnce;
+        if (j < kAhead && i < end) {
+          int mine = page[0];
 #pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            const int i = i0 + (k + m) * kAtOnce;
-            if (j == 0 && i < end) {
-              const u64 key = !there(page[k + m]) ? 0 : nan[m] ? ~0ull : key_of(best[m]);
-              if (in_lds) s_keys[i] = g0 > 0 ? max(s_keys[i], key) : key;
-              else store_key(memory + i, g0 > 0 ? max(load_key(memory + i), key) : key);
-            }
-          }
+          for (int m = 1; m < kAhead; ++m) mine = k == m ? page[m] : mine;
+          const u64 key = !there(mine) ? 0 : nan ? ~0ull : key_of(best);
+          if (in_lds) s_keys[i] = g0 > 0 ? max(s_keys[i], key) : key;
+          else store_key(memory + i, g0 > 0 ? max(load_key(memory + i), key) : key);
         }
       }
     }

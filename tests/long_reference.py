@@ -123,8 +123,8 @@ def selection(q, bounds, table, lens, budget, page, pages):
             for j in there:
                 lo, hi = bounds[table[i, j], h].astype(np.longdouble)
                 s = np.where(qh < 0, qh * lo, qh * hi).sum(-1)
-                score[j] = np.inf if np.isnan(s).any() else float(s.max())
-            best = sorted(sorted(there, key=lambda j: (-score[j], j))[:budget - 1])
+                score[j] = (0, 0.0) if np.isnan(s).any() else (1, -float(s.max()))   # a NaN above everything
+            best = sorted(sorted(there, key=lambda j: (*score[j], j))[:budget - 1])
             chosen = [table[i, j] for j in best] + [table[i, blocks - 1] if 0 <= table[i, blocks - 1] < pages else -1]
             out[i, h, :len(chosen)] = chosen
             tokens[i] = (len(chosen) - 1) * page + (n - 1) % page + 1

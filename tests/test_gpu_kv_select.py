@@ -181,6 +181,28 @@ def test_infinite_and_nan_scores():
     assert got.cpu().tolist() == [[[1, 3]]]
 
 
+@pytest.mark.parametrize("d", [16, 128, 192, 256])
+@pytest.mark.parametrize("rows", [1, 5, 20])
+def test_bounds_that_are_not_finite_beside_others(d, rows):
+    """Infinities on the side that a query's sign does not ask for do not count (zeros ask for hi), those on the other do."""
+    dev, page, pages, n = device(), 16, 300, 200
+    rng = np.random.default_rng(d + rows)
+    cache = B.KvCache(pages, page, 1, d, B.NVFP4_KV_BF16, device=dev)
+    bounds = random_bounds(rng, pages, 1, d)
+    q = G.queries(2, rows, d, seed=d)
+    q[:, :, 3], q[:, :, 4], q[:, :, 5], q[:, :, 6] = 1.0, -1.0, 0.0, -0.0
+    inf = float("inf")
+    for p, (channel, side, value) in zip(range(0, 300, 7), [(c, s, v) for c in (3, 4, 5, 6) for s in (0, 1) for v in (inf, -inf, float("nan"))]):
+        bounds[p, 0, side, channel] = value
+    table = np.stack([rng.permutation(pages)[:n] for _ in range(2)])
+    lens = [n * page, 150 * page + 3]
+    for budget in (2, 9, 30, 150):
+        got, tokens = B.kv_select(q.to(dev), cache, bounds.to(dev), to(dev, table), to(dev, lens), budget)
+        with np.errstate(invalid="ignore"):
+            want, want_tokens = G.selection(q, bounds.double().numpy(), table, lens, budget, page, pages)
+        assert np.array_equal(got.cpu().numpy(), want) and np.array_equal(tokens.cpu().numpy(), want_tokens), budget
+
+
 def test_calls_of_all_kinds():
     """Repeated, prepared, on another stream, captured with lengths that change, outputs given, workspaces shared: same results,
     counters left zero."""
