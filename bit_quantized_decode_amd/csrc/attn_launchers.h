@@ -122,6 +122,8 @@ struct KvBoundsLaunch {
 };
 hipError_t launch_kv_bounds(const KvBoundsLaunch& a, hipStream_t s);
 
+constexpr size_t kSelectCounterBytes = 4096;   // of the workspace, zero between calls
+
 struct KvSelectLaunch {
   int64_t batch;
   int32_t heads, head_dim, group, pages, page_size;

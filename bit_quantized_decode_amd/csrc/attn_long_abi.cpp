@@ -13,6 +13,7 @@ namespace {
 using namespace nvfp4;
 
 constexpr int64_t kMaxBatch = 65536;
+static_assert(NVFP4_SELECT_COUNTER_BYTES == kSelectCounterBytes, "counters");
 
 int check_batch(int64_t batch) {
   if (batch < 0 || batch > kMaxBatch) return fail(NVFP4_ERR_SHAPE, "batch=%lld must be in [0, 65536]", (long long)batch);

@@ -221,7 +221,7 @@ __device__ __forceinline__ bool is_chosen(u64 k, int i, const Chosen& c, int end
 // ---- selection for attention --------------------------------------------------
 
 constexpr int kThreads = 256;
-constexpr int kCounters = 1024;        // (sequence, kv head)s whose scores may be cut over several workgroups
+constexpr int kCounters = kSelectCounterBytes / sizeof(unsigned);  // (sequence, kv head)s whose scores may be cut over workgroups
 
 constexpr int kSelectFew = 4, kSelectMany = 16;  // keys a thread holds: of tables of up to 1024 and 4096 pages
 

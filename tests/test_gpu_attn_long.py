@@ -1,4 +1,6 @@
 """GPU parity of reading less of a long cache: the operators together as a program uses them, and what they share at the edges."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -596,6 +598,50 @@ def test_prepared_under_capture():
             torch.cuda.synchronize()
             assert all(torch.equal(a, b) for a, b in zip(out, want)), step
         assert not ws[:1024].any()
+
+
+def test_strided_rows():
+    """Queries inside QKV rows and outputs inside wider rows, whose other columns stay as they were."""
+    x = Weighed(B.NVFP4_KV_E4M3, [500, 40, 0], 6, 2, 64, 32, seed=34)
+    dev, (q, cache, table, seq) = x.dev, x.args()
+    wide = torch.full((3, 10, 64), 7.0, dtype=torch.bfloat16, device=dev)
+    wide[:, 2:8] = q
+    inside = wide[:, 2:8]
+    bounds = B.kv_bounds(cache, to(dev, x.table.reshape(-1)))
+    bounds[~bounds.isfinite()] = 0.0                     # (of places that were not written)
+    chosen, tokens = B.kv_select(q, cache, bounds, table, seq, 4)
+    assert all(torch.equal(a, b) for a, b in zip(B.kv_select(inside, cache, bounds, table, seq, 4), (chosen, tokens)))
+    w = torch.from_numpy(x.w).to(dev)
+    calls = [lambda q, **kw: B.attn_decode(q, cache, chosen, tokens, lse=True, **kw),
+             lambda q, **kw: B.attn_weigh(q, cache, table, seq, w, 0.5, torch.empty_like(w), lse=True, **kw)]
+    for call in calls:
+        want = [t.clone() for t in call(q)]
+        out = torch.full((3, 9, 64), 5.0, dtype=torch.bfloat16, device=dev)
+        got = call(inside, out=out[:, 1:7])
+        assert all(torch.equal(a, b) for a, b in zip(got, want)) and torch.equal(out[:, 1:7], want[0])
+        assert (out[:, 0] == 5).all() and (out[:, 7:] == 5).all()
+
+
+def test_eviction_without_freed_pages_and_weights():
+    """The C call with neither: table and lengths alone; and with each of them alone."""
+    dev, width, budget = device(), 40, 7
+    rng = np.random.default_rng(35)
+    weights = rng.exponential(size=(3, 2, width)).astype(np.float32)
+    table, lens = rng.permutation(3 * width).reshape(3, width), [width * 16, 100, 0]
+    want = G.eviction(weights, table, lens, 16, budget, 1, 2)
+    w, t, n = torch.from_numpy(weights).to(dev), to(dev, table), to(dev, lens)
+    for with_freed in (False, True):
+        for with_weights in (False, True):
+            got = [torch.full(s, 7, dtype=d, device=dev) for s, d in (((3, budget), torch.int32), ((3,), torch.int32),
+                                                                      ((3, width), torch.int32), ((3, 2, budget), torch.float32))]
+            a = B.KvEvictArgs(batch=3, kv_heads=2, page_size=16, weights=w.data_ptr(), page_table=t.data_ptr(), table_width=width,
+                              seq_lens=n.data_ptr(), budget=budget, sink=1, recent=2, table_out=got[0].data_ptr(),
+                              lens_out=got[1].data_ptr(), freed=got[2].data_ptr() if with_freed else None,
+                              weights_out=got[3].data_ptr() if with_weights else None)
+            B.check(B.lib().nvfp4_kv_evict(ctypes.byref(a), torch.cuda.current_stream().cuda_stream))
+            torch.cuda.synchronize()
+            for i, there in enumerate((True, True, with_freed, with_weights)):
+                assert np.array_equal(got[i].cpu().numpy(), want[i]) if there else (got[i] == 7).all(), i
 
 
 def test_a_stream_of_another_device():
