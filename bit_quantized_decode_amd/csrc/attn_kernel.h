@@ -377,6 +377,16 @@ __device__ __forceinline__ float rounded_product(float a, float b) {
 
 __device__ __forceinline__ float lane_xor(float v, int off) { return __shfl_xor(v, off); }
 
+// Sums of a and b over the lanes of a column (16 h + q for all h): a's where h is even, b's where it is odd.
+__device__ __forceinline__ float half_sums(float a, float b) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b), false, false);
+  const uint32_t r0 = r[0], r1 = r[1];
+  const uint32_t s = __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, r0) + __builtin_bit_cast(float, r1));
+  const auto t = __builtin_amdgcn_permlane32_swap(s, s, false, false);
+  const uint32_t t0 = t[0], t1 = t[1];
+  return __builtin_bit_cast(float, t0) + __builtin_bit_cast(float, t1);
+}
+
 // The largest term is set to 2^kOffset, and none passes 2^(kOffset + kSlack).  f16: 2^15;
 // terms under 2^-14 lose bits: one below 2^-25 of the largest is taken to within 2^-36 of that
 // (half of f16's last step, 2^-25, under the offset).  bf16 has fp32's range: no term passes 1,
@@ -845,10 +855,8 @@ __global__ __launch_bounds__(256 * waves_per_simd(FMT, DB), (waves_per_simd(FMT,
         sum += p[i];
       }
       if constexpr (MODE == kWeigh) {
-        // Lanes 16 h + q with h even keep the first sixteen tokens' sum, h odd the second's: two exchanges for both.
-        const float m0 = p[0] + p[1] + p[2] + p[3], m1 = p[4] + p[5] + p[6] + p[7];
-        float m = ((h & 1) ? m1 : m0) + lane_xor((h & 1) ? m0 : m1, 16);
-        m += lane_xor(m, 32);
+        // Lanes 16 h + q with h even keep the first sixteen tokens' sum, h odd the second's: two swaps of lanes for both.
+        const float m = half_sums(p[0] + p[1] + p[2] + p[3], p[4] + p[5] + p[6] + p[7]);
         const int at = (tok0 - sp.base) / kKvGroup + h;
         if (h < 2 && qn < rows && sp.base + at * kKvGroup < sp.end) mass[at * a.part_rows + qn] = __builtin_amdgcn_logf(m) + shift;
       }

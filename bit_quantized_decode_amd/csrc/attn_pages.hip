@@ -35,6 +35,7 @@ __global__ __launch_bounds__(256) void weigh_kernel(const WeighParams w) {
   if (unit >= (int64_t)a.batch * a.cache.heads) return;
   const int b = (int)(unit / a.cache.heads), head = (int)(unit - (int64_t)b * a.cache.heads);
   const int page = (int)(item - unit * a.table_width);
+  const float before = lane == 0 && w.decay != 0.0f ? w.weights[item] : 0.0f;  // (on its way while the sums are)
   const Span sp = span_of(a, a.lens[b]);
   // The page's tokens inside the span (offsets up to 2^30), as sixteens from the span's base on.
   const int from = max(page * a.cache.page_size, sp.begin), to = min((page + 1) * a.cache.page_size, sp.end);
@@ -66,7 +67,7 @@ __global__ __launch_bounds__(256) void weigh_kernel(const WeighParams w) {
   }
 #pragma unroll
   for (int off = LANES / 2; off >= 1; off >>= 1) sum += __shfl_xor(sum, off);
-  if (lane == 0) w.weights_out[item] = w.decay == 0.0f ? sum : w.decay * w.weights[item] + sum;
+  if (lane == 0) w.weights_out[item] = w.decay == 0.0f ? sum : w.decay * before + sum;
 }
 
 int64_t mass_groups_of(const AttnLaunch& a) {
