@@ -1056,7 +1056,8 @@ def attn_decode(q, cache, page_table, seq_lens, scale=None, window=0, out=None, 
     """Attention of one new token per sequence over the cache: q bf16 [batch][q_heads][head_dim], page_table int32
     [batch][pages], or [batch][kv_heads][pages] for pages of each kv head's own (as kv_select() gives them), seq_lens int32
     [batch] (with the new token), scale 1 / sqrt(head_dim) by default.  Returns out (bf16 like q), or (out, lse) if lse is
-    True or a float32 [batch][q_heads] tensor.  ws: a workspace, zeroed before its first use, that no other running call has."""
+    True or a float32 [batch][q_heads] tensor.  ws: a workspace, zeroed before its first use, that no other running call has; the
+    attentions below and kv_select() may have the same one, the calls of include/nvfp4.h not."""
     return _attn(q, cache, page_table, seq_lens, scale, window, out, lse, ws, stream, False)()
 
 

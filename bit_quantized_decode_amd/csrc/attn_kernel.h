@@ -72,7 +72,7 @@ constexpr int kLead = 3;
 // 13.0 / 12.8 us, 4 heads 14.8 / 13.5 / 13.3 / 14.3, 16 heads 16.6 / 17.4 / 21.5 / 26.5.)
 constexpr int kShareMinLog = 2, kShareMaxLog = 5, kPartsMinLog = 4, kPartsMaxLog = 6;
 constexpr int kJoinBatch = 12;             // parts that a thread of a join reads at once
-static_assert(kCus * 4 <= (int)kAttnCounterBytes, "one counter a workgroup");
+static_assert(kCus * 4 <= (int)kAttnCounterBytes && kAttnCounterBytes <= kCounterBytes, "one counter a workgroup");
 constexpr double kLog2e = 1.4426950408889634;
 constexpr float kLn2 = 0.6931471805599453f;
 // Of a grid made by grid_of().
@@ -1056,7 +1056,7 @@ inline void fill_params(const AttnLaunch& a, AttnParams& p) {
   p.out = a.out;
   p.lse = a.lse;
   p.counters = static_cast<unsigned*>(a.ws);
-  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + kAttnCounterBytes);
+  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + kCounterBytes);
   p.ldq = a.ldq;
   p.ldo = a.ldo;
   p.table_width = a.table_width;

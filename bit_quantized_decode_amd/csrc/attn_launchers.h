@@ -76,7 +76,11 @@ struct AttnLaunch {
   float* lse;              // nullptr: none
   void* ws;
 };
-constexpr size_t kAttnCounterBytes = 1024;  // one counter a workgroup
+constexpr size_t kAttnCounterBytes = 1024;     // one counter a workgroup
+constexpr size_t kSelectCounterBytes = 4096;   // one counter a (sequence, kv head) whose scores are cut
+// In front of every workspace of the attention side: the counters of attention and of selection, from its first byte on, zero
+// between calls of either.  What else a call keeps lies behind, so that one workspace serves both.
+constexpr size_t kCounterBytes = kSelectCounterBytes;
 // Whether the call's tiles can be numbered in 31 bits (at the longest lengths its table allows).
 bool attn_fits(const AttnLaunch& a);
 size_t attn_workspace_bytes(const AttnLaunch& a);
@@ -121,8 +125,6 @@ struct KvBoundsLaunch {
   uint16_t* bounds;        // [pages][heads][2][head_dim]
 };
 hipError_t launch_kv_bounds(const KvBoundsLaunch& a, hipStream_t s);
-
-constexpr size_t kSelectCounterBytes = 4096;   // of the workspace, zero between calls
 
 struct KvSelectLaunch {
   int64_t batch;

@@ -647,14 +647,14 @@ void select_launch(const SelectParams& p, bool cut, dim3 grid, hipStream_t s) {
 size_t kv_select_workspace_bytes(const KvSelectLaunch& a) {
   if (a.table_width <= a.budget) return 0;
   if (chunk_of(a) >= a.table_width && a.table_width <= kThreads * kSelectMany) return 0;
-  return kCounters * sizeof(unsigned) + (size_t)(a.batch * a.heads) * a.table_width * sizeof(u64);
+  return kCounterBytes + (size_t)(a.batch * a.heads) * a.table_width * sizeof(u64);
 }
 
 hipError_t launch_kv_select(const KvSelectLaunch& a, hipStream_t s) {
   SelectParams p;
   p.a = a;
   p.counters = static_cast<unsigned*>(a.ws);
-  p.keys = a.ws ? reinterpret_cast<u64*>(p.counters + kCounters) : nullptr;
+  p.keys = a.ws ? reinterpret_cast<u64*>(static_cast<uint8_t*>(a.ws) + kCounterBytes) : nullptr;
   const int64_t chunk = std::max<int64_t>(a.table_width <= a.budget ? a.table_width : chunk_of(a), 1);
   p.chunk = (int)chunk;
   const bool cut = chunk < a.table_width;

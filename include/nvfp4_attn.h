@@ -207,6 +207,9 @@ int nvfp4_kv_read(const nvfp4_kv_cache* cache /* host */, const int64_t* slots, 
  *
  * The workspace's first NVFP4_ATTN_COUNTER_BYTES must be zero before its first
  * use; every call leaves them zero.  Calls that share one must not overlap.
+ * One workspace may serve the attentions and selections of nvfp4_attn_long.h too,
+ * its first NVFP4_SELECT_COUNTER_BYTES zero before its first use; those of nvfp4.h
+ * are laid out otherwise and apart from it.
  * batch == 0 is a no-op.
  */
 #define NVFP4_ATTN_COUNTER_BYTES 1024

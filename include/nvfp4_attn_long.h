@@ -73,7 +73,8 @@ typedef struct nvfp4_kv_select_args {
   int64_t budget;           /* >= 1; budget * page_size <= 2^30 */
   int32_t* pages_out;       /* [batch][kv_heads][budget] */
   int32_t* lens_out;        /* [batch] */
-  void* workspace;          /* 16-byte aligned; its first NVFP4_SELECT_COUNTER_BYTES zero before its first use */
+  void* workspace;          /* 16-byte aligned; its first NVFP4_SELECT_COUNTER_BYTES zero before its first use, and left zero by
+                             * every call and by every attention: one workspace may serve both */
   size_t workspace_bytes;
 } nvfp4_kv_select_args;
 #define NVFP4_SELECT_COUNTER_BYTES 4096
