@@ -617,6 +617,12 @@ __global__ __launch_bounds__(THREADS) void evict_kernel(const EvictParams p) {
   }
   if (freed)
     for (int64_t i = gone_all + tid; i < a.table_width; i += THREADS) freed[i] = -1;
+  // The workspace's front, where other calls have their counters, held the first sequence's keys alone: it is left zero.
+  static_assert(kCounterBytes <= kEvictMany * kPerMany * sizeof(u64), "counters under one sequence's keys");
+  if (!held && b == 0) {
+    __syncthreads();
+    for (int i = tid; i < (int)(kCounterBytes / sizeof(u64)); i += THREADS) store_key(memory + i, 0);
+  }
 }
 
 // Pages of a workgroup's share: one workgroup a (sequence, kv head) where those fill the GPU or have no counter; else

@@ -115,7 +115,8 @@ int nvfp4_attn_weigh(const nvfp4_attn_weigh_args* args /* host */, void* stream)
  *   weights_out     the kept pages' weights at their new places, then 0 (or NULL);
  *   freed[b]        the ids of the pages dropped, in order, then -1 (or NULL).
  * Keys keep the rotary positions that they were turned by.  The outputs overlap no input.  The workspace needs no
- * initial contents. */
+ * initial contents; what was zero of its first NVFP4_SELECT_COUNTER_BYTES is so again after the call: an attention's or a
+ * selection's workspace may serve. */
 typedef struct nvfp4_kv_evict_args {
   int64_t batch;            /* 0..65536 */
   int64_t kv_heads;         /* 1..1024 */

@@ -1,4 +1,6 @@
 """One workspace for calls of every kind on the attention side, in turn."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -50,3 +52,32 @@ def test_attentions_and_selections_share_a_workspace(fmt):
             torch.cuda.synchronize()
             assert all(torch.equal(a, b) for a, b in zip(out, want)), (round, i)
             assert not ws[:B.NVFP4_SELECT_COUNTER_BYTES].any(), (round, i)
+
+
+@pytest.mark.parametrize("batch", [1, 5])
+def test_eviction_leaves_a_workspace_as_others_need_it(batch):
+    """Keys of tables beyond 8192 pages lie in the workspace: whatever it held, its front is zero afterwards, or as it was where
+    nothing needed keys there; attention and selection may have it next."""
+    dev, hk, width, page, budget = device(), 2, 9001, 16, 700
+    rng = np.random.default_rng(batch)
+    weights = torch.from_numpy(rng.exponential(size=(batch, hk, width)).astype(np.float32)).to(dev)
+    table = to(dev, rng.integers(0, 1 << 20, size=(batch, width)))
+    pool, q, other, seq, bounds = many_pairs(B.NVFP4_KV_NVFP4)
+    w = torch.zeros(16, 32, other.shape[1], device=dev)
+    attend = lambda **kw: B.attn_weigh(q, pool.cache, other, seq, None, 0.0, w, lse=True, **kw)  # noqa: E731
+    select = lambda **kw: B.kv_select(q, pool.cache, bounds, other, seq, 9, **kw)  # noqa: E731
+    want = [t.clone() for t in (*attend(), *select())]
+    ws = torch.zeros(64 << 20, dtype=torch.uint8, device=dev)
+    for longest in (width * page, 8192 * page, 40, width * page - 3):
+        lens = to(dev, [longest] + [rng.integers(0, width * page) for _ in range(batch - 1)])
+        ref = B.kv_evict(weights, table, lens, page, budget, 1, 2)
+        got = [torch.full_like(t, -7) for t in ref]
+        a = B.KvEvictArgs(batch=batch, kv_heads=hk, page_size=page, weights=weights.data_ptr(), page_table=table.data_ptr(),
+                          table_width=width, seq_lens=lens.data_ptr(), budget=budget, sink=1, recent=2, table_out=got[0].data_ptr(),
+                          lens_out=got[1].data_ptr(), freed=got[2].data_ptr(), weights_out=got[3].data_ptr(),
+                          workspace=ws.data_ptr(), workspace_bytes=ws.numel())
+        B.check(B.lib().nvfp4_kv_evict(ctypes.byref(a), torch.cuda.current_stream().cuda_stream))
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, ref)), longest
+        assert not ws[:B.NVFP4_SELECT_COUNTER_BYTES].any(), longest
+        assert all(torch.equal(x, y) for x, y in zip((*attend(ws=ws), *select(ws=ws)), want)), longest
