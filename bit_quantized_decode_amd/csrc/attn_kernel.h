@@ -120,18 +120,23 @@ __device__ __forceinline__ int run_of(const Cut& c, int place) {
 enum Mode {
   kPlain,
   kHeads,    // the page table is [batch][kv_heads][table_width]
-  kWeigh,    // the terms of every sixteen tokens are summed and kept, for the weights of pages
+  kWeigh,    // the terms of every sixteen tokens are summed and kept, and so are the rows' references and sums, for the weights of pages
   kRaw,      // rows are left as reference, sum and sums, for a later join
   kBehind    // each sequence's tokens come behind a prefix with a page table of its own
 };
 template <int MODE>
 struct ModeParams : AttnParams {};
 
-// kWeigh: log2 of the terms' sum over sixteen tokens, [unit][sixteen][part_rows], units
-// numbered by (sequence, kv head, row tile), sixteens from the span's base on.
+// kWeigh: sums of the terms of sixteen tokens and the references that they were formed under,
+// [unit][sixteen][part_rows], units numbered by (sequence, kv head, row tile), sixteens from the span's
+// base on; and each row's final reference and sum, [batch][q_heads].
+struct Mass {
+  float sum, ref;
+};
 template <>
 struct ModeParams<kWeigh> : AttnParams {
-  float* mass;
+  Mass* mass;
+  Mass* rows;
   int64_t groups;      // sixteens of a unit, at most
 };
 
@@ -472,6 +477,9 @@ __device__ __forceinline__ void write_row(const ModeParams<MODE>& a, int b, int 
     if (d == 0) *reinterpret_cast<f32x4*>(to) = f32x4{ref, l, 0.0f, 0.0f};
     *reinterpret_cast<f32x4*>(to + 4 + d) = acc;
   } else {
+    if constexpr (MODE == kWeigh) {
+      if (d == 0) a.rows[(int64_t)b * a.q_heads + qh] = Mass{l, ref};
+    }
     write_out(a, b, qh, d, ref, l, acc);
   }
 }
@@ -788,7 +796,7 @@ __global__ __launch_bounds__(256 * waves_per_simd(FMT, DB), (waves_per_simd(FMT,
     __builtin_amdgcn_sched_barrier(0);
     load_v<FMT, DB>(from, lane, t);
     __builtin_amdgcn_sched_barrier(0);
-    float* mass = nullptr;
+    Mass* mass = nullptr;
     if constexpr (MODE == kWeigh) mass = a.mass + ((int64_t)b * units_per_row + unit) * a.groups * a.part_rows;
     const float score_scale = query_scale<FMT>(qv, a.score_factor, a.score_exp);
 
@@ -858,7 +866,7 @@ __global__ __launch_bounds__(256 * waves_per_simd(FMT, DB), (waves_per_simd(FMT,
         // Lanes 16 h + q with h even keep the first sixteen tokens' sum, h odd the second's: two swaps of lanes for both.
         const float m = half_sums(p[0] + p[1] + p[2] + p[3], p[4] + p[5] + p[6] + p[7]);
         const int at = (tok0 - sp.base) / kKvGroup + h;
-        if (h < 2 && qn < rows && sp.base + at * kKvGroup < sp.end) mass[at * a.part_rows + qn] = __builtin_amdgcn_logf(m) + shift;
+        if (h < 2 && qn < rows && sp.base + at * kKvGroup < sp.end) mass[at * a.part_rows + qn] = Mass{m, shift};
       }
       uint32_t hi[4], lo[4];
       split_terms<FMT>(p, hi, lo);

@@ -2,12 +2,14 @@
 // attention that adds up the weight that each page has had (nvfp4_attn_weigh).
 //
 // Both are attn_kernel (attn_kernel.h).  The first looks its pages up in a table of its own for each kv head.
-// The second keeps the sum of the terms of every sixteen tokens, a byproduct of the pass over the cache: in log2, with
-// the row's reference in it, since that may still move.  A second launch, when the rows' lse is known, turns
-// the sums of a page into its weight:
-//   weight_i = sum over the group's rows r and the page's sixteens t of 2^(mass_rt - lse_r log2 e).
-// Sums of sixteen tokens are 4 bytes a row, for 16 * 2 * head_dim values of the cache; the second launch finds them in the L2
-// and the last-level cache.
+// The second keeps the sum m of the terms of every sixteen tokens, a byproduct of the pass over the cache, with the
+// reference s that they were formed under, since that may still move.  A second launch, when the rows' references R and
+// sums l are final, turns the sums of a page into its weight:
+//   weight_i = sum over the group's rows r and the page's sixteens t of m_rt 2^(s_rt - R_r) / l_r.
+// Both references are log2 of one scale, and s <= R: the exponent is a difference of numbers as they are, so that a row's
+// shares add up to 1 however large its scores.  (As one number, log2 m + s, against lse they were off by half steps of lse: 1e-4
+// at 1000, up to a factor of 2 at 2^20.)  Sums of sixteen tokens are 8 bytes a row, for 16 * 2 * head_dim values of the cache;
+// the second launch finds them in the L2 and the last-level cache.
 //
 // Bound as attn_kernel is; what weighing adds is its 5 us and up to 3 us of the pass: 32 users of up to 8192 NVFP4 tokens 38 us
 // (152 MB, 4.0 TB/s), the attention alone 35; one of 65,536 E4M3 tokens 34 us (135 MB, 4.0 TB/s), the attention alone 29.
@@ -18,7 +20,8 @@ namespace {
 
 struct WeighParams {
   AttnParams attn;
-  const float* mass;
+  const Mass* mass;
+  const Mass* rows;
   const float* weights;
   float* weights_out;
   int64_t groups;
@@ -43,24 +46,24 @@ __global__ __launch_bounds__(256) void weigh_kernel(const WeighParams w) {
   if (from < to) {
     const int first = (from - sp.base) / kKvGroup, n = (to - 1 - sp.base) / kKvGroup + 1 - first;
     for (int rt = 0; rt < a.row_tiles; ++rt) {
-      const float* mass = w.mass + ((unit * a.row_tiles + rt) * w.groups + first) * a.part_rows;
+      const Mass* mass = w.mass + ((unit * a.row_tiles + rt) * w.groups + first) * a.part_rows;
       const int rows = min(a.group - rt * kRows, kRows);
-      const float* lse = a.lse + (int64_t)b * a.q_heads + head * a.group + rt * kRows;
-      // Both loads at once, four of each a trip.  A sum of -inf is one of no terms, or of a row that has none; none is more than
-      // its row's, whatever the rounding of far scores says.
+      const Mass* row = w.rows + (int64_t)b * a.q_heads + head * a.group + rt * kRows;
+      // Both loads at once, four of each a trip.  A sum of 0 is one of no terms, or of a row that has none, but under a reference of
+      // infinity, whose row is NaN.
       for (int e0 = lane; e0 < n * a.part_rows; e0 += 4 * LANES) {
-        float m[4], l[4];
+        Mass m[4], l[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int e = e0 + i * LANES, r = e % a.part_rows;
           const bool in = e < n * a.part_rows && r < rows;
-          m[i] = in ? mass[e] : kNegInf;
-          l[i] = lse[in ? r : 0];
+          m[i] = in ? mass[e] : Mass{0.0f, 0.0f};
+          l[i] = row[in ? r : 0];
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float x = m[i] - l[i] * (float)kLog2e;
-          sum += m[i] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(x > 0.0f ? 0.0f : x);   // NaN stays NaN
+          const float share = m[i].sum * __builtin_amdgcn_exp2f(m[i].ref - l[i].ref) / l[i].sum;
+          sum += m[i].sum == 0.0f && m[i].ref <= kFltMax ? 0.0f : share;   // NaN stays NaN
         }
       }
     }
@@ -78,7 +81,7 @@ int64_t mass_groups_of(const AttnLaunch& a) {
 size_t rounded(size_t bytes) { return (bytes + 255) & ~(size_t)255; }
 
 size_t mass_bytes(const AttnLaunch& a) {
-  return rounded((size_t)(a.batch * a.cache.heads * row_tiles_of(a)) * (size_t)mass_groups_of(a) * part_rows_of(a) * sizeof(float));
+  return rounded((size_t)(a.batch * a.cache.heads * row_tiles_of(a)) * (size_t)mass_groups_of(a) * part_rows_of(a) * sizeof(Mass));
 }
 
 }  // namespace
@@ -90,21 +93,22 @@ hipError_t launch_attn_heads(const AttnLaunch& a, hipStream_t s) {
 }
 
 size_t attn_weigh_workspace_bytes(const AttnWeighLaunch& a) {
-  return rounded(attn_workspace_bytes(a.attn)) + mass_bytes(a.attn) + (size_t)a.attn.batch * a.attn.q_heads * sizeof(float);
+  return rounded(attn_workspace_bytes(a.attn)) + mass_bytes(a.attn) + (size_t)a.attn.batch * a.attn.q_heads * sizeof(Mass);
 }
 
 hipError_t launch_attn_weigh(const AttnWeighLaunch& a, hipStream_t s) {
   ModeParams<kWeigh> p;
   fill_params(a.attn, p);
   uint8_t* mass = static_cast<uint8_t*>(a.attn.ws) + rounded(attn_workspace_bytes(a.attn));
-  p.mass = reinterpret_cast<float*>(mass);
+  p.mass = reinterpret_cast<Mass*>(mass);
+  p.rows = reinterpret_cast<Mass*>(mass + mass_bytes(a.attn));
   p.groups = mass_groups_of(a.attn);
-  if (!p.lse) p.lse = reinterpret_cast<float*>(mass + mass_bytes(a.attn));
   const hipError_t e = attn_launch(a.attn, p, s);
   if (e != hipSuccess || a.attn.table_width == 0) return e;
   WeighParams w;
   w.attn = p;
   w.mass = p.mass;
+  w.rows = p.rows;
   w.weights = a.weights;
   w.weights_out = a.weights_out;
   w.groups = p.groups;
