@@ -92,8 +92,10 @@ int nvfp4_attn_decode_heads(const nvfp4_attn_args* args /* host */, void* stream
  *   weights_out[b][h][i] = decay * weights[b][h][i] + sum exp(s_j - lse)
  * over the query heads of kv head h and the tokens j of page i that they attend to, for all i < table_width: a page's
  * share of what its readers looked at, each query head adding up to 1.  Terms and sums are fp32, as
- * the attention's are, and s_j - lse is off by up to 2^-21 (|s_j| + |lse| + 1), never above 0; a query head whose lse is -inf adds nothing, one whose lse is NaN makes the pages NaN that it
- * attends to, but for those whose terms are all 0.  decay 0: weights is not read and may be NULL.  weights_out may
+ * the attention's are.  A score, d products summed in fp32, is off by up to e_j = (d + 4) 2^-24 scale sum |q_c k_jc|, so that a
+ * share is off by up to e_j + max e of itself; beyond that, whatever the scores' size, by (n + 64 + page_size / 16) 2^-24 of
+ * its query head's 1 (n: the tokens that it attends to).  A query head whose lse is -inf adds nothing, one whose lse is NaN makes
+ * the pages NaN that it attends to, but for those whose terms are all 0.  decay 0: weights is not read and may be NULL.  weights_out may
  * be weights.  q_heads, batch and table as in nvfp4_attn_decode(), and batch * kv_heads * table_width at most 2^31. */
 typedef struct nvfp4_attn_weigh_args {
   nvfp4_attn_args attn;

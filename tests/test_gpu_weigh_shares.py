@@ -74,3 +74,31 @@ def test_shares_of_a_row_in_many_parts():
     _, _, w = B.attn_weigh(*x.args(), None, 0.0, w, scale=64.0, lse=True)
     w = w[0].cpu().numpy()
     assert (w[:, :-1] == 0).all() and np.abs(w[:, -1] - 1).max() <= off(n, page)
+
+
+@pytest.mark.parametrize("fmt", G.FORMATS, ids=G.IDS)
+@pytest.mark.parametrize("d", [128, 256])
+def test_products_that_cancel(fmt, d):
+    """Scores that are small sums of large products: a score is off by up to e = (d + 4) u scale sum |q k|, however small it is, a
+    share p_j by p_j (exp(e_j + max e) - 1) from its own and the others' scores, and beyond that by off()."""
+    n, page, scale = 50, 16, 0.5
+    x = Weighed(fmt, [n], 3, 1, d, page, seed=d)
+    rng = np.random.default_rng(d)
+    # Channels c and c + d / 8 of each quarter have the same query and opposite keys, but where the query is small.
+    pair = lambda a, sign: np.concatenate((a, sign * a), -1).reshape(*a.shape[:-2], d)  # noqa: E731
+    k = pair(rng.uniform(0.5, 4, size=(n, 1, 4, d // 8)), -1)
+    q = pair(2.0 ** rng.uniform(-6, 6, size=(3, 4, d // 8)), 1)
+    q = np.where((q < 0.25) & (np.arange(d) % (d // 4) < d // 8), 0, q)
+    x.pool.write(x.pool.slots(x.table[0], n)[0], torch.from_numpy(k.astype(np.float32)).to(torch.bfloat16), torch.ones(n, 1, d, dtype=torch.bfloat16))
+    x.q[0] = torch.from_numpy(q).to(torch.bfloat16)
+    w = torch.empty(x.w.shape, device=x.dev)
+    _, lse, w = B.attn_weigh(*x.args(), None, 0.0, w, scale=scale, lse=True)
+    k, q = x.pool.k[x.pool.slots(x.table[0], n)[0], 0], x.q[0].double().numpy()
+    s, size = scale * q @ k.T, scale * np.abs(q) @ np.abs(k).T
+    assert np.abs(s).max() < 20 and size.min() > 200      # (products do cancel)
+    p = np.exp(s - s.max(1, keepdims=True))
+    p /= p.sum(1, keepdims=True)
+    e = (d + 4) * R.U24 * size
+    want, bound = (np.add.reduceat(a.sum(0), np.arange(0, n, page)) for a in (p, p * np.expm1(e + e.max(1, keepdims=True))))
+    err = np.abs(w[0, 0].double().cpu().numpy() - want)
+    assert (err <= bound + 3 * off(n, page)).all(), (err / bound).max()
