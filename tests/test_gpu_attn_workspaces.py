@@ -81,3 +81,26 @@ def test_eviction_leaves_a_workspace_as_others_need_it(batch):
         assert all(torch.equal(x, y) for x, y in zip(got, ref)), longest
         assert not ws[:B.NVFP4_SELECT_COUNTER_BYTES].any(), longest
         assert all(torch.equal(x, y) for x, y in zip((*attend(ws=ws), *select(ws=ws)), want)), longest
+
+
+def test_selections_prepared_under_capture_clear_all_their_counters():
+    """More than 256 and fewer than 1024 (sequence, kv head)s, tables cut over workgroups: counters past the first kilobyte.
+    Whatever the workspace holds when a call comes that was prepared inside a capture, and before that graph ever ran."""
+    pool, q, table, lens, bounds = many_pairs(B.NVFP4_KV_E4M3, seed=5)
+    make = lambda: B.kv_select_prepared(q, pool.cache, bounds, table, lens, 9)  # noqa: E731
+    want = [t.clone() for t in make()()]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call = make()
+        out = call()
+    torch.cuda.synchronize()
+    ws = next(t for t in reversed(call.keep) if isinstance(t, torch.Tensor) and t.dtype == torch.uint8)
+    for step, run in enumerate((call, call, graph.replay, call, graph.replay)):
+        for t in out:
+            t.fill_(7)
+        ws[:B.NVFP4_SELECT_COUNTER_BYTES] = 255
+        run()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want)), step
+        assert not ws[:B.NVFP4_SELECT_COUNTER_BYTES].any(), step
