@@ -11,8 +11,9 @@
 // at 1000, up to a factor of 2 at 2^20.)  Sums of sixteen tokens are 8 bytes a row, for 16 * 2 * head_dim values of the cache;
 // the second launch finds them in the L2 and the last-level cache.
 //
-// Bound as attn_kernel is; what weighing adds is its 5 us and up to 3 us of the pass: 32 users of up to 8192 NVFP4 tokens 38 us
-// (152 MB, 4.0 TB/s), the attention alone 35; one of 65,536 E4M3 tokens 34 us (135 MB, 4.0 TB/s), the attention alone 29.
+// Bound as attn_kernel is; what weighing adds is its 5 us and up to 5 us of the pass, for which it writes 8 bytes a row and sixteen
+// tokens: 32 users of up to 8192 NVFP4 tokens 43 us for both launches (152 MB, 3.5 TB/s), the attention alone 35; one of 65,536 E4M3
+// tokens 34 us (135 MB, 4.0 TB/s), the attention alone 29.
 #include "attn_kernel.h"
 
 namespace nvfp4 {
@@ -113,9 +114,10 @@ hipError_t launch_attn_weigh(const AttnWeighLaunch& a, hipStream_t s) {
   w.weights_out = a.weights_out;
   w.groups = p.groups;
   w.decay = a.decay;
-  // Lanes a page: sixteen where they find fewer than eight sums each, a wavefront from there on.  (One user of 131,072
-  // tokens, five rows a kv head: pages of 16 42 us against 56, of 64 39 against 42, of 256 40 against 39; 32 users of 4096, sixteen
-  // rows: pages of 128 38.5 against 37.1.)
+  // Lanes a page: sixteen where they find fewer than eight sums each, a wavefront from there on.  (Both launches, sixteen lanes
+  // against a wavefront.  One user of 131,072 NVFP4 tokens, five rows a kv head: pages of 16 45 us against 64, of 64 40 against 45, of
+  // 512 42 against 41, of 1024 41.4 against 39.1; sixteen rows: of 256 47 against 46, of 1024 54.6 against 45.8, of 4096 86 against
+  // 53.  32 users of 4096, sixteen rows: of 64 37.7 against 42.2, of 128 37.6 against 38.6, of 256 38.5 against 37.7.)
   const int64_t pages = a.attn.batch * a.attn.cache.heads * a.attn.table_width;
   if (a.attn.cache.gpp * p.part_rows < 128)
     hipLaunchKernelGGL((weigh_kernel<16>), grid_of((pages + 15) / 16), dim3(256), 0, s, w);

@@ -403,8 +403,9 @@ __global__ __launch_bounds__(256) void join_kernel(const JoinParams a) {
 
 template <int DP>
 void join_launch(const JoinParams& p, hipStream_t s) {
-  // A wavefront a row where its pieces are few, a workgroup where there are more than it reads at once.  (200 users of 40 heads,
-  // a piece or two a row: 96 us against 102; 16 users of 8 heads, 64 pieces: 27 us against 35.)
+  // A wavefront a row where its pieces are few, a workgroup where there are more than it reads at once.  (200 users of 40 heads
+  // under 8192 bf16 tokens, a piece or two a row: 83 us against 92, 64-wide 56 against 63; 16 users of 8 heads under 32,768, 32 pieces: 45 us
+  // against 40; 7 users of 256-wide heads under 50,001 E4M3 tokens, 64 pieces: 58 against 40.)
   const int64_t rows = (int64_t)p.batch * p.q_heads, pieces = p.prefix.grid / p.prefix.units + 1;
   if (pieces <= 8 * (256 / DP)) hipLaunchKernelGGL((join_kernel<DP, 64>), grid_of((rows + 3) / 4), dim3(256), 0, s, p);
   else hipLaunchKernelGGL((join_kernel<DP, 256>), grid_of(rows), dim3(256), 0, s, p);
@@ -450,9 +451,13 @@ AttnLaunch behind_of(const AttnSharedLaunch& a) {
   return l;
 }
 // Whether each sequence reads the prefix by itself (kBehind), in one launch instead of three: where a prefix that fills its table
-// is so few bytes, most of which come from caches, or nothing would be shared.  (32 users of 40 heads, NVFP4: under 500 tokens 11.2 us
-// against 20.6, 2000 (66 MB) 18.4 against 23.2, 4000 (131 MB) 26.6 against 24.9; 16 users, bf16: 1000 13.0 against 19.3, 2000
-// (131 MB) 18.8 against 20.9, 4000 22.8 against 22.9; one user of 16 heads under 30,000 E4M3 tokens 17.4 against 22.0.)
+// is so few bytes, most of which come from caches, or nothing would be shared.  The host knows the table's size and not the
+// prefix's, so that a short prefix in a large table takes three launches.
+// (One against three, 40 heads.  NVFP4, 32 users: under 500 tokens 9.7 us against 19.1, 2000 (66 MB) 17.3 against 22.0, 3000 (98 MB)
+// 21.8 against 23.0, 4000 (131 MB) 25.9 against 23.8.  The limit is where these cross.  The wider formats cross later: E4M3, 32 users,
+// 2000 tokens (131 MB) 17.2 against 21.2, 3000 21.6 against 22.0, 4000 25.5 against 23.5; bf16, 16 users, 2000 (131 MB) 18.1 against
+// 20.1, 4000 (262 MB) 21.5 against 22.5, 6000 28.8 against 23.6, 32 users 1000 (131 MB) 12.0 against 19.4, 2000 (262 MB) 15.9
+// against 21.3.  One user of 16 heads under 30,000 E4M3 tokens 17.4 against 22.0.)
 constexpr int64_t kApartBytes = int64_t(96) << 20;
 bool apart(const AttnSharedLaunch& a) {
   const int64_t row_tiles = row_tiles_of(a.attn), block = kRows * block_tiles_of(a);

@@ -17,7 +17,10 @@
 // What bounds them is latency where little is to be done: one user's choice of 64 pages out of 2048 for each of 8 kv
 // heads (8.4 MB of bounds) takes 15 us, of which the launch 3, the scores 4, the way to the last workgroup of a pair 4 and
 // choosing 4; 256 pages of 32 users are evicted in 8 us, 8192 of one in 35 (keys 9, choosing 11, places and outputs 11).
-// Many scores are bound by fp64 arithmetic: 32 users of up to 512 pages and 8 kv heads of five rows 22 us, 150 of 500 pages 77 us.
+// So are 32 users of up to 512 pages and 8 kv heads of five rows, 20.5 us for 35 MB of bounds: the vector units issue in 24 % of the
+// cycles, and wavefronts wait in 51 %.  Where scores are many, their rows count: 150 users of 500 pages (307 MB, most of it from the
+// caches) take 47 us for one row a kv head (6.5 TB/s), 77 for five and 190 for sixteen, the vector units issuing in 50, 60 and 69 %
+// of the cycles.
 #include <algorithm>
 #include <type_traits>
 
@@ -626,8 +629,9 @@ __global__ __launch_bounds__(THREADS) void evict_kernel(const EvictParams p) {
 }
 
 // Pages of a workgroup's share: one workgroup a (sequence, kv head) where those fill the GPU or have no counter; else
-// so that there are four a CU, but 64 pages at least.  (32 users of 8 kv heads: two a CU 53 us for 1000 pages against 46, 31 for 500
-// against 28.  One user: shares of 32 pages and more 18 us for 2048 pages against 15.5, of 128 17.8.)
+// so that there are four a CU, but 64 pages at least.  (32 users of 8 kv heads: two a CU 45 us for 1000 pages against 42.6, 25.8 for 500
+// against 25.3.  One user: shares of 32 pages and more 23.4 us for 2048 pages against 20.7, of 128 22.3; for 500 10.2 and 12.5 against
+// 9.7.)
 int64_t chunk_of(const KvSelectLaunch& a) {
   const int64_t pairs = a.batch * a.heads;
   if (pairs >= kCounters) return a.table_width;
@@ -643,7 +647,7 @@ void select_launch_per(const SelectParams& p, bool cut, dim3 grid, hipStream_t s
 }
 template <int DB>
 void select_launch(const SelectParams& p, bool cut, dim3 grid, hipStream_t s) {
-  // (One user of 1000 pages 14.6 us against 18.9, 150 users 180 against 192.)
+  // (One user of 1000 pages 14.1 us against 18.5, 32 users of 500 25.4 against 30.1, 150 of 500 77.6 against 84.7.)
   if (p.a.table_width <= kThreads * kSelectFew) select_launch_per<DB, kSelectFew>(p, cut, grid, s);
   else select_launch_per<DB, kSelectMany>(p, cut, grid, s);
 }

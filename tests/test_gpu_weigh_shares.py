@@ -2,10 +2,11 @@
 
 A row's share of a page is sum p_j / l over terms p_j = 2^(s_j - r): whatever the scores' own rounding is, terms enter the
 page's sum and l alike, so that the shares of a row add up to 1.  What is left are roundings of positive numbers, each at most
-u = 2^-24 of what it rounds: up to n additions into l (n: the row's tokens), sixteen into a sixteen's sum and one for each
+u = 2^-24 of what it rounds: up to n additions into l and moves of its reference (n: the row's tokens; in a lane, eight
+additions and one move of four steps at most for 32 of them), sixteen into a sixteen's sum and one for each
 sixteen of the page; up to eight steps for each of the two exponentials by which a term's stretch reaches its row's reference
-(an exponent d is off by u |d|, which moves 2^-|d| by less than u of the row), and the quotient.  So (n + 64) u of
-a row, and as much again where a page has more than 48 sixteens."""
+(an exponent d is off by u |d|, which moves 2^-|d| by less than u of the row), and the quotient.  So
+(n + 64 + page / 16) u of a row."""
 import numpy as np
 import pytest
 import torch
